@@ -10,6 +10,8 @@
  *                        gated residual;
  *   dart_decode_step     one new token per sequence against the cache of
  *                        chunk memories and the recurrent state.
+ * For serving from a pool of pages, with several new tokens per sequence, see
+ * dart_ssd_extend, dart_sma_paged and dart_cache_write_paged.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -377,6 +379,122 @@ dart_status dart_decode_step_noalloc(const dart_dims* dims, dart_dtype dtype,
                                      void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Paged memory cache: several new tokens per sequence in one pass
+ * ---------------------------------------------------------------------------
+ * The calls below serve a ragged batch whose chunk memories live in pages of a
+ * pool that all sequences share, instead of one [cmax] stretch per sequence.
+ *
+ * Pages.  A page holds page_size memories of every head.  Memory m of sequence
+ * b is slot m % page_size of page table[b, m / page_size].  Two sequences may
+ * name the same page to read it; a page that dart_cache_write_paged or
+ * dart_ssd_extend writes belongs to one sequence.  Entries past a sequence's
+ * memories are not read.
+ *   DART_CACHE_DTYPE  pages dtype [npages,H,page_size,N,P]; scales NULL.
+ *   DART_CACHE_MXFP4  pages uint8 [npages,H,page_size,P,N/2] and scales uint8
+ *     [npages,H,page_size,P,N/32]: 4-bit E2M1 codes (sign, then 0 0.5 1 1.5 2 3
+ *     4 6), two to a byte, the lower nibble first; the 32 values
+ *     V[32k..32k+31, p] of a memory are their codes times 2^(scales[p,k] - 127).
+ *     The code of V[16i+4q+j, p] stands at place q N/4 + 4i + j of row p.  A
+ *     quantized block has the least power of two with max|V| <= 6 * scale,
+ *     within 2^-126..2^126, codes rounded to nearest, ties to even; a block
+ *     that holds an infinity or a NaN gets the scale byte 255 and reads as NaN.
+ *
+ * Tokens.  dims->batch sequences own rows cu_tokens[b] .. cu_tokens[b+1]-1 of
+ * the packed token tensors (x[T,H,P] and so on), dims->seqlen = T rows in all;
+ * cu_tokens is int32 [batch+1] on the device.  Sequences may own no row, and
+ * rows that none owns are left as they are.
+ *
+ * int32 vectors (the table and cu_tokens, first, count, mem_count, n_chunks and
+ * pos) need 4-byte alignment only, so that a sequence's row of a table can be
+ * passed by itself; all other tensors 16 bytes, as everywhere.
+ *
+ * Errors the device finds (a range, counter, count or page that is out of
+ * bounds) are latched as DART_ERR_DEVICE; the sequence, or the row, that they
+ * concern is left as it is and the others are computed.
+ *
+ * Compiled for (N, P) = (128, 64), (64, 64) and, in DART_CACHE_DTYPE, (16, 16);
+ * any chunk S >= 1.  At most 2^19 memories per sequence.
+ */
+typedef enum { DART_CACHE_DTYPE = 0, DART_CACHE_MXFP4 = 1 } dart_cache_format;
+
+typedef struct {
+    dart_cache_format format;
+    int npages;              /* pages in the pool */
+    int page_size;           /* memories per page */
+    int table_width;         /* entries of a sequence's row of the table */
+    void* pages;
+    unsigned char* scales;   /* MXFP4 only */
+    const int* table;        /* int32 [batch, table_width], device */
+} dart_paged_cache;
+
+/*
+ * Memories into pages (the handoff from dart_ssd_chunk_scan, or a finished
+ * dH_cur): memory first[b] + i of sequence b = dH[b, :, i] for i < count[b],
+ * copied or quantized as the cache's format says.
+ *   dH: dtype [B,H,nmem,N,P]; first, count: int32 [B] on the device, 0 <=
+ *   count[b] <= nmem.  Uses batch, nheads, headdim, dstate of dims (seqlen and
+ *   chunk are ignored, chunk >= 1).  One kernel.
+ */
+dart_status dart_cache_write_paged(const dart_dims* dims, dart_dtype dtype, const void* dH, int nmem,
+                                   const int* first, const int* count, const dart_paged_cache* cache,
+                                   void* stream);
+
+/*
+ * The reverse: dH[b, :, i] = memory first[b] + i of sequence b for i < count[b],
+ * widened from codes and rounded to dtype; other entries of dH are left as they
+ * are.  A DART_CACHE_DTYPE cache is of the same dtype.  One kernel.
+ */
+dart_status dart_cache_read_paged(const dart_dims* dims, dart_dtype dtype, const dart_paged_cache* cache,
+                                  const int* first, const int* count, void* dH, int nmem, void* stream);
+
+/*
+ * A run of new tokens per sequence through the recurrence, from the middle of a
+ * chunk on: dart_decode_step's update for every token of the run, in order,
+ *   H = exp(dt A) H + dt B x^T,  D = exp(dt A) D + dt B x^T,  y = H^T C,
+ * and at the last token of a chunk D becomes the sequence's next memory (in the
+ * cache's format) and restarts at 0.
+ *   x[T,H,P], Bm[T,G,N], Cm[T,G,N]: dtype; dt[T,H], A[H]: float.
+ *   state, dH_cur: float [B,H,N,P], H and D before the run; state_out,
+ *   dH_cur_out: after it.  The same pointers update in place; others must not
+ *   overlap the inputs, which then keep the state a caller can go back to when
+ *   some of the tokens (drafts) turn out not to be wanted.
+ *   n_chunks, pos: int32 [B], memories finished and tokens into the chunk, before
+ *   the run; n_chunks_out, pos_out: after it, in memory of their own.
+ *   y: float [T,H,P].  mem_count: int32 [T], the number of memories each token may
+ *   attend to (those finished before it), -1 for the tokens of a sequence that
+ *   was left as it is; dart_sma_paged's argument of that name.
+ * A token sees a finished chunk only through its memory, so the pages must have
+ * room for n_chunks + (pos + tokens) / S memories.  One kernel.
+ */
+dart_status dart_ssd_extend(const dart_dims* dims, dart_dtype dtype, const void* x, const float* dt,
+                            const float* A, const void* Bm, const void* Cm, const int* cu_tokens,
+                            const float* state, float* state_out, const float* dH_cur, float* dH_cur_out,
+                            const dart_paged_cache* cache, const int* n_chunks, const int* pos,
+                            int* n_chunks_out, int* pos_out, float* y, int* mem_count, void* stream);
+
+/* Workspace for dart_sma_paged, in bytes: partial results of the items that
+ * several blocks share.  Depends on headdim alone. */
+size_t dart_sma_paged_workspace_bytes(const dart_dims* dims);
+
+/*
+ * State-memory attention of the packed tokens over their sequences' paged
+ * memories (dart_sma_forward's attention): token t of sequence b sees the
+ * sequence's first mem_count[t] memories,
+ *   out = y_ssd + g * o  (y_ssd != NULL), else out = o;  o = 0 with none to see.
+ *   Q[T,H,N], E[T,H,P], Cm[T,G,N]: dtype; y_ssd: nullable float [T,H,P]; out:
+ *   float [T,H,P], y_ssd itself or not overlapping it.
+ *   mem_count: int32 [T]; -1 marks a row that is left as it is.
+ *   workspace: dart_sma_paged_workspace_bytes(), 16-byte aligned, contents on
+ *   entry do not matter; calls that may overlap on the GPU need one each.
+ * Limits: batch + T / 8 <= 4096.  Deterministic.  Two kernels.
+ */
+dart_status dart_sma_paged(const dart_dims* dims, dart_dtype dtype, const void* Q, const void* E,
+                           const void* Cm, const int* cu_tokens, const dart_paged_cache* cache,
+                           const int* mem_count, float g, const float* y_ssd, float* out, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
  * 1 when (dstate N, headdim P, chunk S, dtype) is compiled in, else 0.
  */
 int dart_supported(int dstate, int headdim, int chunk, dart_dtype dtype);
@@ -409,9 +527,10 @@ dart_status dart_selftest_wait_timeout(unsigned int limit_us, void* stream);
 /* Message describing the last failure on the calling host thread ("" if none). */
 const char* dart_last_error(void);
 
-/* ABI version, bumped on any signature change or addition (2: the decayed-memory,
+/* ABI version, bumped when an existing call changes (2: the decayed-memory,
  * E4M3-cache and backward entry points; 3: dCm_add of the scan backward and
- * ngroups; 4: dart_selftest_wait_timeout). */
+ * ngroups; 4: dart_selftest_wait_timeout).  The paged-cache calls were added to
+ * version 4: they change none of its calls. */
 int dart_abi_version(void);
 
 /*

@@ -7,6 +7,7 @@
 #include <string.h>
 
 #include "dart_backward.cuh"
+#include "dart_paged.cuh"
 
 namespace dart {
 // [0]: status flags; [1]: (kernel id << 8 | wait site) of the first bounded
@@ -70,6 +71,14 @@ size_t scan_asum_bytes(size_t bhc) { return (bhc * sizeof(float) + 255) & ~size_
             return fail(DART_ERR_INVALID_ARG, "%s: not 16-byte aligned", #p);         \
     } while (0)
 
+// int32 vectors (tables, ranges, counters) may be slices: their own alignment is enough
+#define DART_REQUIRE_INTS(p)                                                          \
+    do {                                                                              \
+        if (!(p)) return fail(DART_ERR_INVALID_ARG, "%s: null pointer", #p);          \
+        if (reinterpret_cast<uintptr_t>(p) & 3u)                                      \
+            return fail(DART_ERR_INVALID_ARG, "%s: not 4-byte aligned", #p);          \
+    } while (0)
+
 dart_status check_common(const dart_dims* d, dart_dtype dt, bool need_seqlen) {
     if (!d) return fail(DART_ERR_INVALID_ARG, "dims: null pointer");
     if (dt != DART_F32 && dt != DART_BF16) return fail(DART_ERR_INVALID_ARG, "dtype: unknown value %d", (int)dt);
@@ -82,6 +91,28 @@ dart_status check_common(const dart_dims* d, dart_dtype dt, bool need_seqlen) {
     }
     if (d->batch > 65535 || d->nheads > 65535)
         return fail(DART_ERR_UNSUPPORTED, "batch and nheads must be <= 65535");
+    return DART_OK;
+}
+
+// The paged cache's own fields, and the memory shape it is asked to hold.
+dart_status check_paged(const char* call, const dart_dims* d, const dart_paged_cache* c, dart::PagedCache* out) {
+    if (!c) return fail(DART_ERR_INVALID_ARG, "%s: cache: null pointer", call);
+    if (c->format != DART_CACHE_DTYPE && c->format != DART_CACHE_MXFP4)
+        return fail(DART_ERR_INVALID_ARG, "%s: cache format: unknown value %d", call, (int)c->format);
+    const int mxfp4 = c->format == DART_CACHE_MXFP4;
+    if (!dart::paged_supported(d->dstate, d->headdim, mxfp4))
+        return fail(DART_ERR_UNSUPPORTED, "%s: (N=%d, P=%d) not compiled for this cache format", call, d->dstate,
+                    d->headdim);
+    if (c->npages < 1 || c->page_size < 1 || c->table_width < 1)
+        return fail(DART_ERR_INVALID_ARG, "%s: npages, page_size and table_width must be >= 1", call);
+    if ((long long)c->page_size * c->table_width > dart::kPagedMaxMemories ||
+        (long long)c->npages * c->page_size * d->nheads > 0x7fffffffLL)
+        return fail(DART_ERR_UNSUPPORTED, "%s: at most %lld memories a sequence and 2^31 - 1 in the pool", call,
+                    dart::kPagedMaxMemories);
+    const void *pages = c->pages, *table = c->table, *scales = c->scales;
+    DART_REQUIRE_PTR(pages); DART_REQUIRE_INTS(table);
+    if (mxfp4) DART_REQUIRE_PTR(scales);
+    *out = dart::PagedCache{mxfp4, c->npages, c->page_size, c->table_width, c->pages, c->scales, c->table};
     return DART_OK;
 }
 
@@ -446,6 +477,113 @@ dart_status dart_decode_step_noalloc(const dart_dims* d, dart_dtype dtype, const
     return DART_OK;
 }
 
+static dart_status cache_copy(const char* call, bool write, const dart_dims* d, dart_dtype dtype, void* dH, int nmem,
+                              const int* first, const int* count, const dart_paged_cache* cache, void* stream) {
+    t_err[0] = 0;
+    dart_status st = check_common(d, dtype, false);
+    if (st != DART_OK) return st;
+    dart::CacheCopyArgs a{};
+    if ((st = check_paged(call, d, cache, &a.cache)) != DART_OK) return st;
+    if (nmem < 1) return fail(DART_ERR_INVALID_ARG, "%s: nmem = %d: must be >= 1", call, nmem);
+    DART_REQUIRE_PTR(dH); DART_REQUIRE_INTS(first); DART_REQUIRE_INTS(count);
+    a.B = d->batch; a.C = nmem; a.H = d->nheads; a.P = d->headdim; a.N = d->dstate;
+    a.dH = dH; a.first = first; a.count = count; a.status = status_word();
+    if (!a.status) return fail(DART_ERR_CUDA, "%s: no device status word", call);
+    cudaError_t e = write ? dart::launch_cache_write(a, dtype, static_cast<cudaStream_t>(stream))
+                          : dart::launch_cache_read(a, dtype, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, call);
+    return DART_OK;
+}
+
+dart_status dart_cache_write_paged(const dart_dims* d, dart_dtype dtype, const void* dH, int nmem, const int* first,
+                                   const int* count, const dart_paged_cache* cache, void* stream) {
+    return cache_copy("dart_cache_write_paged", true, d, dtype, const_cast<void*>(dH), nmem, first, count, cache, stream);
+}
+
+dart_status dart_cache_read_paged(const dart_dims* d, dart_dtype dtype, const dart_paged_cache* cache, const int* first,
+                                  const int* count, void* dH, int nmem, void* stream) {
+    return cache_copy("dart_cache_read_paged", false, d, dtype, dH, nmem, first, count, cache, stream);
+}
+
+dart_status dart_ssd_extend(const dart_dims* d, dart_dtype dtype, const void* x, const float* dt, const float* A,
+                            const void* Bm, const void* Cm, const int* cu_tokens, const float* state, float* state_out,
+                            const float* dH_cur, float* dH_cur_out, const dart_paged_cache* cache, const int* n_chunks,
+                            const int* pos, int* n_chunks_out, int* pos_out, float* y, int* mem_count, void* stream) {
+    t_err[0] = 0;
+    dart_status st = check_common(d, dtype, false);
+    if (st != DART_OK) return st;
+    dart::ExtendArgs a{};
+    if ((st = check_paged("dart_ssd_extend", d, cache, &a.cache)) != DART_OK) return st;
+    if (d->seqlen < 0) return fail(DART_ERR_INVALID_ARG, "dart_ssd_extend: seqlen (packed token rows) must be >= 0");
+    if (d->seqlen > 0) {
+        DART_REQUIRE_PTR(x); DART_REQUIRE_PTR(dt); DART_REQUIRE_PTR(Bm); DART_REQUIRE_PTR(Cm);
+        DART_REQUIRE_PTR(y); DART_REQUIRE_INTS(mem_count);
+    }
+    DART_REQUIRE_PTR(A); DART_REQUIRE_INTS(cu_tokens); DART_REQUIRE_PTR(state); DART_REQUIRE_PTR(state_out);
+    DART_REQUIRE_PTR(dH_cur); DART_REQUIRE_PTR(dH_cur_out); DART_REQUIRE_INTS(n_chunks); DART_REQUIRE_INTS(pos);
+    DART_REQUIRE_INTS(n_chunks_out); DART_REQUIRE_INTS(pos_out);
+    // The blocks of a sequence read its counters at their own time: the new ones go elsewhere.
+    const int* in[2] = {n_chunks, pos};
+    const int* out[2] = {n_chunks_out, pos_out};
+    for (const int* i : in)
+        for (const int* o : out)
+            if (i < o + d->batch && o < i + d->batch)
+                return fail(DART_ERR_INVALID_ARG, "dart_ssd_extend: n_chunks_out and pos_out overlap n_chunks or pos");
+    const size_t floats = (size_t)d->batch * d->nheads * d->dstate * d->headdim;
+    const float* from[2] = {state, dH_cur};
+    const float* to[2] = {state_out, dH_cur_out};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j)
+            if ((i != j || from[i] != to[j]) && from[i] < to[j] + floats && to[j] < from[i] + floats)
+                return fail(DART_ERR_INVALID_ARG,
+                            "dart_ssd_extend: state_out and dH_cur_out are their inputs or apart from both");
+    a.B = d->batch; a.T = d->seqlen; a.H = d->nheads; a.P = d->headdim; a.N = d->dstate; a.S = d->chunk; a.G = d->ngroups;
+    a.x = x; a.dt = dt; a.A = A; a.Bm = Bm; a.Cm = Cm; a.cu = cu_tokens;
+    a.state = state; a.state_out = state_out; a.cur = dH_cur; a.cur_out = dH_cur_out;
+    a.nchunks = n_chunks; a.pos = pos; a.nchunks_out = n_chunks_out; a.pos_out = pos_out;
+    a.y = y; a.mem_count = mem_count; a.status = status_word();
+    if (!a.status) return fail(DART_ERR_CUDA, "dart_ssd_extend: no device status word");
+    cudaError_t e = dart::launch_ssd_extend(a, dtype, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "dart_ssd_extend launch");
+    return DART_OK;
+}
+
+size_t dart_sma_paged_workspace_bytes(const dart_dims* d) {
+    return d && d->headdim > 0 ? dart::sma_paged_workspace_bytes(d->headdim) : 0;
+}
+
+dart_status dart_sma_paged(const dart_dims* d, dart_dtype dtype, const void* Q, const void* E, const void* Cm,
+                           const int* cu_tokens, const dart_paged_cache* cache, const int* mem_count, float g,
+                           const float* y_ssd, float* out, void* workspace, size_t workspace_bytes, void* stream) {
+    t_err[0] = 0;
+    dart_status st = check_common(d, dtype, false);
+    if (st != DART_OK) return st;
+    dart::SmaPagedArgs a{};
+    if ((st = check_paged("dart_sma_paged", d, cache, &a.cache)) != DART_OK) return st;
+    if (d->seqlen < 0) return fail(DART_ERR_INVALID_ARG, "dart_sma_paged: seqlen (packed token rows) must be >= 0");
+    if (d->seqlen == 0) return DART_OK;
+    DART_REQUIRE_PTR(Q); DART_REQUIRE_PTR(E); DART_REQUIRE_PTR(Cm); DART_REQUIRE_INTS(cu_tokens);
+    DART_REQUIRE_INTS(mem_count); DART_OPTIONAL_PTR(y_ssd); DART_REQUIRE_PTR(out); DART_REQUIRE_PTR(workspace);
+    if (y_ssd && y_ssd != out) {
+        const size_t floats = (size_t)d->seqlen * d->nheads * d->headdim;
+        if (y_ssd < out + floats && out < y_ssd + floats)
+            return fail(DART_ERR_INVALID_ARG, "dart_sma_paged: out overlaps y_ssd without being the same pointer");
+    }
+    if (dart::sma_paged_tiles(d->batch, d->seqlen) > dart::sma_paged_max_tiles())
+        return fail(DART_ERR_UNSUPPORTED, "dart_sma_paged: %d sequences and %d tokens are too many for one call "
+                    "(batch + seqlen / 8 must be <= %lld)", d->batch, d->seqlen, dart::sma_paged_max_tiles());
+    const size_t need = dart_sma_paged_workspace_bytes(d);
+    if (workspace_bytes < need)
+        return fail(DART_ERR_INVALID_ARG, "workspace: %zu bytes, need %zu", workspace_bytes, need);
+    a.B = d->batch; a.T = d->seqlen; a.H = d->nheads; a.P = d->headdim; a.N = d->dstate; a.G = d->ngroups;
+    a.Q = Q; a.E = E; a.Cm = Cm; a.cu = cu_tokens; a.mem_count = mem_count; a.g = g; a.y_ssd = y_ssd; a.out = out;
+    a.part = static_cast<float*>(workspace); a.status = status_word();
+    if (!a.status) return fail(DART_ERR_CUDA, "dart_sma_paged: no device status word");
+    cudaError_t e = dart::launch_sma_paged(a, dtype, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "dart_sma_paged launch");
+    return DART_OK;
+}
+
 dart_status dart_selftest_wait_timeout(unsigned int limit_us, void* stream) {
     t_err[0] = 0;
     if (limit_us < 1 || limit_us > 2000000)
@@ -474,7 +612,7 @@ dart_status dart_sync_status(void* stream) {
         return fail(DART_ERR_TIMEOUT, "a bounded device wait gave up (kernel %d, wait site %d)", words[1] >> 8,
                     words[1] & 0xff);
     if (words[0] & dart::kStatusDevice)
-        return fail(DART_ERR_DEVICE, "device flagged bad state (decode counters out of range or cache full)");
+        return fail(DART_ERR_DEVICE, "device flagged bad state (decode or paged-cache counters, ranges or pages out of range, or cache full)");
     return DART_OK;
 }
 

@@ -1,0 +1,295 @@
+// sma_paged.cu -- state-memory attention of packed new tokens over paged chunk
+// memories, on CUDA cores.
+//
+// Per token t, head h and visible memory M_c (N x P):
+//   u = Q_t^T M_c,  v = C_t^T M_c,  s = u . E_t / sqrt(N),
+//   o = sum_c softmax_c(s) v_c,  out = y_ssd + g o        (o = 0 with none visible).
+//
+// A warp takes a memory at a time, a lane two of its columns: it streams the
+// rows past up to 8 tokens held as pairs, so a value is loaded once for
+// 2 x 8 products.  Scores are summed over the warp, the softmax runs online in
+// base 2, and v is folded into the lane's own columns, so that the eight warps
+// of a block meet only at the end of a piece.
+#include "sma_paged.cuh"
+
+namespace dart {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTT = 8;        // tokens of a tile
+constexpr int kCap = 4096;    // tiles of a call
+constexpr int kLeast = 8;     // units below which a run is not cut
+
+template <int N, int P>
+struct Smem {
+    TileList<kCap> tiles;
+    float qc[N][2 * kTT];              // Q (times log2(e) / sqrt(N)) and C of the tile's tokens
+    float m[kWarps][kTT], l[kWarps][kTT];
+    float o[kWarps][kTT][P];
+    int count[kTT], bad;
+};
+
+// Rows of a memory as (n, two columns) for this lane, eight at a time.
+template <typename T, int N, int P>
+struct Rows {
+    static constexpr int LPR = P / 2, RPW = 32 / LPR;      // lanes of a row, rows of a warp load
+    static constexpr int STEPS = N / RPW, BATCH = STEPS < 8 ? STEPS : 8;
+    const T* at;
+    __device__ Rows(const PagedCache& c, size_t mem, int lane)
+        : at(static_cast<const T*>(c.pages) + mem * (size_t)(N * P) + (lane / LPR) * P + 2 * (lane % LPR)) {}
+    __device__ __forceinline__ static int row(int step, int lane) { return step * RPW + lane / LPR; }
+    __device__ __forceinline__ void load(int step, float2 (&v)[BATCH]) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const T* p = at + (size_t)(step + i) * RPW * P;
+            if constexpr (sizeof(T) == 4) {
+                v[i] = __ldcs(reinterpret_cast<const float2*>(p));
+            } else {
+                const unsigned w = __ldcs(reinterpret_cast<const unsigned*>(p));
+                v[i] = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+            }
+        }
+    }
+};
+
+struct Fp4 {};
+template <int N, int P>
+struct Rows<Fp4, N, P> {
+    static constexpr int STEPS = N, BATCH = 8, K = N / 32;
+    const uint32_t* codes;
+    const uint8_t* scales;
+    __device__ Rows(const PagedCache& c, size_t mem, int lane)
+        : codes(static_cast<const uint32_t*>(c.pages) + mem * (N * P / 8) + 2 * lane * (N / 8)),
+          scales(c.scales + mem * (N * P / 32) + 2 * lane * K) {}
+    // step = 8 (q K + k) + c is row 32k + 16 (c / 4) + 4q + c % 4
+    __device__ __forceinline__ static int row(int step, int) {
+        const int w = step / 8, c = step % 8;
+        return 32 * (w % K) + 16 * (c / 4) + 4 * (w / K) + c % 4;
+    }
+    __device__ __forceinline__ void load(int step, float2 (&v)[BATCH]) {
+        const int w = step / 8;
+        const uint32_t c0 = codes[w], c1 = codes[N / 8 + w];
+        const float s0 = mxfp4_scale(scales[w % K]), s1 = mxfp4_scale(scales[K + w % K]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            v[c] = make_float2(mxfp4_level(c0 >> (4 * c) & 15u) * s0, mxfp4_level(c1 >> (4 * c) & 15u) * s1);
+    }
+};
+
+// This warp's memories of a piece for the first NT tokens of the tile.
+template <typename T, int N, int P, int NT>
+__device__ __forceinline__ void run_piece(const SmaPagedArgs& a, Smem<N, P>& s, const Walk& w, const int* table, const float2 (&e)[kTT]) {
+    using R = Rows<T, N, P>;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float m[NT], l[NT];
+    float2 o[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) { m[t] = -INFINITY; l[t] = 0.f; o[t] = make_float2(0.f, 0.f); }
+    const int last = min(w.last, s.bad);
+    for (int c = w.first + warp; c < last; c += kWarps) {
+        R rows(a.cache, memory_index(a.cache, a.H, table[c / a.cache.R], w.h, c % a.cache.R), lane);
+        float2 u[NT], v[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) u[t] = v[t] = make_float2(0.f, 0.f);
+        for (int st = 0; st < R::STEPS; st += R::BATCH) {
+            float2 x[R::BATCH];
+            rows.load(st, x);
+#pragma unroll
+            for (int i = 0; i < R::BATCH; ++i) {
+                const float* qc = s.qc[R::row(st + i, lane)];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    u[t].x = fmaf(qc[t], x[i].x, u[t].x);
+                    u[t].y = fmaf(qc[t], x[i].y, u[t].y);
+                    v[t].x = fmaf(qc[kTT + t], x[i].x, v[t].x);
+                    v[t].y = fmaf(qc[kTT + t], x[i].y, v[t].y);
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const float sc = warp_sum(fmaf(u[t].x, e[t].x, u[t].y * e[t].y));
+            if (c < s.count[t]) {                     // the row sees this memory (same for the whole warp)
+                const float mn = fmaxf(m[t], sc);
+                const bool none = mn == -INFINITY;    // only scores of -inf so far: they weigh nothing
+                const float al = none ? 1.f : exp2f(m[t] - mn), wt = none ? 0.f : exp2f(sc - mn);
+                l[t] = fmaf(l[t], al, wt);
+                m[t] = mn;
+                if (wt != 0.f) {                      // 0 weight reads nothing, whatever the value is
+                    o[t].x = fmaf(o[t].x, al, wt * v[t].x);
+                    o[t].y = fmaf(o[t].y, al, wt * v[t].y);
+                }
+            }
+        }
+    }
+    // a lane's o holds the rows it read: sum over the lanes of the same columns
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int off = P / 2; off < 32; off <<= 1) {
+            o[t].x += __shfl_xor_sync(0xffffffffu, o[t].x, off);
+            o[t].y += __shfl_xor_sync(0xffffffffu, o[t].y, off);
+        }
+        if (lane < P / 2) *reinterpret_cast<float2*>(&s.o[warp][t][2 * lane]) = o[t];
+        if (lane == 0) { s.m[warp][t] = m[t]; s.l[warp][t] = l[t]; }
+    }
+}
+
+template <typename T, typename M, int N, int P>
+__global__ void __launch_bounds__(kThreads) sma_paged_kernel(SmaPagedArgs a) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    Smem<N, P>& s = *reinterpret_cast<Smem<N, P>*>(raw);
+    const int tid = threadIdx.x, lane = tid & 31;
+    build_tiles<kTT, kCap>(a, s.tiles);
+    if (tid < 2) piece_header(a.part, blockIdx.x, tid)->state = 0;
+    if (s.tiles.n == 0) return;
+    const long long limit = (long long)a.cache.width * a.cache.R;
+    const float qscale = kLog2e * rsqrtf((float)N);
+    __syncthreads();
+    for (Walk w = start_walk(s.tiles, a.H, kLeast); next_piece(w); advance(s.tiles, w, a.H)) {
+        const int b = s.tiles.seq[w.k], t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, b, t0, kTT);
+        const int* table = a.cache.table + (size_t)b * a.cache.width;
+        __syncthreads();
+        const int grp = group_of(w.h, a.H, a.G);
+        for (int i = tid; i < kTT * N; i += kThreads) {
+            const int t = i / N, n = i % N;
+            const bool live = t < rows;
+            s.qc[n][t] = live ? qscale * ldf(static_cast<const T*>(a.Q) + ((size_t)(t0 + t) * a.H + w.h) * N + n) : 0.f;
+            s.qc[n][kTT + t] = live ? ldf(static_cast<const T*>(a.Cm) + ((size_t)(t0 + t) * a.G + grp) * N + n) : 0.f;
+        }
+        if (tid < kTT) s.count[tid] = tid < rows ? a.mem_count[t0 + tid] : -1;
+        if (tid < 32) {
+            const int most = s.tiles.pre[w.k + 1] - s.tiles.pre[w.k];
+            // a tile with nothing to read has one unit and no page
+            int seen = 0;
+            for (int r = 0; r < rows; ++r) seen = max(seen, usable_count(a.mem_count[t0 + r], limit));
+            const int bad = first_bad_memory(table, a.cache, min(most, seen));
+            if (lane == 0) {
+                s.bad = bad;
+                if (bad < seen) flag_status(a.status, kStatusDevice);
+            }
+        }
+        float2 e[kTT];
+#pragma unroll
+        for (int t = 0; t < kTT; ++t) {
+            e[t] = make_float2(0.f, 0.f);
+            if (t < rows) {
+                const T* src = static_cast<const T*>(a.E) + ((size_t)(t0 + t) * a.H + w.h) * P + 2 * (lane % (P / 2));
+                e[t] = make_float2(ldf(src), ldf(src + 1));
+            }
+        }
+        __syncthreads();
+        if (rows == 1) run_piece<M, N, P, 1>(a, s, w, table, e);
+        else if (rows <= 4) run_piece<M, N, P, 4>(a, s, w, table, e);
+        else run_piece<M, N, P, 8>(a, s, w, table, e);
+        __syncthreads();
+        // join the warps; a whole item is written out, a part of one kept for the join
+        const bool whole = w.last - w.first == w.units;
+        const int which = w.first > 0 ? 0 : 1;
+        if (!whole && tid == 0) {
+            PieceHeader* hd = piece_header(a.part, blockIdx.x, which);
+            *hd = PieceHeader{w.last == w.units ? 2 : 1, t0, rows, w.h};
+        }
+        for (int i = tid; i < rows * P; i += kThreads) {
+            const int t = i / P, p = i % P;
+            float mm = -INFINITY, l = 0.f, o = 0.f;
+            for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, s.m[k][t]);
+            for (int k = 0; k < kWarps; ++k) {
+                const float f = s.l[k][t] == 0.f ? 0.f : exp2f(s.m[k][t] - mm);
+                l = fmaf(s.l[k][t], f, l);
+                if (f != 0.f) o = fmaf(s.o[k][t][p], f, o);
+            }
+            const int count = s.count[t];
+            if (whole) {
+                if (count < 0 || count > s.bad) continue;      // a row that is not to be computed
+                const size_t at = ((size_t)(t0 + t) * a.H + w.h) * P + p;
+                const float oo = l == 0.f ? 0.f : o / l;
+                a.out[at] = a.y_ssd ? fmaf(a.g, oo, a.y_ssd[at]) : oo;
+            } else {
+                float* row = piece_rows<kTT, P>(a.part, blockIdx.x, which) + t * (2 + P);
+                // the sum of a row that is not to be computed is kept as -1
+                if (p == 0) { row[0] = mm; row[1] = count < 0 || count > s.bad ? -1.f : l; }
+                row[2 + p] = o;
+            }
+        }
+    }
+}
+
+// Block i joins the item that begins in block i's run and ends in a later one's.
+template <int TT, int P>
+__global__ void __launch_bounds__(256) sma_paged_combine_kernel(SmaPagedArgs a, int blocks) {
+    const PieceHeader hd = *piece_header(a.part, blockIdx.x, 1);
+    if (hd.state != 1) return;
+    int end = blockIdx.x + 1;                 // the block that has the item's last piece
+    while (end < blocks && piece_header(a.part, end, 0)->state != 2) ++end;
+    for (int i = threadIdx.x; i < hd.rows * P; i += blockDim.x) {
+        const int t = i / P, p = i % P;
+        const float* row = piece_rows<TT, P>(a.part, blockIdx.x, 1) + t * (2 + P);
+        float m = row[0], l = row[1], o = row[2 + p];
+        if (l < 0.f) continue;
+        for (int j = blockIdx.x + 1; j <= end && j < blocks; ++j) {
+            if (piece_header(a.part, j, 0)->state == 0) continue;
+            const float* r = piece_rows<TT, P>(a.part, j, 0) + t * (2 + P);
+            if (r[1] == 0.f) continue;        // saw nothing
+            const float mn = fmaxf(m, r[0]);
+            const float f = l == 0.f ? 0.f : exp2f(m - mn), k = exp2f(r[0] - mn);
+            l = fmaf(l, f, r[1] * k);
+            o = (f == 0.f ? 0.f : o * f) + r[2 + p] * k;
+            m = mn;
+        }
+        const size_t at = ((size_t)(hd.t0 + t) * a.H + hd.h) * P + p;
+        const float oo = l == 0.f ? 0.f : o / l;
+        a.out[at] = a.y_ssd ? fmaf(a.g, oo, a.y_ssd[at]) : oo;
+    }
+}
+
+int sm_count_now() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return n;
+}
+
+template <typename T, typename M, int N, int P>
+cudaError_t run(const SmaPagedArgs& a, cudaStream_t st) {
+    auto kern = sma_paged_kernel<T, M, N, P>;
+    const int smem = (int)sizeof(Smem<N, P>);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int sms = sm_count_now();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const int blocks = min(2 * sms, kMaxBlocks);
+    kern<<<blocks, kThreads, smem, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    sma_paged_combine_kernel<kTT, P><<<blocks, 256, 0, st>>>(a, blocks);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    count_launches(2);
+    return cudaSuccess;
+}
+
+template <typename T>
+cudaError_t run_type(const SmaPagedArgs& a, cudaStream_t st) {
+    if (a.cache.mxfp4) {
+        if (a.N == 128 && a.P == 64) return run<T, Fp4, 128, 64>(a, st);
+        if (a.N == 64 && a.P == 64) return run<T, Fp4, 64, 64>(a, st);
+        return cudaErrorInvalidValue;
+    }
+    if (a.N == 128 && a.P == 64) return run<T, T, 128, 64>(a, st);
+    if (a.N == 64 && a.P == 64) return run<T, T, 64, 64>(a, st);
+    if (a.N == 16 && a.P == 16) return run<T, T, 16, 16>(a, st);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+size_t sma_paged_workspace_bytes(int P) {
+    return 2 * (size_t)kMaxBlocks * (sizeof(PieceHeader) + sizeof(float) * kTT * (2 + (size_t)P));
+}
+long long sma_paged_tiles(int B, int T) { return B + (long long)T / kTT; }
+long long sma_paged_max_tiles() { return kCap; }
+
+cudaError_t launch_sma_paged(const SmaPagedArgs& a, dart_dtype dt, cudaStream_t st) {
+    return dt == DART_F32 ? run_type<float>(a, st) : run_type<__nv_bfloat16>(a, st);
+}
+
+}  // namespace dart

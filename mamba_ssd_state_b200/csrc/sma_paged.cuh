@@ -1,0 +1,196 @@
+// sma_paged.cuh -- how the paged attention kernels divide their work.
+//
+// The packed tokens of a sequence are cut into tiles of TT rows.  A tile reads,
+// for every head, the memories its rows may see (up to the largest count among
+// them): (tile, head, memory) in that order is one long list of equal units,
+// and block i of G takes the i-th of G equal runs of it, whatever the batch
+// looks like.  An item, (tile, head), whose memories fall into several runs
+// leaves one partial result (running maximum, sum, weighted values) per block
+// in the workspace; a block has at most two such pieces, the one its run
+// begins with and the one it ends with.  sma_paged_combine joins them in order.
+//
+// Every block computes the list itself from cu_tokens and mem_count (they live
+// on the device), which costs less than a launch of its own would.
+#pragma once
+
+#include "dart_paged.cuh"
+
+namespace dart {
+
+// Workspace: per block kPieceInts ints of header for its first and its last
+// piece, then the pieces, rows of 2 + P floats.
+struct PieceHeader {
+    int state;    // 0: no such piece, 1: more pieces follow, 2: the item ends here
+    int t0;       // first token row of the tile
+    int rows;
+    int h;
+};
+constexpr int kMaxBlocks = 512;   // persistent blocks of any of the kernels, and header slots
+
+#ifdef __CUDACC__
+
+// Tiles of the batch in shared memory: tile k covers rows t0[k] .. of sequence
+// seq[k] and has pre[k+1] - pre[k] >= 1 units a head (1 with nothing to read).
+template <int CAP>
+struct TileList {
+    int pre[CAP + 1];
+    int seq[CAP];
+    int t0[CAP];
+    int scan[32];
+    int n;
+};
+
+// Rows of tile k.
+__device__ __forceinline__ int tile_rows(const int* cu, int seq, int t0, int TT) { return min(TT, cu[seq + 1] - t0); }
+
+// The count a row may really see: 0 for rows that are not to be computed.
+__device__ __forceinline__ int usable_count(int c, long long limit) { return c < 0 || c > limit ? 0 : c; }
+
+// Sum over the block of one value per thread, exclusive; total to all.  scan: 32 ints.
+__device__ __forceinline__ int block_scan(int v, int* scan, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (int)blockDim.x >> 5;
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += u;
+    }
+    __syncthreads();   // scan may still be read from the last call
+    if (lane == 31) scan[warp] = s;
+    __syncthreads();
+    int before = 0;
+    total = 0;
+    for (int w = 0; w < warps; ++w) {
+        if (w < warp) before += scan[w];
+        total += scan[w];
+    }
+    return before + s - v;
+}
+
+// Builds the list; all threads of the block.  Ranges that are no ranges, counts
+// beyond the table and lists longer than CAP (only overlapping ranges make one)
+// are flagged, and what they name is left out.
+template <int TT, int CAP>
+__device__ __forceinline__ void build_tiles(const SmaPagedArgs& a, TileList<CAP>& L) {
+    const int threads = blockDim.x, tid = threadIdx.x;
+    const long long limit = (long long)a.cache.width * a.cache.R;
+    bool bad = false;
+    int n = 0;
+    for (int b0 = 0; b0 < a.B; b0 += threads) {
+        const int b = b0 + tid;
+        int t0 = 0, t1 = 0, tiles = 0;
+        if (b < a.B) {
+            if (token_range(a.cu, b, a.T, t0, t1)) tiles = (t1 - t0 + TT - 1) / TT;
+            else bad = true;
+        }
+        int total;
+        const int at = n + block_scan(tiles, L.scan, total);
+        for (int j = 0; j < tiles; ++j) {
+            if (at + j >= CAP) { bad = true; break; }
+            L.seq[at + j] = b;
+            L.t0[at + j] = t0 + j * TT;
+        }
+        n = min(CAP, n + total);
+    }
+    __syncthreads();
+    int sum = 0;
+    for (int k0 = 0; k0 < n; k0 += threads) {
+        const int k = k0 + tid;
+        int most = 0;
+        if (k < n) {
+            const int t0 = L.t0[k], rows = tile_rows(a.cu, L.seq[k], t0, TT);
+#pragma unroll 8
+            for (int r = 0; r < rows; ++r) {
+                const int c = a.mem_count[t0 + r];
+                bad |= c < -1 || c > limit;
+                most = max(most, usable_count(c, limit));
+            }
+            most = max(most, 1);
+        }
+        int total;
+        const int at = sum + block_scan(most, L.scan, total);
+        if (k < n) L.pre[k] = at;
+        sum += total;
+    }
+    if (tid == 0) { L.pre[n] = sum; L.n = n; }
+    if (bad && blockIdx.x == 0) flag_status(a.status, kStatusDevice);
+    __syncthreads();
+}
+
+// This block's run of units, and the walk over its pieces.
+struct Walk {
+    long long u, end;    // next unit, end of the run
+    int k, h, c;         // tile, head, memory of unit u
+    int first, last;     // memories of the piece: [first, last)
+    int units;           // units of the item
+};
+
+// Runs of fewer than `least` units are not cut smaller.
+template <int CAP>
+__device__ __forceinline__ Walk start_walk(const TileList<CAP>& L, int H, int least) {
+    Walk w;
+    const long long W = (long long)L.pre[L.n] * H;
+    const long long G = min((long long)gridDim.x, (W + least - 1) / least);
+    const long long i = blockIdx.x;
+    w.u = i < G ? W * i / G : W;
+    w.end = i < G ? W * (i + 1) / G : W;
+    int lo = 0, hi = L.n - 1;              // the tile of unit u
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if ((long long)L.pre[mid] * H <= w.u) lo = mid; else hi = mid - 1;
+    }
+    w.k = lo;
+    w.units = 1;
+    w.h = w.c = 0;
+    if (w.u < w.end) {
+        w.units = L.pre[lo + 1] - L.pre[lo];
+        const long long r = w.u - (long long)L.pre[lo] * H;
+        w.h = (int)(r / w.units);
+        w.c = (int)(r % w.units);
+    }
+    return w;
+}
+// The next piece; false at the end of the run.
+__device__ __forceinline__ bool next_piece(Walk& w) {
+    if (w.u >= w.end) return false;
+    w.first = w.c;
+    w.last = (int)min((long long)w.units, w.c + (w.end - w.u));
+    return true;
+}
+template <int CAP>
+__device__ __forceinline__ void advance(const TileList<CAP>& L, Walk& w, int H) {
+    w.u += w.last - w.first;
+    w.c = 0;
+    if (++w.h == H) {
+        w.h = 0;
+        ++w.k;
+        if (w.k < L.n) w.units = L.pre[w.k + 1] - L.pre[w.k];
+    }
+}
+
+// Header and rows of a block's piece in the workspace: which = 0 for the piece
+// that its run begins with when the item began earlier, 1 for an item that
+// begins in the run and does not end there.
+__device__ __forceinline__ PieceHeader* piece_header(float* part, int block, int which) {
+    return reinterpret_cast<PieceHeader*>(part) + 2 * block + which;
+}
+template <int TT, int P>
+__device__ __forceinline__ float* piece_rows(float* part, int block, int which) {
+    return part + 2 * kMaxBlocks * (sizeof(PieceHeader) / sizeof(float)) + (size_t)(2 * block + which) * TT * (2 + P);
+}
+
+// First memory of sequence row `table` whose page is no page, among the first
+// `count`; `count` if there is none.  All lanes of a warp.
+__device__ __forceinline__ int first_bad_memory(const int* table, const PagedCache& c, int count) {
+    const int lane = threadIdx.x & 31, pages = (int)(((long long)count + c.R - 1) / c.R);
+    for (int k = 0; k < pages; k += 32) {
+        const int page = k + lane < pages ? table[k + lane] : 0;
+        const unsigned m = __ballot_sync(0xffffffffu, page < 0 || page >= c.npages);
+        if (m) return min(count, (k + __ffs(m) - 1) * c.R);
+    }
+    return count;
+}
+
+#endif
+
+}  // namespace dart

@@ -35,7 +35,8 @@ EXPORTS = ("dart_ssd_chunk_scan_workspace_bytes", "dart_ssd_chunk_scan", "dart_s
            "dart_sma_forward_decayed", "dart_decode_step_decayed", "dart_decode_memlog_init",
            "dart_decode_step_e4m3", "dart_cache_quantize_e4m3", "dart_sma_backward_workspace_bytes",
            "dart_sma_backward", "dart_ssd_scan_backward_workspace_bytes", "dart_ssd_scan_backward",
-           "dart_selftest_wait_timeout")
+           "dart_selftest_wait_timeout", "dart_cache_write_paged", "dart_cache_read_paged", "dart_ssd_extend",
+           "dart_sma_paged", "dart_sma_paged_workspace_bytes")
 
 
 class DartError(RuntimeError):
@@ -48,6 +49,14 @@ class Dims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in
                 ("batch", "seqlen", "nheads", "headdim", "dstate", "chunk", "ngroups")]
 
+
+class PagedCache(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int), ("npages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("table_width", ctypes.c_int), ("pages", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("table", ctypes.c_void_p)]
+
+
+DART_CACHE_DTYPE, DART_CACHE_MXFP4 = 0, 1
 
 _P = ctypes.c_void_p
 _lib = None
@@ -114,6 +123,18 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
     lib.dart_decode_step_noalloc.restype = ctypes.c_int
     lib.dart_decode_step_noalloc.argtypes = ([D, ctypes.c_int] + [_P] * 7 + [ctypes.c_float] + [_P] * 3
                                              + [ctypes.c_int] + [_P] * 4)
+    K = ctypes.POINTER(PagedCache)
+    lib.dart_cache_write_paged.restype = ctypes.c_int
+    lib.dart_cache_write_paged.argtypes = [D, ctypes.c_int, _P, ctypes.c_int, _P, _P, K, _P]
+    lib.dart_cache_read_paged.restype = ctypes.c_int
+    lib.dart_cache_read_paged.argtypes = [D, ctypes.c_int, K, _P, _P, _P, ctypes.c_int, _P]
+    lib.dart_ssd_extend.restype = ctypes.c_int
+    lib.dart_ssd_extend.argtypes = [D, ctypes.c_int] + [_P] * 10 + [K] + [_P] * 7
+    lib.dart_sma_paged_workspace_bytes.restype = ctypes.c_size_t
+    lib.dart_sma_paged_workspace_bytes.argtypes = [D]
+    lib.dart_sma_paged.restype = ctypes.c_int
+    lib.dart_sma_paged.argtypes = ([D, ctypes.c_int] + [_P] * 4 + [K, _P, ctypes.c_float] + [_P] * 3
+                                   + [ctypes.c_size_t, _P])
     _lib = lib
     return lib
 
@@ -545,6 +566,202 @@ def decode_memlog_init(dt, A, chunk: int, memlog):
         _check(lib.dart_decode_memlog_init(ctypes.byref(dims), _ptr(dt), _ptr(A), _ptr(memlog),
                                            memlog.shape[2], _stream()))
     return memlog
+
+
+# ---------------------------------------------------------------------------
+# Paged memory cache: ragged batches with several new tokens per sequence.
+# Memory m of sequence b is slot m % R of page table[b, m // R]; pages is
+# [npages,H,R,N,P] in the tokens' dtype, or uint8 codes [npages,H,R,P,N/2] with
+# scales uint8 [npages,H,R,P,N/32] (the 4-bit format of include/dart.h).
+# ---------------------------------------------------------------------------
+def _in_place(**tensors):
+    for name, t in tensors.items():
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor")
+
+
+def _counters(dev, length, **tensors):
+    """int32 device vectors of a given length."""
+    _in_place(**tensors)
+    for name, t in tensors.items():
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name} must be int32, got {t.dtype}")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the pages on {dev}")
+        _shape(name, t, (length,))
+
+
+def _paged(pages, scales, table, dtype, B, H, N, P) -> PagedCache:
+    """The C description of a paged cache, after checking it against the shapes it has to hold."""
+    _in_place(pages=pages, table=table, **({} if scales is None else {"scales": scales}))
+    if table.dtype != torch.int32 or table.dim() != 2:
+        raise TypeError("table must be an int32 tensor [B, width]")
+    _shape("table", table, (B, table.shape[1]))
+    if pages.dim() != 5:
+        raise ValueError(f"pages: expected 5 dimensions, got shape {tuple(pages.shape)}")
+    npages, _, R = pages.shape[:3]
+    for t in (table, scales):
+        if t is not None and t.device != pages.device:
+            raise ValueError(f"table, scales and pages are on different devices ({t.device}, {pages.device})")
+    if pages.dtype == torch.uint8:
+        if scales is None or scales.dtype != torch.uint8:
+            raise TypeError("4-bit (uint8) pages need their uint8 scales")
+        _shape("pages", pages, (npages, H, R, P, N // 2))
+        _shape("scales", scales, (npages, H, R, P, N // 32))
+        fmt = DART_CACHE_MXFP4
+    else:
+        if scales is not None:
+            raise ValueError("scales belong to 4-bit (uint8) pages")
+        if pages.dtype != dtype:
+            raise TypeError(f"pages are {pages.dtype}, the inputs {dtype}")
+        _shape("pages", pages, (npages, H, R, N, P))
+        fmt = DART_CACHE_DTYPE
+    return PagedCache(fmt, npages, R, table.shape[1], _ptr(pages), _ptr(scales), _ptr(table))
+
+
+def dart_cache_write_paged(dH, first, count, pages, table, *, scales=None):
+    """Memories into pages: memory first[b] + i of sequence b = dH[b, :, i] for
+    i < count[b].  dH [B,H,C,N,P] (float32 or bfloat16, e.g. dart_ssd_chunk_scan's
+    memories), first and count int32 [B], pages/scales in place; all on the
+    device.  uint8 pages take 4-bit codes.  Returns (pages, scales)."""
+    lib = load()
+    _in_place(dH=dH)
+    B, H, C, N, P = dH.shape
+    dev = pages.device
+    cache = _paged(pages, scales, table, dH.dtype, B, H, N, P)
+    if dH.device != dev:
+        raise ValueError(f"dH is on {dH.device}, the pages on {dev}")
+    _counters(dev, B, first=first, count=count)
+    dims = Dims(B, 0, H, P, N, 1, 1)
+    with torch.cuda.device(dev):
+        _check(lib.dart_cache_write_paged(ctypes.byref(dims), _dtype_code(dH.dtype), _ptr(dH), C, _ptr(first),
+                                          _ptr(count), ctypes.byref(cache), _stream()))
+    return pages, scales
+
+
+def dart_cache_read_paged(pages, table, first, count, *, out, scales=None):
+    """Memories out of pages: out[b, :, i] = memory first[b] + i of sequence b for
+    i < count[b]; other entries of out [B,H,C,N,P] (float32 or bfloat16; the
+    pages' dtype unless they hold 4-bit codes) are left as they are.  Returns out."""
+    lib = load()
+    _in_place(out=out)
+    B, H, C, N, P = out.shape
+    dev = pages.device
+    cache = _paged(pages, scales, table, out.dtype, B, H, N, P)
+    if out.device != dev:
+        raise ValueError(f"out is on {out.device}, the pages on {dev}")
+    _counters(dev, B, first=first, count=count)
+    dims = Dims(B, 0, H, P, N, 1, 1)
+    with torch.cuda.device(dev):
+        _check(lib.dart_cache_read_paged(ctypes.byref(dims), _dtype_code(out.dtype), ctypes.byref(cache), _ptr(first),
+                                         _ptr(count), _ptr(out), C, _stream()))
+    return out
+
+
+def dart_ssd_extend(x, dt, A, Bm, Cm, cu_tokens, state, dH_cur, pages, table, nchunks, pos, chunk: int, *,
+                    scales=None, state_out=None, dH_cur_out=None, nchunks_out=None, pos_out=None, y=None,
+                    mem_count=None) -> dict:
+    """A run of new tokens per sequence through the recurrence, from the middle of
+    a chunk on; chunks that close on the way append their memory to the pages.
+
+    x[T,H,P], Bm/Cm[T,N] or [T,G,N] (float32 or bfloat16), dt[T,H], A[H] float32:
+    the packed tokens, sequence b owning rows cu_tokens[b]..cu_tokens[b+1]-1
+    (int32 [B+1]).  state, dH_cur float32 [B,H,N,P]; nchunks, pos int32 [B].
+    Without state_out / dH_cur_out the state is updated in place; with them the
+    old one is kept (to go back to when drafted tokens are not accepted).  The
+    counters are always returned in tensors of their own.  Returns a dict: y
+    float32 [T,H,P], state, dH_cur, nchunks, pos (after the run) and mem_count
+    int32 [T] for dart_sma_paged.  Rows no sequence owns are not written."""
+    lib = load()
+    dev = pages.device
+    x, Bm, Cm = (_dev(v, dev, x.dtype) for v in (x, Bm, Cm))
+    dt, A = _dev(dt, dev, torch.float32), _dev(A, dev, torch.float32)
+    T, H, P = x.shape
+    B, _, N, _ = state.shape
+    _shape("dt", dt, (T, H)); _shape("A", A, (H,))
+    G = _bc_groups("Bm", Bm, (T,), H)
+    if Bm.shape[-1] != N or Cm.shape != Bm.shape:
+        raise ValueError("Bm and Cm must both be [T,N] or [T,G,N] with the state's N")
+    state_out = state if state_out is None else state_out
+    dH_cur_out = dH_cur if dH_cur_out is None else dH_cur_out
+    for name, t in (("state", state), ("dH_cur", dH_cur), ("state_out", state_out), ("dH_cur_out", dH_cur_out)):
+        _in_place(**{name: t})
+        _shape(name, t, (B, H, N, P))
+        if t.dtype != torch.float32 or t.device != dev:
+            raise TypeError(f"{name} must be float32 on {dev}")
+    cache = _paged(pages, scales, table, x.dtype, B, H, N, P)
+    nchunks_out = torch.empty_like(nchunks) if nchunks_out is None else nchunks_out
+    pos_out = torch.empty_like(pos) if pos_out is None else pos_out
+    _counters(dev, B, nchunks=nchunks, pos=pos, nchunks_out=nchunks_out, pos_out=pos_out)
+    _counters(dev, B + 1, cu_tokens=cu_tokens)
+    if y is None:
+        y = torch.empty((T, H, P), device=dev, dtype=torch.float32)
+    if mem_count is None:
+        mem_count = torch.empty((T,), device=dev, dtype=torch.int32)
+    _in_place(y=y)
+    _shape("y", y, (T, H, P))
+    if y.dtype != torch.float32 or y.device != dev:
+        raise TypeError(f"y must be float32 on {dev}")
+    _counters(dev, T, mem_count=mem_count)
+    dims = Dims(B, T, H, P, N, chunk, G)
+    with torch.cuda.device(dev):
+        _check(lib.dart_ssd_extend(ctypes.byref(dims), _dtype_code(x.dtype), _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm),
+                                   _ptr(Cm), _ptr(cu_tokens), _ptr(state), _ptr(state_out), _ptr(dH_cur),
+                                   _ptr(dH_cur_out), ctypes.byref(cache), _ptr(nchunks), _ptr(pos),
+                                   _ptr(nchunks_out), _ptr(pos_out), _ptr(y), _ptr(mem_count), _stream()))
+    return {"y": y, "state": state_out, "dH_cur": dH_cur_out, "nchunks": nchunks_out, "pos": pos_out,
+            "mem_count": mem_count}
+
+
+def dart_sma_paged(Q, E, Cm, cu_tokens, pages, table, mem_count, g: float, y_ssd=None, *, scales=None, out=None,
+                   workspace=None):
+    """State-memory attention of packed tokens over paged memories: float32
+    [T,H,P] equal to y_ssd + g*o (or o when y_ssd is None), token t of sequence b
+    seeing the sequence's first mem_count[t] memories (int32 [T], as
+    dart_ssd_extend returns it; -1 leaves the row as it is).  Q[T,H,N], E[T,H,P],
+    Cm[T,N] or [T,G,N] in one dtype.  out may be y_ssd itself.  Rows no sequence
+    owns are not written."""
+    lib = load()
+    dev = pages.device
+    Q, E, Cm = (_dev(v, dev, Q.dtype) for v in (Q, E, Cm))
+    y_ssd = _dev(y_ssd, dev, torch.float32)
+    T, H, N = Q.shape
+    P = E.shape[-1]
+    B = table.shape[0]
+    _shape("E", E, (T, H, P))
+    G = _bc_groups("Cm", Cm, (T,), H)
+    _shape("Cm", Cm, (*Cm.shape[:-1], N))
+    cache = _paged(pages, scales, table, Q.dtype, B, H, N, P)
+    _counters(dev, B + 1, cu_tokens=cu_tokens)
+    _counters(dev, T, mem_count=mem_count)
+    if y_ssd is not None:
+        _shape("y_ssd", y_ssd, (T, H, P))
+    if out is None:
+        out = torch.empty((T, H, P), device=dev, dtype=torch.float32)
+    _in_place(out=out)
+    _shape("out", out, (T, H, P))
+    if out.dtype != torch.float32 or out.device != dev:
+        raise TypeError(f"out must be float32 on {dev}")
+    dims = Dims(B, T, H, P, N, 1, G)
+    if workspace is None:
+        workspace = torch.empty(lib.dart_sma_paged_workspace_bytes(ctypes.byref(dims)), device=dev, dtype=torch.uint8)
+    with torch.cuda.device(dev):
+        _check(lib.dart_sma_paged(ctypes.byref(dims), _dtype_code(Q.dtype), _ptr(Q), _ptr(E), _ptr(Cm),
+                                  _ptr(cu_tokens), ctypes.byref(cache), _ptr(mem_count), float(g), _ptr(y_ssd),
+                                  _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                  _stream()))
+    return out
+
+
+def layer_extend(x, dt, A, Bm, Cm, Q, E, g: float, cu_tokens, state, dH_cur, pages, table, nchunks, pos, chunk: int, *,
+                 scales=None, state_out=None, dH_cur_out=None) -> dict:
+    """The DART layer for a run of new tokens per sequence: dart_ssd_extend, then
+    dart_sma_paged with the gated residual written in place over y.  Returns
+    dart_ssd_extend's dict with y the layer output."""
+    res = dart_ssd_extend(x, dt, A, Bm, Cm, cu_tokens, state, dH_cur, pages, table, nchunks, pos, chunk,
+                          scales=scales, state_out=state_out, dH_cur_out=dH_cur_out)
+    dart_sma_paged(Q, E, Cm, cu_tokens, pages, table, res["mem_count"], g, res["y"], scales=scales, out=res["y"])
+    return res
 
 
 def dart_decode_step_noalloc(x, dt, A, Bm, Cm, Q, E, g: float, state, dH_cur, cache, nchunks, pos,
