@@ -487,7 +487,7 @@ size_t dart_sma_paged_workspace_bytes(const dart_dims* dims);
  *   mem_count: int32 [T]; -1 marks a row that is left as it is.
  *   workspace: dart_sma_paged_workspace_bytes(), 16-byte aligned, contents on
  *   entry do not matter; calls that may overlap on the GPU need one each.
- * Limits: batch + T / 8 <= 4096.  Deterministic.  Two kernels.
+ * Limits: batch + T / 4 <= 4096.  Deterministic.  Two kernels.
  */
 dart_status dart_sma_paged(const dart_dims* dims, dart_dtype dtype, const void* Q, const void* E,
                            const void* Cm, const int* cu_tokens, const dart_paged_cache* cache,

@@ -571,7 +571,7 @@ dart_status dart_sma_paged(const dart_dims* d, dart_dtype dtype, const void* Q, 
     }
     if (dart::sma_paged_tiles(d->batch, d->seqlen) > dart::sma_paged_max_tiles())
         return fail(DART_ERR_UNSUPPORTED, "dart_sma_paged: %d sequences and %d tokens are too many for one call "
-                    "(batch + seqlen / 8 must be <= %lld)", d->batch, d->seqlen, dart::sma_paged_max_tiles());
+                    "(batch + seqlen / 4 must be <= %lld)", d->batch, d->seqlen, dart::sma_paged_max_tiles());
     const size_t need = dart_sma_paged_workspace_bytes(d);
     if (workspace_bytes < need)
         return fail(DART_ERR_INVALID_ARG, "workspace: %zu bytes, need %zu", workspace_bytes, need);

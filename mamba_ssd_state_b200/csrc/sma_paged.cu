@@ -1,5 +1,5 @@
 // sma_paged.cu -- state-memory attention of packed new tokens over paged chunk
-// memories, on CUDA cores.
+// memories, on CUDA cores: float32, and the shape (16, 16).
 //
 // Per token t, head h and visible memory M_c (N x P):
 //   u = Q_t^T M_c,  v = C_t^T M_c,  s = u . E_t / sqrt(N),
@@ -10,6 +10,9 @@
 // 2 x 8 products.  Scores are summed over the warp, the softmax runs online in
 // base 2, and v is folded into the lane's own columns, so that the eight warps
 // of a block meet only at the end of a piece.
+#include <atomic>
+
+#include "sm100.cuh"
 #include "sma_paged.cuh"
 
 namespace dart {
@@ -53,30 +56,6 @@ struct Rows {
     }
 };
 
-struct Fp4 {};
-template <int N, int P>
-struct Rows<Fp4, N, P> {
-    static constexpr int STEPS = N, BATCH = 8, K = N / 32;
-    const uint32_t* codes;
-    const uint8_t* scales;
-    __device__ Rows(const PagedCache& c, size_t mem, int lane)
-        : codes(static_cast<const uint32_t*>(c.pages) + mem * (N * P / 8) + 2 * lane * (N / 8)),
-          scales(c.scales + mem * (N * P / 32) + 2 * lane * K) {}
-    // step = 8 (q K + k) + c is row 32k + 16 (c / 4) + 4q + c % 4
-    __device__ __forceinline__ static int row(int step, int) {
-        const int w = step / 8, c = step % 8;
-        return 32 * (w % K) + 16 * (c / 4) + 4 * (w / K) + c % 4;
-    }
-    __device__ __forceinline__ void load(int step, float2 (&v)[BATCH]) {
-        const int w = step / 8;
-        const uint32_t c0 = codes[w], c1 = codes[N / 8 + w];
-        const float s0 = mxfp4_scale(scales[w % K]), s1 = mxfp4_scale(scales[K + w % K]);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            v[c] = make_float2(mxfp4_level(c0 >> (4 * c) & 15u) * s0, mxfp4_level(c1 >> (4 * c) & 15u) * s1);
-    }
-};
-
 // This warp's memories of a piece for the first NT tokens of the tile.
 template <typename T, int N, int P, int NT>
 __device__ __forceinline__ void run_piece(const SmaPagedArgs& a, Smem<N, P>& s, const Walk& w, const int* table, const float2 (&e)[kTT]) {
@@ -113,7 +92,7 @@ __device__ __forceinline__ void run_piece(const SmaPagedArgs& a, Smem<N, P>& s, 
             if (c < s.count[t]) {                     // the row sees this memory (same for the whole warp)
                 const float mn = fmaxf(m[t], sc);
                 const bool none = mn == -INFINITY;    // only scores of -inf so far: they weigh nothing
-                const float al = none ? 1.f : exp2f(m[t] - mn), wt = none ? 0.f : exp2f(sc - mn);
+                const float al = none ? 1.f : exp2f(m[t] - mn), wt = none ? (sc == sc ? 0.f : sc) : exp2f(sc - mn);
                 l[t] = fmaf(l[t], al, wt);
                 m[t] = mn;
                 if (wt != 0.f) {                      // 0 weight reads nothing, whatever the value is
@@ -136,7 +115,7 @@ __device__ __forceinline__ void run_piece(const SmaPagedArgs& a, Smem<N, P>& s, 
     }
 }
 
-template <typename T, typename M, int N, int P>
+template <typename T, int N, int P>
 __global__ void __launch_bounds__(kThreads) sma_paged_kernel(SmaPagedArgs a) {
     extern __shared__ __align__(16) uint8_t raw[];
     Smem<N, P>& s = *reinterpret_cast<Smem<N, P>*>(raw);
@@ -180,45 +159,18 @@ __global__ void __launch_bounds__(kThreads) sma_paged_kernel(SmaPagedArgs a) {
             }
         }
         __syncthreads();
-        if (rows == 1) run_piece<M, N, P, 1>(a, s, w, table, e);
-        else if (rows <= 4) run_piece<M, N, P, 4>(a, s, w, table, e);
-        else run_piece<M, N, P, 8>(a, s, w, table, e);
+        if (rows == 1) run_piece<T, N, P, 1>(a, s, w, table, e);
+        else if (rows <= 4) run_piece<T, N, P, 4>(a, s, w, table, e);
+        else run_piece<T, N, P, 8>(a, s, w, table, e);
         __syncthreads();
-        // join the warps; a whole item is written out, a part of one kept for the join
-        const bool whole = w.last - w.first == w.units;
-        const int which = w.first > 0 ? 0 : 1;
-        if (!whole && tid == 0) {
-            PieceHeader* hd = piece_header(a.part, blockIdx.x, which);
-            *hd = PieceHeader{w.last == w.units ? 2 : 1, t0, rows, w.h};
-        }
-        for (int i = tid; i < rows * P; i += kThreads) {
-            const int t = i / P, p = i % P;
-            float mm = -INFINITY, l = 0.f, o = 0.f;
-            for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, s.m[k][t]);
-            for (int k = 0; k < kWarps; ++k) {
-                const float f = s.l[k][t] == 0.f ? 0.f : exp2f(s.m[k][t] - mm);
-                l = fmaf(s.l[k][t], f, l);
-                if (f != 0.f) o = fmaf(s.o[k][t][p], f, o);
-            }
-            const int count = s.count[t];
-            if (whole) {
-                if (count < 0 || count > s.bad) continue;      // a row that is not to be computed
-                const size_t at = ((size_t)(t0 + t) * a.H + w.h) * P + p;
-                const float oo = l == 0.f ? 0.f : o / l;
-                a.out[at] = a.y_ssd ? fmaf(a.g, oo, a.y_ssd[at]) : oo;
-            } else {
-                float* row = piece_rows<kTT, P>(a.part, blockIdx.x, which) + t * (2 + P);
-                // the sum of a row that is not to be computed is kept as -1
-                if (p == 0) { row[0] = mm; row[1] = count < 0 || count > s.bad ? -1.f : l; }
-                row[2 + p] = o;
-            }
-        }
+        finish_piece<kWarps, kTT, P, P>(a, w, t0, rows, s.count, s.bad, s.m, s.l, s.o, nullptr, tid, kThreads);
     }
 }
 
 // Block i joins the item that begins in block i's run and ends in a later one's.
 template <int TT, int P>
 __global__ void __launch_bounds__(256) sma_paged_combine_kernel(SmaPagedArgs a, int blocks) {
+    sm100::griddep_wait();
     const PieceHeader hd = *piece_header(a.part, blockIdx.x, 1);
     if (hd.state != 1) return;
     int end = blockIdx.x + 1;                 // the block that has the item's last piece
@@ -244,52 +196,57 @@ __global__ void __launch_bounds__(256) sma_paged_combine_kernel(SmaPagedArgs a, 
     }
 }
 
-int sm_count_now() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return n;
-}
-
-template <typename T, typename M, int N, int P>
+template <typename T, int N, int P>
 cudaError_t run(const SmaPagedArgs& a, cudaStream_t st) {
-    auto kern = sma_paged_kernel<T, M, N, P>;
-    const int smem = (int)sizeof(Smem<N, P>);
+    auto kern = sma_paged_kernel<T, N, P>;
+    const int smem = (int)sizeof(Smem<N, P>), sms = paged_sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int sms = sm_count_now();
-    if (sms <= 0) return cudaErrorInvalidDevice;
     const int blocks = min(2 * sms, kMaxBlocks);
     kern<<<blocks, kThreads, smem, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    sma_paged_combine_kernel<kTT, P><<<blocks, 256, 0, st>>>(a, blocks);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    count_launches(2);
-    return cudaSuccess;
-}
-
-template <typename T>
-cudaError_t run_type(const SmaPagedArgs& a, cudaStream_t st) {
-    if (a.cache.mxfp4) {
-        if (a.N == 128 && a.P == 64) return run<T, Fp4, 128, 64>(a, st);
-        if (a.N == 64 && a.P == 64) return run<T, Fp4, 64, 64>(a, st);
-        return cudaErrorInvalidValue;
-    }
-    if (a.N == 128 && a.P == 64) return run<T, T, 128, 64>(a, st);
-    if (a.N == 64 && a.P == 64) return run<T, T, 64, 64>(a, st);
-    if (a.N == 16 && a.P == 16) return run<T, T, 16, 16>(a, st);
-    return cudaErrorInvalidValue;
+    count_launches(1);
+    return launch_sma_paged_combine(a, blocks, kTT, st);
 }
 
 }  // namespace
 
+int paged_sm_count() {
+    static std::atomic<int> cache[64];   // threads that race on the first lookup store the same value
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        cache[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+cudaError_t launch_sma_paged_combine(const SmaPagedArgs& a, int blocks, int tt, cudaStream_t st) {
+    cudaError_t e;
+    if (a.P == 64)
+        e = tt == 8 ? launch_dependent(sma_paged_combine_kernel<8, 64>, dim3(blocks), dim3(256), 0, st, 1, a, blocks)
+                    : launch_dependent(sma_paged_combine_kernel<4, 64>, dim3(blocks), dim3(256), 0, st, 1, a, blocks);
+    else
+        e = launch_dependent(sma_paged_combine_kernel<8, 16>, dim3(blocks), dim3(256), 0, st, 1, a, blocks);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
 size_t sma_paged_workspace_bytes(int P) {
     return 2 * (size_t)kMaxBlocks * (sizeof(PieceHeader) + sizeof(float) * kTT * (2 + (size_t)P));
 }
-long long sma_paged_tiles(int B, int T) { return B + (long long)T / kTT; }
+long long sma_paged_tiles(int B, int T) { return B + (long long)T / 4; }   // of 4 rows, the smallest tiles
 long long sma_paged_max_tiles() { return kCap; }
 
 cudaError_t launch_sma_paged(const SmaPagedArgs& a, dart_dtype dt, cudaStream_t st) {
-    return dt == DART_F32 ? run_type<float>(a, st) : run_type<__nv_bfloat16>(a, st);
+    if (a.P == 64 && (a.cache.mxfp4 || dt == DART_BF16)) return launch_sma_paged_mma(a, dt, st);
+    if (a.N == 128 && a.P == 64 && dt == DART_F32) return run<float, 128, 64>(a, st);
+    if (a.N == 64 && a.P == 64 && dt == DART_F32) return run<float, 64, 64>(a, st);
+    if (a.N == 16 && a.P == 16) return dt == DART_F32 ? run<float, 16, 16>(a, st) : run<__nv_bfloat16, 16, 16>(a, st);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace dart

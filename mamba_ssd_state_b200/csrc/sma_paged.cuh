@@ -27,6 +27,13 @@ struct PieceHeader {
 };
 constexpr int kMaxBlocks = 512;   // persistent blocks of any of the kernels, and header slots
 
+// Joins the pieces that the blocks of a kernel with tiles of tt rows left.
+cudaError_t launch_sma_paged_combine(const SmaPagedArgs& a, int blocks, int tt, cudaStream_t st);
+// sma_paged_mma.cu: bfloat16 and 4-bit memories with P = 64, runs of few tokens.
+cudaError_t launch_sma_paged_mma(const SmaPagedArgs& a, dart_dtype dt, cudaStream_t st);
+// Multiprocessors of the current device, looked up once; 0 on failure.
+int paged_sm_count();
+
 #ifdef __CUDACC__
 
 // Tiles of the batch in shared memory: tile k covers rows t0[k] .. of sequence
@@ -189,6 +196,45 @@ __device__ __forceinline__ int first_bad_memory(const int* table, const PagedCac
         if (m) return min(count, (k + __ffs(m) - 1) * c.R);
     }
     return count;
+}
+
+// The end of a piece: each of WARPS warps has left its running maximum, sum and
+// weighted values per token; `threads` threads (this one is tid) join them and
+// write the rows of a whole item, or keep the piece for the combine kernel.
+// The caller orders this after the warps' stores and before the next ones.
+// vscale: what the stored values are to be multiplied by, per token.
+template <int WARPS, int TT, int P, int OS>
+__device__ __forceinline__ void finish_piece(const SmaPagedArgs& a, const Walk& w, int t0, int rows, const int* count, int bad,
+                                             const float (&m)[WARPS][TT], const float (&l)[WARPS][TT],
+                                             const float (&o)[WARPS][TT][OS], const float* vscale, int tid, int threads) {
+    const bool whole = w.last - w.first == w.units;
+    const int which = w.first > 0 ? 0 : 1;
+    if (!whole && tid == 0)
+        *piece_header(a.part, blockIdx.x, which) = PieceHeader{w.last == w.units ? 2 : 1, t0, rows, w.h};
+    for (int i = tid; i < rows * P; i += threads) {
+        const int t = i / P, p = i % P;
+        float mm = -INFINITY, ll = 0.f, oo = 0.f;
+#pragma unroll
+        for (int k = 0; k < WARPS; ++k) mm = fmaxf(mm, m[k][t]);
+#pragma unroll
+        for (int k = 0; k < WARPS; ++k) {
+            const float f = l[k][t] == 0.f ? 0.f : exp2f(m[k][t] - mm);
+            ll = fmaf(l[k][t], f, ll);
+            if (f != 0.f) oo = fmaf(o[k][t][p], f, oo);
+        }
+        if (vscale) oo *= vscale[t];
+        const bool left = count[t] < 0 || count[t] > bad;   // a row that is not to be computed
+        if (whole) {
+            if (left) continue;
+            const size_t at = ((size_t)(t0 + t) * a.H + w.h) * P + p;
+            const float r = ll == 0.f ? 0.f : oo / ll;
+            a.out[at] = a.y_ssd ? fmaf(a.g, r, a.y_ssd[at]) : r;
+        } else {
+            float* row = piece_rows<TT, P>(a.part, blockIdx.x, which) + t * (2 + P);
+            if (p == 0) { row[0] = mm; row[1] = left ? -1.f : ll; }
+            row[2 + p] = oo;
+        }
+    }
 }
 
 #endif

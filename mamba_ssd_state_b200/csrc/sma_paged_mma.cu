@@ -1,0 +1,443 @@
+// sma_paged_mma.cu -- state-memory attention of runs of few tokens over paged
+// memories, bfloat16 or 4-bit, P = 64.
+//
+// For up to 8 tokens t of one (sequence, head) and every visible memory M (N x P):
+//   U = M^T [Q_t ...] (P x tokens),  V = M^T [C_t ...],  s_t = U_t . E_t / sqrt(N),
+//   online softmax over the memories, o_t = sum w_t V_t.
+// A memory is read once for all tokens of the tile, so the kernel is bound by
+// HBM as long as the products keep up: 4 N P a token do on tensor cores and do
+// not on CUDA cores (8 tokens: 262 thousand multiply-adds a memory of 16 KB).
+// The products are small (M = P, N = 8 columns), which is the shape of the
+// warp-level m16n8k16; a 128-row tile of tcgen05 would be 1/16 full.
+//
+// Roles: one warp copies memories into a ring of stages in shared memory (one
+// memory a stage: a 128-byte-swizzled tile by TMA, or codes and scales by two
+// bulk copies); eight warps take the memories in turn.  The copies run ahead
+// over the ends of items, and the warps of a block meet only there.
+//
+// M^T is the A operand: bfloat16 through ldmatrix.trans; codes become float16
+// in registers (E2M1 values are exact there), laid out in memory so that a lane
+// finds the codes of its fragments in its own 16 bytes of a column.  The columns
+// of B are tokens: with up to 4 tokens one tile of 8 columns holds Q and C, else
+// one tile each.  float16 operands hold Q and C scaled by a power of two per
+// token, so that nothing is lost but what lies 2^-29 below a row's largest value;
+// float32 inputs are split into a high and a low float16 half (22 bits).
+// A block of 32 codes is two k steps: their product is multiplied by the block's
+// scale in float32 before it is added, so a scale costs 4 multiply-adds for
+// every 2 products and no bit.
+#include <cuda_fp16.h>
+#include <string.h>
+
+#include "sm100.cuh"
+#include "sma_paged.cuh"
+#include "tensor_map.h"
+
+namespace dart {
+namespace {
+
+using namespace sm100;
+
+constexpr int kP = 64;
+constexpr int kWarps = 8;                       // warps that multiply
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kCap = 4096;                      // tiles of a call
+constexpr int kLeast = 4;                       // units below which a run is not cut
+constexpr int kOS = kP + 4;                     // row of the warps' values: lanes of a store hit all banks
+
+// What a memory is kept as.
+template <int N> struct Bf16Mem {
+    static constexpr bool kFp4 = false;
+    static constexpr uint32_t kBytes = N * kP * 2, kStageBytes = kBytes;
+    static constexpr int kStages = 8 * 128 / N;   // 128 KB in flight
+};
+template <int N> struct Fp4Mem {
+    static constexpr bool kFp4 = true;
+    static constexpr uint32_t kCodeBytes = N * kP / 2, kScaleBytes = N * kP / 32;
+    static constexpr uint32_t kBytes = kCodeBytes + kScaleBytes, kStageBytes = kBytes;
+    static constexpr int kStages = 32;            // 136 KB at N = 128
+};
+
+// A stage is always taken by the same warp, so that its fills are waited for in
+// their order (a wait by parity tells a phase from its neighbours only).
+template <typename M, int TT>
+struct Smem {
+    static_assert(M::kStages % kWarps == 0, "stages are dealt to the warps in turn");
+    uint8_t ring[M::kStages * M::kStageBytes];    // first: tiles are 1024-byte aligned
+    float o[kWarps][TT][kOS];
+    float m[kWarps][TT], l[kWarps][TT];
+    float qscale[TT], vscale[TT];
+    uint64_t bars[2 * M::kStages];                // full, then empty
+    int abort_flag;
+    TileList<kCap> tiles;
+};
+
+struct Params {
+    CUtensorMap map;      // bfloat16 memories: (P, rows of N), boxes of one memory
+    SmaPagedArgs a;
+};
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// The four bytes of w, two codes each, as pairs of float16.
+__device__ __forceinline__ void widen_codes(uint32_t w, uint32_t (&r)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A lane's columns of B: PARTS float16 halves (or bfloat16 as it is) of N / 16
+// k steps.  Slots 2q, 2q+1, 2q+8, 2q+9 of k step i stand for rows
+// 16i + 4q + {0,1,2,3} with codes, and for 16i + {2q, 2q+1, 2q+8, 2q+9} else
+// (there the rows of a ldmatrix are eight neighbours, in eight different banks).
+template <typename M, int N, int PARTS>
+struct Column {
+    uint32_t b[PARTS][N / 16][2];
+
+    // src: the row of Q or C, nullptr for an unused column.  Returns the power of
+    // two that the column was multiplied by (its lanes are those of equal lane / 4).
+    template <typename T>
+    __device__ __forceinline__ float load(const T* src) {
+        const int q = threadIdx.x & 3;
+        float amax = 0.f;
+        float f[N / 16][4];
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int n = M::kFp4 ? 16 * i + 4 * q + j : 16 * i + 2 * q + (j & 1) + 8 * (j >> 1);
+                f[i][j] = src ? ldf(src + n) : 0.f;
+                amax = fmaxf(amax, fabsf(f[i][j]));
+            }
+        float scale = 1.f;
+        if constexpr (M::kFp4) {
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // largest value to [2^14, 2^15); a row that is not finite stays as it is
+            const int e = (int)(__float_as_uint(amax) >> 23);      // biased exponent, 0 for 0 and subnormals
+            if (amax > 0.f && e < 255) scale = mxfp4_pow2(min(max(14 - (e - 127), -126), 126));
+        }
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) {
+            if constexpr (M::kFp4) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float u = f[i][2 * j] * scale, v = f[i][2 * j + 1] * scale;
+                    b[0][i][j] = pack_half(u, v);
+                    if constexpr (PARTS == 2) {
+                        const __half2 h = *reinterpret_cast<const __half2*>(&b[0][i][j]);
+                        b[1][i][j] = pack_half(u - __low2float(h), v - __high2float(h));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(f[i][2 * j], f[i][2 * j + 1]);   // exact: it was bfloat16
+                    b[0][i][j] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+            }
+        }
+        return scale;
+    }
+};
+
+// acc[t][m] += (memory in `stage`)^T times the columns.  Returns whether the
+// memory is free of NaN blocks (bfloat16 carries its own).
+template <typename M, int N, int NT, int PARTS>
+__device__ __forceinline__ bool multiply(const uint8_t* stage, const Column<M, N, PARTS> (&col)[NT], float (&acc)[NT][4][4]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[t][m][r] = 0.f;
+    if constexpr (!M::kFp4) {
+        const int mi = lane >> 3, r = lane & 7;
+        const uint32_t base = smem_u32(stage) + (uint32_t)((mi >> 1) * 8 + r) * 128u;
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                uint32_t a[4];
+                ldmatrix_x4_trans(base + (uint32_t)i * 2048u + (uint32_t)(((2 * m + (mi & 1)) ^ r) << 4), a);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma_bf16(acc[t][m], a, col[t].b[0][i]);
+            }
+        }
+        return true;
+    } else {
+        constexpr int K = N / 32;
+        const int g = lane >> 2, q = lane & 3;
+        const uint8_t* scales = stage + M::kCodeBytes;
+        uint32_t nan = 0;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int p = 16 * m + g;
+            uint32_t lo[K], hi[K], slo, shi;
+            if constexpr (K == 4) {
+                const uint4 u = *reinterpret_cast<const uint4*>(stage + p * (N / 2) + q * 16);
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + (p + 8) * (N / 2) + q * 16);
+                lo[0] = u.x; lo[1] = u.y; lo[2] = u.z; lo[3] = u.w;
+                hi[0] = v.x; hi[1] = v.y; hi[2] = v.z; hi[3] = v.w;
+                slo = *reinterpret_cast<const uint32_t*>(scales + p * 4);
+                shi = *reinterpret_cast<const uint32_t*>(scales + (p + 8) * 4);
+            } else {
+                const uint2 u = *reinterpret_cast<const uint2*>(stage + p * (N / 2) + q * 8);
+                const uint2 v = *reinterpret_cast<const uint2*>(stage + (p + 8) * (N / 2) + q * 8);
+                lo[0] = u.x; lo[1] = u.y;
+                hi[0] = v.x; hi[1] = v.y;
+                slo = *reinterpret_cast<const uint16_t*>(scales + p * 2);
+                shi = *reinterpret_cast<const uint16_t*>(scales + (p + 8) * 2);
+            }
+            nan |= __vcmpeq4(slo, 0xffffffffu) | __vcmpeq4(shi, 0xffffffffu);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                uint32_t ra[4], rb[4];
+                widen_codes(lo[k], ra);
+                widen_codes(hi[k], rb);
+                const uint32_t a0[4] = {ra[0], rb[0], ra[1], rb[1]}, a1[4] = {ra[2], rb[2], ra[3], rb[3]};
+                // 2^(s - 127) of the two rows (2^-127 counts as 0)
+                const float s0 = __uint_as_float((k < 3 ? slo << (23 - 8 * k) : slo >> 1) & 0x7f800000u);
+                const float s1 = __uint_as_float((k < 3 ? shi << (23 - 8 * k) : shi >> 1) & 0x7f800000u);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int h = 0; h < PARTS; ++h) {
+                        mma_f16(d, a0, col[t].b[h][2 * k]);
+                        mma_f16(d, a1, col[t].b[h][2 * k + 1]);
+                    }
+                    acc[t][m][0] = fmaf(d[0], s0, acc[t][m][0]);
+                    acc[t][m][1] = fmaf(d[1], s0, acc[t][m][1]);
+                    acc[t][m][2] = fmaf(d[2], s1, acc[t][m][2]);
+                    acc[t][m][3] = fmaf(d[3], s1, acc[t][m][3]);
+                }
+            }
+        }
+        return !__any_sync(0xffffffffu, nan != 0);
+    }
+}
+
+// One warp's memories of a piece.  NT = 1: columns 0-3 of the tile are Q and 4-7
+// C of up to 4 tokens; NT = 2: a tile each of up to 8.  it: number of the
+// piece's first memory in this block's order.
+template <typename T, typename M, int N, int TT, int NT, int PARTS>
+__device__ __forceinline__ void run_piece(const SmaPagedArgs& a, Smem<M, TT>& s, const Walk& w, int t0, int rows, int bad, int it,
+                                          const WaitCtx& wc, bool& ok) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    const int grp = group_of(w.h, a.H, a.G);
+    const T *Q = static_cast<const T*>(a.Q), *C = static_cast<const T*>(a.Cm), *E = static_cast<const T*>(a.E);
+    auto q_row = [&](int t) { return t < rows ? Q + ((size_t)(t0 + t) * a.H + w.h) * N : nullptr; };
+    auto c_row = [&](int t) { return t < rows ? C + ((size_t)(t0 + t) * a.G + grp) * N : nullptr; };
+    Column<M, N, PARTS> col[NT];
+    // this lane's two tokens, as columns of the results
+    const int tk = NT == 2 ? 2 * q : 2 * (q & 1);
+    float qs[2];
+    if constexpr (NT == 2) {
+        const float sq = col[0].load(q_row(g)), sv = col[1].load(c_row(g));
+        if (warp == 0 && q == 0) s.vscale[g] = 1.f / sv;
+        qs[0] = 1.f / __shfl_sync(0xffffffffu, sq, 4 * tk);
+        qs[1] = 1.f / __shfl_sync(0xffffffffu, sq, 4 * tk + 4);
+    } else {
+        const float sc = col[0].load(g < 4 ? q_row(g) : c_row(g - 4));
+        if (warp == 0 && q == 0 && g >= 4) s.vscale[g - 4] = 1.f / sc;
+        qs[0] = 1.f / __shfl_sync(0xffffffffu, sc, 4 * tk);
+        qs[1] = 1.f / __shfl_sync(0xffffffffu, sc, 4 * tk + 4);
+    }
+    const float sscale = kLog2e * rsqrtf((float)N);
+    float e[4][4];        // E of (token, column) as the results are laid out
+    int count[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        qs[j] *= sscale;
+        count[j] = tk + j < rows ? a.mem_count[t0 + tk + j] : 0;
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                e[m][2 * r + j] = tk + j < rows && (NT == 2 || q < 2)
+                                      ? ldf(E + ((size_t)(t0 + tk + j) * a.H + w.h) * kP + 16 * m + g + 8 * r) : 0.f;
+    }
+    float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[4][4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[m][r] = 0.f;
+
+    const int n = min(w.last, bad) - w.first;
+    for (int i = (warp - it % kWarps + kWarps) % kWarps; i < n; i += kWarps) {
+        const int st = (it + i) % M::kStages;
+        const uint32_t ph = (uint32_t)((it + i) / M::kStages) & 1u;
+        if (ok) ok = mbar_wait_warp(smem_u32(&s.bars[st]), ph, wc, 2);
+        if (!ok) continue;
+        float acc[NT][4][4];
+        const bool clean = multiply<M, N, NT, PARTS>(s.ring + (size_t)st * M::kStageBytes, col, acc);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.bars[M::kStages + st]));
+        const int c = w.first + i;
+        float sc[2], f[2], wt[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float v = 0.f;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) v = fmaf(acc[0][m][j], e[m][j], fmaf(acc[0][m][2 + j], e[m][2 + j], v));
+            v += __shfl_xor_sync(0xffffffffu, v, 4);
+            v += __shfl_xor_sync(0xffffffffu, v, 8);
+            v += __shfl_xor_sync(0xffffffffu, v, 16);
+            if (NT == 1) v = __shfl_sync(0xffffffffu, v, lane & ~2);   // the C columns take the scores of the Q columns
+            sc[j] = clean ? v * qs[j] : __int_as_float(0x7fffffff);
+            if (c >= count[j]) sc[j] = -INFINITY;
+            const float mn = fmaxf(mx[j], sc[j]);
+            const bool none = mn == -INFINITY;      // nothing seen yet, or only scores of -inf: they weigh nothing
+            f[j] = none ? 1.f : exp2f(mx[j] - mn);
+            wt[j] = none ? (sc[j] == sc[j] ? 0.f : sc[j]) : exp2f(sc[j] - mn);
+            l[j] = fmaf(l[j], f[j], wt[j]);
+            mx[j] = mn;
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int j = r & 1;
+                // 0 weight reads nothing, whatever the value is
+                const float v = wt[j] != 0.f ? wt[j] * acc[NT - 1][m][r] : 0.f;
+                o[m][r] = fmaf(o[m][r], f[j], v);
+            }
+    }
+    if (NT == 2 || q >= 2) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int t = tk + j;
+            if (t < TT) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    s.o[warp][t][16 * m + g] = o[m][j];
+                    s.o[warp][t][16 * m + g + 8] = o[m][2 + j];
+                }
+                if (g == 0) { s.m[warp][t] = mx[j]; s.l[warp][t] = l[j]; }
+            }
+        }
+    }
+}
+
+template <typename T, typename M, int N, int TT, int PARTS>
+__global__ void __launch_bounds__(kThreads, 1) sma_paged_mma_kernel(const __grid_constant__ Params prm) {
+    extern __shared__ uint8_t raw[];
+    Smem<M, TT>& s = *reinterpret_cast<Smem<M, TT>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const SmaPagedArgs& a = prm.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < 2 * M::kStages; ++i) mbar_init(smem_u32(&s.bars[i]), 1);
+        s.abort_flag = 0;
+        fence_mbar_init();
+    }
+    griddep_wait();
+    if (tid < 2) piece_header(a.part, blockIdx.x, tid)->state = 0;
+    build_tiles<TT, kCap>(a, s.tiles);
+    const WaitCtx wc{&s.abort_flag, a.status, 10};
+    const long long limit = (long long)a.cache.width * a.cache.R;
+    const int R = a.cache.R;
+    bool ok = true;
+    int it = 0;           // memories of the pieces before this one
+    int issued = 0;       // copies started
+    if (s.tiles.n > 0)
+        for (Walk w = start_walk(s.tiles, a.H, kLeast); next_piece(w); advance(s.tiles, w, a.H)) {
+            const int b = s.tiles.seq[w.k], t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, b, t0, TT);
+            const int* table = a.cache.table + (size_t)b * a.cache.width;
+            int seen = lane < rows ? usable_count(a.mem_count[t0 + lane], limit) : 0;
+            seen = __reduce_max_sync(0xffffffffu, seen);
+            const int bad = first_bad_memory(table, a.cache, seen);
+            const int n = max(0, min(w.last, bad) - w.first);
+            if (warp == kWarps) {
+                // ---- copies
+                if (bad < seen && lane == 0) flag_status(a.status, kStatusDevice);
+                for (int i = 0; i < n && ok; ++i) {
+                    const int c = w.first + i, st = (it + i) % M::kStages;
+                    const uint32_t ph = (uint32_t)((it + i) / M::kStages) & 1u;
+                    ok = mbar_wait_warp(smem_u32(&s.bars[M::kStages + st]), ph ^ 1u, wc, 1);
+                    if (ok && lane == 0) {
+                        const size_t mem = memory_index(a.cache, a.H, table[c / R], w.h, c % R);
+                        const uint32_t full = smem_u32(&s.bars[st]), dst = smem_u32(s.ring + (size_t)st * M::kStageBytes);
+                        issued = it + i + 1;
+                        mbar_expect_tx(full, M::kBytes);
+                        if constexpr (M::kFp4) {
+                            bulk_load(dst, static_cast<const uint8_t*>(a.cache.pages) + mem * M::kCodeBytes, M::kCodeBytes, full);
+                            bulk_load(dst + M::kCodeBytes, a.cache.scales + mem * M::kScaleBytes, M::kScaleBytes, full);
+                        } else {
+                            tma_load_2d(dst, &prm.map, full, 0, (int)(mem * N));
+                        }
+                    }
+                }
+                __syncwarp();
+            } else {
+                if (TT == 8 && rows > 4) {
+                    if constexpr (TT == 8) run_piece<T, M, N, TT, 2, PARTS>(a, s, w, t0, rows, bad, it, wc, ok);
+                } else {
+                    run_piece<T, M, N, TT, 1, PARTS>(a, s, w, t0, rows, bad, it, wc, ok);
+                }
+                named_bar_sync(1, 32 * kWarps);
+                finish_piece<kWarps, TT, kP, kOS>(a, w, t0, rows, a.mem_count + t0, bad, s.m, s.l, s.o, s.vscale, tid, 32 * kWarps);
+                named_bar_sync(1, 32 * kWarps);
+            }
+            it += n;
+        }
+    // Every copy has been waited for by the warp that used it, unless a wait gave
+    // up: what is in flight then is waited for here, before its shared memory goes.
+    if (warp == kWarps && lane == 0 && !ok)
+        for (int i = max(0, issued - M::kStages); i < issued; ++i)
+            for (int k = 0; k < (1 << 20) && !mbar_try_wait(smem_u32(&s.bars[i % M::kStages]), (uint32_t)(i / M::kStages) & 1u); ++k) {}
+    __syncthreads();
+}
+
+template <typename T, typename M, int N, int TT, int PARTS>
+cudaError_t run(const SmaPagedArgs& a, cudaStream_t st) {
+    auto kern = sma_paged_mma_kernel<T, M, N, TT, PARTS>;
+    const int smem = (int)sizeof(Smem<M, TT>) + 1024, sms = paged_sm_count();
+    static_assert(sizeof(Smem<M, TT>) + 1024 <= 232448, "shared memory");
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    Params prm;
+    memset(&prm.map, 0, sizeof(prm.map));
+    prm.a = a;
+    if constexpr (!M::kFp4) {
+        const uint64_t rows = (uint64_t)a.cache.npages * a.H * a.cache.R * N;
+        if (rows > 0x7fffffffull) return cudaErrorInvalidValue;      // 256 GB and more of N = 128 memories
+        const uint64_t dims[2] = {kP, rows}, strides[1] = {kP * 2};
+        const uint32_t box[2] = {kP, N};
+        if (!encode_tile_map_bf16(&prm.map, 2, a.cache.pages, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int blocks = min(sms, kMaxBlocks);
+    if ((e = launch_dependent(kern, dim3(blocks), dim3(kThreads), smem, st, 1, prm)) != cudaSuccess) return e;
+    count_launches(1);
+    return launch_sma_paged_combine(a, blocks, TT, st);
+}
+
+}  // namespace
+
+cudaError_t launch_sma_paged_mma(const SmaPagedArgs& a, dart_dtype dt, cudaStream_t st) {
+    if (a.cache.mxfp4) {
+        if (dt == DART_F32) return a.N == 128 ? run<float, Fp4Mem<128>, 128, 4, 2>(a, st) : run<float, Fp4Mem<64>, 64, 4, 2>(a, st);
+        return a.N == 128 ? run<__nv_bfloat16, Fp4Mem<128>, 128, 8, 1>(a, st) : run<__nv_bfloat16, Fp4Mem<64>, 64, 8, 1>(a, st);
+    }
+    return a.N == 128 ? run<__nv_bfloat16, Bf16Mem<128>, 128, 8, 1>(a, st) : run<__nv_bfloat16, Bf16Mem<64>, 64, 8, 1>(a, st);
+}
+
+}  // namespace dart
