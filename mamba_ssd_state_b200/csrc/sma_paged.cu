@@ -65,8 +65,8 @@ __device__ __forceinline__ void run_piece(const SmaPagedArgs& a, Smem<N, P>& s, 
     float2 o[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) { m[t] = -INFINITY; l[t] = 0.f; o[t] = make_float2(0.f, 0.f); }
-    const int last = min(w.last, s.bad);
-    for (int c = w.first + warp; c < last; c += kWarps) {
+    const int last = min(w.last_memory(), s.bad);
+    for (int c = w.first_memory() + warp; c < last; c += kWarps) {
         R rows(a.cache, memory_index(a.cache, a.H, table[c / a.cache.R], w.h, c % a.cache.R), lane);
         float2 u[NT], v[NT];
 #pragma unroll
@@ -123,10 +123,9 @@ __global__ void __launch_bounds__(kThreads) sma_paged_kernel(SmaPagedArgs a) {
     build_tiles<kTT, kCap>(a, s.tiles);
     if (tid < 2) piece_header(a.part, blockIdx.x, tid)->state = 0;
     if (s.tiles.n == 0) return;
-    const long long limit = (long long)a.cache.width * a.cache.R;
     const float qscale = kLog2e * rsqrtf((float)N);
     __syncthreads();
-    for (Walk w = start_walk(s.tiles, a.H, kLeast); next_piece(w); advance(s.tiles, w, a.H)) {
+    for (Walk w = start_walk(s.tiles, a.H, blockIdx.x, gridDim.x, kLeast); next_piece(w); advance(s.tiles, w, a.H)) {
         const int b = s.tiles.seq[w.k], t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, b, t0, kTT);
         const int* table = a.cache.table + (size_t)b * a.cache.width;
         __syncthreads();
@@ -139,11 +138,8 @@ __global__ void __launch_bounds__(kThreads) sma_paged_kernel(SmaPagedArgs a) {
         }
         if (tid < kTT) s.count[tid] = tid < rows ? a.mem_count[t0 + tid] : -1;
         if (tid < 32) {
-            const int most = s.tiles.pre[w.k + 1] - s.tiles.pre[w.k];
-            // a tile with nothing to read has one unit and no page
-            int seen = 0;
-            for (int r = 0; r < rows; ++r) seen = max(seen, usable_count(a.mem_count[t0 + r], limit));
-            const int bad = first_bad_memory(table, a.cache, min(most, seen));
+            const int seen = w.units - 1;      // the most that a row of the tile sees
+            const int bad = first_bad_memory(table, a.cache, seen);
             if (lane == 0) {
                 s.bad = bad;
                 if (bad < seen) flag_status(a.status, kStatusDevice);
@@ -163,24 +159,50 @@ __global__ void __launch_bounds__(kThreads) sma_paged_kernel(SmaPagedArgs a) {
         else if (rows <= 4) run_piece<T, N, P, 4>(a, s, w, table, e);
         else run_piece<T, N, P, 8>(a, s, w, table, e);
         __syncthreads();
-        finish_piece<kWarps, kTT, P, P>(a, w, t0, rows, s.count, s.bad, s.m, s.l, s.o, nullptr, tid, kThreads);
+        // join the warps: a whole item is written out, a part of one kept for the combine kernel
+        const int which = w.c > 0 ? 0 : 1;
+        if (!w.whole() && tid == 0)
+            *piece_header(a.part, blockIdx.x, which) = PieceHeader{w.last == w.units ? 2 : 1, t0, rows, w.h};
+        for (int i = tid; i < rows * P; i += kThreads) {
+            const int t = i / P, p = i % P;
+            float mm = -INFINITY, l = 0.f, o = 0.f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, s.m[k][t]);
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                const float f = s.l[k][t] == 0.f ? 0.f : exp2f(s.m[k][t] - mm);
+                l = fmaf(s.l[k][t], f, l);
+                if (f != 0.f) o = fmaf(s.o[k][t][p], f, o);
+            }
+            const bool left = s.count[t] < 0 || s.count[t] > s.bad;   // a row that is not to be computed
+            if (w.whole()) {
+                if (left) continue;
+                const size_t at = ((size_t)(t0 + t) * a.H + w.h) * P + p;
+                const float r = l == 0.f ? 0.f : o / l;
+                a.out[at] = a.y_ssd ? fmaf(a.g, r, a.y_ssd[at]) : r;
+            } else {
+                float* row = piece_rows<kTT, P>(a.part, blockIdx.x, which) + t * (2 + P);
+                if (p == 0) { row[0] = mm; row[1] = left ? -1.f : l; }
+                row[2 + p] = o;
+            }
+        }
     }
 }
 
-// Block i joins the item that begins in block i's run and ends in a later one's.
+// Block i joins the item that begins in run i and ends in a later one.
 template <int TT, int P>
-__global__ void __launch_bounds__(256) sma_paged_combine_kernel(SmaPagedArgs a, int blocks) {
+__global__ void __launch_bounds__(128) sma_paged_combine_kernel(SmaPagedArgs a, int runs) {
     sm100::griddep_wait();
     const PieceHeader hd = *piece_header(a.part, blockIdx.x, 1);
     if (hd.state != 1) return;
-    int end = blockIdx.x + 1;                 // the block that has the item's last piece
-    while (end < blocks && piece_header(a.part, end, 0)->state != 2) ++end;
+    int end = blockIdx.x + 1;                 // the run that has the item's last piece
+    while (end < runs && piece_header(a.part, end, 0)->state != 2) ++end;
     for (int i = threadIdx.x; i < hd.rows * P; i += blockDim.x) {
         const int t = i / P, p = i % P;
         const float* row = piece_rows<TT, P>(a.part, blockIdx.x, 1) + t * (2 + P);
         float m = row[0], l = row[1], o = row[2 + p];
         if (l < 0.f) continue;
-        for (int j = blockIdx.x + 1; j <= end && j < blocks; ++j) {
+        for (int j = blockIdx.x + 1; j <= end && j < runs; ++j) {
             if (piece_header(a.part, j, 0)->state == 0) continue;
             const float* r = piece_rows<TT, P>(a.part, j, 0) + t * (2 + P);
             if (r[1] == 0.f) continue;        // saw nothing
@@ -203,7 +225,7 @@ cudaError_t run(const SmaPagedArgs& a, cudaStream_t st) {
     if (sms <= 0) return cudaErrorInvalidDevice;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int blocks = min(2 * sms, kMaxBlocks);
+    const int blocks = min(2 * sms, kMaxRuns);
     kern<<<blocks, kThreads, smem, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     count_launches(1);
@@ -224,19 +246,19 @@ int paged_sm_count() {
     return n;
 }
 
-cudaError_t launch_sma_paged_combine(const SmaPagedArgs& a, int blocks, int tt, cudaStream_t st) {
+cudaError_t launch_sma_paged_combine(const SmaPagedArgs& a, int runs, int tt, cudaStream_t st) {
     cudaError_t e;
     if (a.P == 64)
-        e = tt == 8 ? launch_dependent(sma_paged_combine_kernel<8, 64>, dim3(blocks), dim3(256), 0, st, 1, a, blocks)
-                    : launch_dependent(sma_paged_combine_kernel<4, 64>, dim3(blocks), dim3(256), 0, st, 1, a, blocks);
+        e = tt == 8 ? launch_dependent(sma_paged_combine_kernel<8, 64>, dim3(runs), dim3(128), 0, st, 1, a, runs)
+                    : launch_dependent(sma_paged_combine_kernel<4, 64>, dim3(runs), dim3(128), 0, st, 1, a, runs);
     else
-        e = launch_dependent(sma_paged_combine_kernel<8, 16>, dim3(blocks), dim3(256), 0, st, 1, a, blocks);
+        e = launch_dependent(sma_paged_combine_kernel<8, 16>, dim3(runs), dim3(128), 0, st, 1, a, runs);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
 
 size_t sma_paged_workspace_bytes(int P) {
-    return 2 * (size_t)kMaxBlocks * (sizeof(PieceHeader) + sizeof(float) * kTT * (2 + (size_t)P));
+    return 2 * (size_t)kMaxRuns * (sizeof(PieceHeader) + sizeof(float) * kTT * (2 + (size_t)P));
 }
 long long sma_paged_tiles(int B, int T) { return B + (long long)T / 4; }   // of 4 rows, the smallest tiles
 long long sma_paged_max_tiles() { return kCap; }

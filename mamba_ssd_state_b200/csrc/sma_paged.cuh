@@ -1,13 +1,14 @@
 // sma_paged.cuh -- how the paged attention kernels divide their work.
 //
-// The packed tokens of a sequence are cut into tiles of TT rows.  A tile reads,
-// for every head, the memories its rows may see (up to the largest count among
-// them): (tile, head, memory) in that order is one long list of equal units,
-// and block i of G takes the i-th of G equal runs of it, whatever the batch
-// looks like.  An item, (tile, head), whose memories fall into several runs
-// leaves one partial result (running maximum, sum, weighted values) per block
-// in the workspace; a block has at most two such pieces, the one its run
-// begins with and the one it ends with.  sma_paged_combine joins them in order.
+// The packed tokens of a sequence are cut into tiles of TT rows.  An item is a
+// tile and a head; it reads the memories its rows may see (up to the largest
+// count among them), one unit each, and one unit stands for the item itself.
+// The units in the order (tile, head, memory) are cut into equal runs, one for
+// every worker (a block, or a warp), whatever the batch looks like.  An item
+// that falls into several runs leaves one partial result (running maximum, sum,
+// weighted values) per run in the workspace; a run has at most two such pieces,
+// the one it begins with and the one it ends with.  sma_paged_combine joins
+// them in order.
 //
 // Every block computes the list itself from cu_tokens and mem_count (they live
 // on the device), which costs less than a launch of its own would.
@@ -17,18 +18,18 @@
 
 namespace dart {
 
-// Workspace: per block kPieceInts ints of header for its first and its last
-// piece, then the pieces, rows of 2 + P floats.
+// Workspace: per run a header for its first and its last piece, then the pieces,
+// rows of 2 + P floats.
 struct PieceHeader {
     int state;    // 0: no such piece, 1: more pieces follow, 2: the item ends here
     int t0;       // first token row of the tile
     int rows;
     int h;
 };
-constexpr int kMaxBlocks = 512;   // persistent blocks of any of the kernels, and header slots
+constexpr int kMaxRuns = 2048;   // runs of any of the kernels
 
-// Joins the pieces that the blocks of a kernel with tiles of tt rows left.
-cudaError_t launch_sma_paged_combine(const SmaPagedArgs& a, int blocks, int tt, cudaStream_t st);
+// Joins the pieces that the runs of a kernel with tiles of tt rows left.
+cudaError_t launch_sma_paged_combine(const SmaPagedArgs& a, int runs, int tt, cudaStream_t st);
 // sma_paged_mma.cu: bfloat16 and 4-bit memories with P = 64, runs of few tokens.
 cudaError_t launch_sma_paged_mma(const SmaPagedArgs& a, dart_dtype dt, cudaStream_t st);
 // Multiprocessors of the current device, looked up once; 0 on failure.
@@ -37,7 +38,7 @@ int paged_sm_count();
 #ifdef __CUDACC__
 
 // Tiles of the batch in shared memory: tile k covers rows t0[k] .. of sequence
-// seq[k] and has pre[k+1] - pre[k] >= 1 units a head (1 with nothing to read).
+// seq[k] and has pre[k+1] - pre[k] units a head, 1 + the memories it reads.
 template <int CAP>
 struct TileList {
     int pre[CAP + 1];
@@ -112,7 +113,7 @@ __device__ __forceinline__ void build_tiles(const SmaPagedArgs& a, TileList<CAP>
                 bad |= c < -1 || c > limit;
                 most = max(most, usable_count(c, limit));
             }
-            most = max(most, 1);
+            ++most;
         }
         int total;
         const int at = sum + block_scan(most, L.scan, total);
@@ -124,21 +125,23 @@ __device__ __forceinline__ void build_tiles(const SmaPagedArgs& a, TileList<CAP>
     __syncthreads();
 }
 
-// This block's run of units, and the walk over its pieces.
+// A run of units, and the walk over its pieces.
 struct Walk {
     long long u, end;    // next unit, end of the run
-    int k, h, c;         // tile, head, memory of unit u
-    int first, last;     // memories of the piece: [first, last)
+    int k, h, c;         // tile, head, unit of the item at u
     int units;           // units of the item
+    int last;            // the piece: units [c, last) of the item
+    __device__ __forceinline__ int first_memory() const { return max(c - 1, 0); }
+    __device__ __forceinline__ int last_memory() const { return last - 1; }
+    __device__ __forceinline__ bool whole() const { return last - c == units; }
 };
 
-// Runs of fewer than `least` units are not cut smaller.
+// Run i of G; runs of fewer than `least` units are not cut smaller.
 template <int CAP>
-__device__ __forceinline__ Walk start_walk(const TileList<CAP>& L, int H, int least) {
+__device__ __forceinline__ Walk start_walk(const TileList<CAP>& L, int H, int i, int runs, int least) {
     Walk w;
     const long long W = (long long)L.pre[L.n] * H;
-    const long long G = min((long long)gridDim.x, (W + least - 1) / least);
-    const long long i = blockIdx.x;
+    const long long G = min((long long)runs, (W + least - 1) / least);
     w.u = i < G ? W * i / G : W;
     w.end = i < G ? W * (i + 1) / G : W;
     int lo = 0, hi = L.n - 1;              // the tile of unit u
@@ -160,13 +163,12 @@ __device__ __forceinline__ Walk start_walk(const TileList<CAP>& L, int H, int le
 // The next piece; false at the end of the run.
 __device__ __forceinline__ bool next_piece(Walk& w) {
     if (w.u >= w.end) return false;
-    w.first = w.c;
     w.last = (int)min((long long)w.units, w.c + (w.end - w.u));
     return true;
 }
 template <int CAP>
 __device__ __forceinline__ void advance(const TileList<CAP>& L, Walk& w, int H) {
-    w.u += w.last - w.first;
+    w.u += w.last - w.c;
     w.c = 0;
     if (++w.h == H) {
         w.h = 0;
@@ -175,15 +177,15 @@ __device__ __forceinline__ void advance(const TileList<CAP>& L, Walk& w, int H) 
     }
 }
 
-// Header and rows of a block's piece in the workspace: which = 0 for the piece
-// that its run begins with when the item began earlier, 1 for an item that
-// begins in the run and does not end there.
-__device__ __forceinline__ PieceHeader* piece_header(float* part, int block, int which) {
-    return reinterpret_cast<PieceHeader*>(part) + 2 * block + which;
+// Header and rows of a run's piece in the workspace: which = 0 for the piece
+// that it begins with when the item began earlier, 1 for an item that begins in
+// it and does not end there.
+__device__ __forceinline__ PieceHeader* piece_header(float* part, int run, int which) {
+    return reinterpret_cast<PieceHeader*>(part) + 2 * run + which;
 }
 template <int TT, int P>
-__device__ __forceinline__ float* piece_rows(float* part, int block, int which) {
-    return part + 2 * kMaxBlocks * (sizeof(PieceHeader) / sizeof(float)) + (size_t)(2 * block + which) * TT * (2 + P);
+__device__ __forceinline__ float* piece_rows(float* part, int run, int which) {
+    return part + 2 * kMaxRuns * (sizeof(PieceHeader) / sizeof(float)) + (size_t)(2 * run + which) * TT * (2 + P);
 }
 
 // First memory of sequence row `table` whose page is no page, among the first
@@ -196,45 +198,6 @@ __device__ __forceinline__ int first_bad_memory(const int* table, const PagedCac
         if (m) return min(count, (k + __ffs(m) - 1) * c.R);
     }
     return count;
-}
-
-// The end of a piece: each of WARPS warps has left its running maximum, sum and
-// weighted values per token; `threads` threads (this one is tid) join them and
-// write the rows of a whole item, or keep the piece for the combine kernel.
-// The caller orders this after the warps' stores and before the next ones.
-// vscale: what the stored values are to be multiplied by, per token.
-template <int WARPS, int TT, int P, int OS>
-__device__ __forceinline__ void finish_piece(const SmaPagedArgs& a, const Walk& w, int t0, int rows, const int* count, int bad,
-                                             const float (&m)[WARPS][TT], const float (&l)[WARPS][TT],
-                                             const float (&o)[WARPS][TT][OS], const float* vscale, int tid, int threads) {
-    const bool whole = w.last - w.first == w.units;
-    const int which = w.first > 0 ? 0 : 1;
-    if (!whole && tid == 0)
-        *piece_header(a.part, blockIdx.x, which) = PieceHeader{w.last == w.units ? 2 : 1, t0, rows, w.h};
-    for (int i = tid; i < rows * P; i += threads) {
-        const int t = i / P, p = i % P;
-        float mm = -INFINITY, ll = 0.f, oo = 0.f;
-#pragma unroll
-        for (int k = 0; k < WARPS; ++k) mm = fmaxf(mm, m[k][t]);
-#pragma unroll
-        for (int k = 0; k < WARPS; ++k) {
-            const float f = l[k][t] == 0.f ? 0.f : exp2f(m[k][t] - mm);
-            ll = fmaf(l[k][t], f, ll);
-            if (f != 0.f) oo = fmaf(o[k][t][p], f, oo);
-        }
-        if (vscale) oo *= vscale[t];
-        const bool left = count[t] < 0 || count[t] > bad;   // a row that is not to be computed
-        if (whole) {
-            if (left) continue;
-            const size_t at = ((size_t)(t0 + t) * a.H + w.h) * P + p;
-            const float r = ll == 0.f ? 0.f : oo / ll;
-            a.out[at] = a.y_ssd ? fmaf(a.g, r, a.y_ssd[at]) : r;
-        } else {
-            float* row = piece_rows<TT, P>(a.part, blockIdx.x, which) + t * (2 + P);
-            if (p == 0) { row[0] = mm; row[1] = left ? -1.f : ll; }
-            row[2 + p] = oo;
-        }
-    }
 }
 
 #endif

@@ -10,10 +10,12 @@
 // The products are small (M = P, N = 8 columns), which is the shape of the
 // warp-level m16n8k16; a 128-row tile of tcgen05 would be 1/16 full.
 //
-// Roles: one warp copies memories into a ring of stages in shared memory (one
-// memory a stage: a 128-byte-swizzled tile by TMA, or codes and scales by two
-// bulk copies); eight warps take the memories in turn.  The copies run ahead
-// over the ends of items, and the warps of a block meet only there.
+// Every warp is a worker of its own, with its run of units, its ring of stages in
+// shared memory and its softmax: it starts the copy that refills a stage as soon
+// as it has read it, running ahead of itself over the ends of items, and never
+// waits for another warp.  (With one copying warp and eight that shared the
+// pieces of a block, the joins and loads at the ends of items were what bound
+// short ones: 616 us where this takes 495 for 64 sequences of one token and 128 memories.)
 //
 // M^T is the A operand: bfloat16 through ldmatrix.trans; codes become float16
 // in registers (E2M1 values are exact there), laid out in memory so that a lane
@@ -38,38 +40,32 @@ namespace {
 using namespace sm100;
 
 constexpr int kP = 64;
-constexpr int kWarps = 8;                       // warps that multiply
-constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kCap = 4096;                      // tiles of a call
-constexpr int kLeast = 4;                       // units below which a run is not cut
-constexpr int kOS = kP + 4;                     // row of the warps' values: lanes of a store hit all banks
+constexpr int kLeast = 1;                       // units below which a run is not cut
 
-// What a memory is kept as.
+// What a memory is kept as, and the stages it passes through: kPieces of them.
 template <int N> struct Bf16Mem {
     static constexpr bool kFp4 = false;
-    static constexpr uint32_t kBytes = N * kP * 2, kStageBytes = kBytes;
-    static constexpr int kStages = 8 * 128 / N;   // 128 KB in flight
+    static constexpr int kWarps = 8, kStages = 2;             // 128 KB of copies in flight
+    static constexpr int kRows = 64, kPieces = N / kRows;     // rows of a stage
+    static constexpr uint32_t kStageBytes = kRows * kP * 2;
 };
 template <int N> struct Fp4Mem {
     static constexpr bool kFp4 = true;
+    static constexpr int kWarps = 8, kStages = 4, kPieces = 1;
     static constexpr uint32_t kCodeBytes = N * kP / 2, kScaleBytes = N * kP / 32;
-    static constexpr uint32_t kBytes = kCodeBytes + kScaleBytes, kStageBytes = kBytes;
-    static constexpr int kStages = 32;            // 136 KB at N = 128
+    static constexpr uint32_t kStageBytes = kCodeBytes + kScaleBytes;
 };
 
-// A stage is always taken by the same warp, so that its fills are waited for in
-// their order (a wait by parity tells a phase from its neighbours only).
-template <typename M, int TT>
+template <typename M>
 struct Smem {
-    static_assert(M::kStages % kWarps == 0, "stages are dealt to the warps in turn");
-    uint8_t ring[M::kStages * M::kStageBytes];    // first: tiles are 1024-byte aligned
-    float o[kWarps][TT][kOS];
-    float m[kWarps][TT], l[kWarps][TT];
-    float qscale[TT], vscale[TT];
-    uint64_t bars[2 * M::kStages];                // full, then empty
+    uint8_t ring[M::kWarps][M::kStages][M::kStageBytes];    // first: tiles are 1024-byte aligned
+    uint64_t full[M::kWarps][M::kStages];
     int abort_flag;
     TileList<kCap> tiles;
 };
+
+template <int I> struct Piece { static constexpr int value = I; };
 
 struct Params {
     CUtensorMap map;      // bfloat16 memories: (P, rows of N), boxes of one memory
@@ -89,6 +85,11 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], c
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
 }
 // The four bytes of w, two codes each, as pairs of float16.
 __device__ __forceinline__ void widen_codes(uint32_t w, uint32_t (&r)[4]) {
@@ -157,28 +158,22 @@ struct Column {
     }
 };
 
-// acc[t][m] += (memory in `stage`)^T times the columns.  Returns whether the
-// memory is free of NaN blocks (bfloat16 carries its own).
-template <typename M, int N, int NT, int PARTS>
+// acc[t][m] += (piece of a memory in `stage`)^T times the columns.  Returns
+// whether the memory is free of NaN blocks (bfloat16 carries its own).
+template <typename M, int N, int NT, int PARTS, int PIECE>
 __device__ __forceinline__ bool multiply(const uint8_t* stage, const Column<M, N, PARTS> (&col)[NT], float (&acc)[NT][4][4]) {
     const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[t][m][r] = 0.f;
     if constexpr (!M::kFp4) {
         const int mi = lane >> 3, r = lane & 7;
         const uint32_t base = smem_u32(stage) + (uint32_t)((mi >> 1) * 8 + r) * 128u;
 #pragma unroll
-        for (int i = 0; i < N / 16; ++i) {
+        for (int i = 0; i < M::kRows / 16; ++i) {
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 uint32_t a[4];
                 ldmatrix_x4_trans(base + (uint32_t)i * 2048u + (uint32_t)(((2 * m + (mi & 1)) ^ r) << 4), a);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) mma_bf16(acc[t][m], a, col[t].b[0][i]);
+                for (int t = 0; t < NT; ++t) mma_bf16(acc[t][m], a, col[t].b[0][PIECE * (M::kRows / 16) + i]);
             }
         }
         return true;
@@ -218,11 +213,12 @@ __device__ __forceinline__ bool multiply(const uint8_t* stage, const Column<M, N
                 const float s1 = __uint_as_float((k < 3 ? shi << (23 - 8 * k) : shi >> 1) & 0x7f800000u);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int h = 0; h < PARTS; ++h) {
-                        mma_f16(d, a0, col[t].b[h][2 * k]);
-                        mma_f16(d, a1, col[t].b[h][2 * k + 1]);
+                    float d[4];
+                    mma_f16_first(d, a0, col[t].b[0][2 * k]);
+                    mma_f16(d, a1, col[t].b[0][2 * k + 1]);
+                    if constexpr (PARTS == 2) {
+                        mma_f16(d, a0, col[t].b[1][2 * k]);
+                        mma_f16(d, a1, col[t].b[1][2 * k + 1]);
                     }
                     acc[t][m][0] = fmaf(d[0], s0, acc[t][m][0]);
                     acc[t][m][1] = fmaf(d[1], s0, acc[t][m][1]);
@@ -235,31 +231,84 @@ __device__ __forceinline__ bool multiply(const uint8_t* stage, const Column<M, N
     }
 }
 
-// One warp's memories of a piece.  NT = 1: columns 0-3 of the tile are Q and 4-7
-// C of up to 4 tokens; NT = 2: a tile each of up to 8.  it: number of the
-// piece's first memory in this block's order.
+// What a worker copies: the memories of its run, piece by piece, ahead of the
+// part of it that multiplies.
+template <typename M, int N, int TT>
+struct Feed {
+    Walk w;
+    const int* table;
+    int c, last, piece;      // next memory and piece of it, end of the memories of this part of the run
+    int issued;              // stages filled
+    bool more;
+
+    __device__ __forceinline__ void start(const SmaPagedArgs& a, const TileList<kCap>& L) {
+        // to the next part of the run that has memories to copy
+        while ((more = next_piece(w))) {
+            table = a.cache.table + (size_t)L.seq[w.k] * a.cache.width;
+            const int seen = w.units - 1, bad = first_bad_memory(table, a.cache, seen);
+            if (bad < seen && (threadIdx.x & 31) == 0) flag_status(a.status, kStatusDevice);
+            c = w.first_memory();
+            last = min(w.last_memory(), bad);
+            piece = 0;
+            if (c < last) return;
+            advance(L, w, a.H);
+        }
+    }
+    __device__ __forceinline__ void fill(const Params& prm, Smem<M>& s) {
+        if (!more) return;
+        const SmaPagedArgs& a = prm.a;
+        const int st = issued % M::kStages, warp = threadIdx.x >> 5;
+        if ((threadIdx.x & 31) == 0) {
+            const size_t mem = memory_index(a.cache, a.H, table[c / a.cache.R], w.h, c % a.cache.R);
+            const uint32_t full = smem_u32(&s.full[warp][st]), dst = smem_u32(s.ring[warp][st]);
+            mbar_expect_tx(full, M::kStageBytes);
+            if constexpr (M::kFp4) {
+                bulk_load(dst, static_cast<const uint8_t*>(a.cache.pages) + mem * M::kCodeBytes, M::kCodeBytes, full);
+                bulk_load(dst + M::kCodeBytes, a.cache.scales + mem * M::kScaleBytes, M::kScaleBytes, full);
+            } else {
+                tma_load_2d(dst, &prm.map, full, 0, (int)(mem * N) + piece * M::kRows);
+            }
+        }
+        ++issued;
+        if (++piece == M::kPieces) {
+            piece = 0;
+            if (++c == last) {
+                advance(s.tiles, w, a.H);
+                start(a, s.tiles);
+            }
+        }
+    }
+};
+
+// One piece of the run.  NT = 1: columns 0-3 of the tile are Q and 4-7 C of up to
+// 4 tokens; NT = 2: a tile each of up to 8.
 template <typename T, typename M, int N, int TT, int NT, int PARTS>
-__device__ __forceinline__ void run_piece(const SmaPagedArgs& a, Smem<M, TT>& s, const Walk& w, int t0, int rows, int bad, int it,
-                                          const WaitCtx& wc, bool& ok) {
+__device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const Walk& w, int run, int t0, int rows, int bad,
+                                          Feed<M, N, TT>& feed, int& taken, const WaitCtx& wc, bool& ok) {
+    const SmaPagedArgs& a = prm.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
     const int grp = group_of(w.h, a.H, a.G);
     const T *Q = static_cast<const T*>(a.Q), *C = static_cast<const T*>(a.Cm), *E = static_cast<const T*>(a.E);
     auto q_row = [&](int t) { return t < rows ? Q + ((size_t)(t0 + t) * a.H + w.h) * N : nullptr; };
     auto c_row = [&](int t) { return t < rows ? C + ((size_t)(t0 + t) * a.G + grp) * N : nullptr; };
     Column<M, N, PARTS> col[NT];
-    // this lane's two tokens, as columns of the results
+    // this lane's two tokens, as columns of the results, and what their scores and values are to be multiplied by
     const int tk = NT == 2 ? 2 * q : 2 * (q & 1);
-    float qs[2];
+    float qs[2], vs[2];
     if constexpr (NT == 2) {
         const float sq = col[0].load(q_row(g)), sv = col[1].load(c_row(g));
-        if (warp == 0 && q == 0) s.vscale[g] = 1.f / sv;
-        qs[0] = 1.f / __shfl_sync(0xffffffffu, sq, 4 * tk);
-        qs[1] = 1.f / __shfl_sync(0xffffffffu, sq, 4 * tk + 4);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            qs[j] = 1.f / __shfl_sync(0xffffffffu, sq, 4 * (tk + j));
+            vs[j] = 1.f / __shfl_sync(0xffffffffu, sv, 4 * (tk + j));
+        }
     } else {
         const float sc = col[0].load(g < 4 ? q_row(g) : c_row(g - 4));
-        if (warp == 0 && q == 0 && g >= 4) s.vscale[g - 4] = 1.f / sc;
-        qs[0] = 1.f / __shfl_sync(0xffffffffu, sc, 4 * tk);
-        qs[1] = 1.f / __shfl_sync(0xffffffffu, sc, 4 * tk + 4);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            qs[j] = 1.f / __shfl_sync(0xffffffffu, sc, 4 * (tk + j));
+            vs[j] = 1.f / __shfl_sync(0xffffffffu, sc, 4 * (4 + tk + j));
+        }
     }
     const float sscale = kLog2e * rsqrtf((float)N);
     float e[4][4];        // E of (token, column) as the results are laid out
@@ -281,18 +330,28 @@ __device__ __forceinline__ void run_piece(const SmaPagedArgs& a, Smem<M, TT>& s,
 #pragma unroll
         for (int r = 0; r < 4; ++r) o[m][r] = 0.f;
 
-    const int n = min(w.last, bad) - w.first;
-    for (int i = (warp - it % kWarps + kWarps) % kWarps; i < n; i += kWarps) {
-        const int st = (it + i) % M::kStages;
-        const uint32_t ph = (uint32_t)((it + i) / M::kStages) & 1u;
-        if (ok) ok = mbar_wait_warp(smem_u32(&s.bars[st]), ph, wc, 2);
-        if (!ok) continue;
+    const int last = min(w.last_memory(), bad);
+    for (int c = w.first_memory(); c < last; ++c) {
         float acc[NT][4][4];
-        const bool clean = multiply<M, N, NT, PARTS>(s.ring + (size_t)st * M::kStageBytes, col, acc);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s.bars[M::kStages + st]));
-        const int c = w.first + i;
-        float sc[2], f[2], wt[2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[t][m][r] = 0.f;
+        bool clean = true;
+        auto take = [&](auto piece) {
+            const int st = taken % M::kStages;
+            if (ok) ok = mbar_wait_warp(smem_u32(&s.full[warp][st]), (uint32_t)(taken / M::kStages) & 1u, wc, 1);
+            ++taken;
+            if (!ok) return;
+            clean &= multiply<M, N, NT, PARTS, decltype(piece)::value>(s.ring[warp][st], col, acc);
+            __syncwarp();        // every lane has read the stage
+            feed.fill(prm, s);
+        };
+        take(Piece<0>{});
+        if constexpr (M::kPieces == 2) take(Piece<1>{});
+        float f[2], wt[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             float v = 0.f;
@@ -302,12 +361,12 @@ __device__ __forceinline__ void run_piece(const SmaPagedArgs& a, Smem<M, TT>& s,
             v += __shfl_xor_sync(0xffffffffu, v, 8);
             v += __shfl_xor_sync(0xffffffffu, v, 16);
             if (NT == 1) v = __shfl_sync(0xffffffffu, v, lane & ~2);   // the C columns take the scores of the Q columns
-            sc[j] = clean ? v * qs[j] : __int_as_float(0x7fffffff);
-            if (c >= count[j]) sc[j] = -INFINITY;
-            const float mn = fmaxf(mx[j], sc[j]);
+            float sc = clean ? v * qs[j] : __int_as_float(0x7fffffff);
+            if (c >= count[j]) sc = -INFINITY;
+            const float mn = fmaxf(mx[j], sc);
             const bool none = mn == -INFINITY;      // nothing seen yet, or only scores of -inf: they weigh nothing
             f[j] = none ? 1.f : exp2f(mx[j] - mn);
-            wt[j] = none ? (sc[j] == sc[j] ? 0.f : sc[j]) : exp2f(sc[j] - mn);
+            wt[j] = none ? (sc == sc ? 0.f : sc) : exp2f(sc - mn);
             l[j] = fmaf(l[j], f[j], wt[j]);
             mx[j] = mn;
         }
@@ -321,113 +380,104 @@ __device__ __forceinline__ void run_piece(const SmaPagedArgs& a, Smem<M, TT>& s,
                 o[m][r] = fmaf(o[m][r], f[j], v);
             }
     }
-    if (NT == 2 || q >= 2) {
+    // a whole item is written out, a part of one kept for the combine kernel
+    const bool whole = w.whole();
+    const int which = w.c > 0 ? 0 : 1;
+    if (!whole && lane == 0) *piece_header(a.part, run, which) = PieceHeader{w.last == w.units ? 2 : 1, t0, rows, w.h};
+    if (NT == 1 && q < 2) return;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int t = tk + j;
-            if (t < TT) {
+    for (int j = 0; j < 2; ++j) {
+        const int t = tk + j;
+        if (t >= rows) continue;
+        const bool left = count[j] < 0 || count[j] > bad;     // a row that is not to be computed
+        if (whole) {
+            if (left) continue;
+            const size_t at = ((size_t)(t0 + t) * a.H + w.h) * kP + g;
+            const float inv = l[j] == 0.f ? 0.f : vs[j] / l[j];
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    s.o[warp][t][16 * m + g] = o[m][j];
-                    s.o[warp][t][16 * m + g + 8] = o[m][2 + j];
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const size_t p = at + 16 * m + 8 * r;
+                    const float v = o[m][2 * r + j] * inv;
+                    a.out[p] = a.y_ssd ? fmaf(a.g, v, a.y_ssd[p]) : v;
                 }
-                if (g == 0) { s.m[warp][t] = mx[j]; s.l[warp][t] = l[j]; }
-            }
+        } else {
+            float* row = piece_rows<TT, kP>(a.part, run, which) + t * (2 + kP);
+            if (g == 0) { row[0] = mx[j]; row[1] = left ? -1.f : l[j]; }
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) row[2 + g + 16 * m + 8 * r] = o[m][2 * r + j] * vs[j];
         }
     }
 }
 
 template <typename T, typename M, int N, int TT, int PARTS>
-__global__ void __launch_bounds__(kThreads, 1) sma_paged_mma_kernel(const __grid_constant__ Params prm) {
+__global__ void __launch_bounds__(32 * M::kWarps, 1) sma_paged_mma_kernel(const __grid_constant__ Params prm) {
     extern __shared__ uint8_t raw[];
-    Smem<M, TT>& s = *reinterpret_cast<Smem<M, TT>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    Smem<M>& s = *reinterpret_cast<Smem<M>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const SmaPagedArgs& a = prm.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
-        for (int i = 0; i < 2 * M::kStages; ++i) mbar_init(smem_u32(&s.bars[i]), 1);
+        for (int i = 0; i < M::kWarps * M::kStages; ++i) mbar_init(smem_u32(&s.full[0][0] + i), 1);
         s.abort_flag = 0;
         fence_mbar_init();
     }
+    // neighbours in the order of units go to different blocks: a few units spread over all of them
+    const int runs = gridDim.x * M::kWarps, run = warp * gridDim.x + blockIdx.x;
     griddep_wait();
-    if (tid < 2) piece_header(a.part, blockIdx.x, tid)->state = 0;
+    if (lane < 2) piece_header(a.part, run, lane)->state = 0;
+    __syncwarp();
     build_tiles<TT, kCap>(a, s.tiles);
+    if (s.tiles.n == 0) return;
     const WaitCtx wc{&s.abort_flag, a.status, 10};
-    const long long limit = (long long)a.cache.width * a.cache.R;
-    const int R = a.cache.R;
     bool ok = true;
-    int it = 0;           // memories of the pieces before this one
-    int issued = 0;       // copies started
-    if (s.tiles.n > 0)
-        for (Walk w = start_walk(s.tiles, a.H, kLeast); next_piece(w); advance(s.tiles, w, a.H)) {
-            const int b = s.tiles.seq[w.k], t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, b, t0, TT);
-            const int* table = a.cache.table + (size_t)b * a.cache.width;
-            int seen = lane < rows ? usable_count(a.mem_count[t0 + lane], limit) : 0;
-            seen = __reduce_max_sync(0xffffffffu, seen);
-            const int bad = first_bad_memory(table, a.cache, seen);
-            const int n = max(0, min(w.last, bad) - w.first);
-            if (warp == kWarps) {
-                // ---- copies
-                if (bad < seen && lane == 0) flag_status(a.status, kStatusDevice);
-                for (int i = 0; i < n && ok; ++i) {
-                    const int c = w.first + i, st = (it + i) % M::kStages;
-                    const uint32_t ph = (uint32_t)((it + i) / M::kStages) & 1u;
-                    ok = mbar_wait_warp(smem_u32(&s.bars[M::kStages + st]), ph ^ 1u, wc, 1);
-                    if (ok && lane == 0) {
-                        const size_t mem = memory_index(a.cache, a.H, table[c / R], w.h, c % R);
-                        const uint32_t full = smem_u32(&s.bars[st]), dst = smem_u32(s.ring + (size_t)st * M::kStageBytes);
-                        issued = it + i + 1;
-                        mbar_expect_tx(full, M::kBytes);
-                        if constexpr (M::kFp4) {
-                            bulk_load(dst, static_cast<const uint8_t*>(a.cache.pages) + mem * M::kCodeBytes, M::kCodeBytes, full);
-                            bulk_load(dst + M::kCodeBytes, a.cache.scales + mem * M::kScaleBytes, M::kScaleBytes, full);
-                        } else {
-                            tma_load_2d(dst, &prm.map, full, 0, (int)(mem * N));
-                        }
-                    }
-                }
-                __syncwarp();
-            } else {
-                if (TT == 8 && rows > 4) {
-                    if constexpr (TT == 8) run_piece<T, M, N, TT, 2, PARTS>(a, s, w, t0, rows, bad, it, wc, ok);
-                } else {
-                    run_piece<T, M, N, TT, 1, PARTS>(a, s, w, t0, rows, bad, it, wc, ok);
-                }
-                named_bar_sync(1, 32 * kWarps);
-                finish_piece<kWarps, TT, kP, kOS>(a, w, t0, rows, a.mem_count + t0, bad, s.m, s.l, s.o, s.vscale, tid, 32 * kWarps);
-                named_bar_sync(1, 32 * kWarps);
-            }
-            it += n;
+    int taken = 0;
+    Feed<M, N, TT> feed;
+    feed.w = start_walk(s.tiles, a.H, run, runs, kLeast);
+    feed.issued = 0;
+    Walk w = feed.w;
+    feed.start(a, s.tiles);
+    for (int i = 0; i < M::kStages; ++i) feed.fill(prm, s);
+    for (; next_piece(w); advance(s.tiles, w, a.H)) {
+        const int b = s.tiles.seq[w.k], t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, b, t0, TT);
+        const int bad = first_bad_memory(a.cache.table + (size_t)b * a.cache.width, a.cache, w.units - 1);
+        if (TT == 8 && rows > 4) {
+            if constexpr (TT == 8) run_piece<T, M, N, TT, 2, PARTS>(prm, s, w, run, t0, rows, bad, feed, taken, wc, ok);
+        } else {
+            run_piece<T, M, N, TT, 1, PARTS>(prm, s, w, run, t0, rows, bad, feed, taken, wc, ok);
         }
-    // Every copy has been waited for by the warp that used it, unless a wait gave
-    // up: what is in flight then is waited for here, before its shared memory goes.
-    if (warp == kWarps && lane == 0 && !ok)
-        for (int i = max(0, issued - M::kStages); i < issued; ++i)
-            for (int k = 0; k < (1 << 20) && !mbar_try_wait(smem_u32(&s.bars[i % M::kStages]), (uint32_t)(i / M::kStages) & 1u); ++k) {}
-    __syncthreads();
+    }
+    // Every copy has been waited for, unless a wait gave up: what is in flight then
+    // is waited for here, before its shared memory goes away.
+    if (!ok && lane == 0)
+        for (int i = max(0, feed.issued - M::kStages); i < feed.issued; ++i)
+            for (int k = 0; k < (1 << 20) && !mbar_try_wait(smem_u32(&s.full[warp][i % M::kStages]), (uint32_t)(i / M::kStages) & 1u); ++k) {}
 }
 
 template <typename T, typename M, int N, int TT, int PARTS>
 cudaError_t run(const SmaPagedArgs& a, cudaStream_t st) {
     auto kern = sma_paged_mma_kernel<T, M, N, TT, PARTS>;
-    const int smem = (int)sizeof(Smem<M, TT>) + 1024, sms = paged_sm_count();
-    static_assert(sizeof(Smem<M, TT>) + 1024 <= 232448, "shared memory");
+    const int smem = (int)sizeof(Smem<M>) + 1024, sms = paged_sm_count();
+    static_assert(sizeof(Smem<M>) + 1024 <= 232448, "shared memory");
     if (sms <= 0) return cudaErrorInvalidDevice;
     Params prm;
     memset(&prm.map, 0, sizeof(prm.map));
     prm.a = a;
     if constexpr (!M::kFp4) {
         const uint64_t rows = (uint64_t)a.cache.npages * a.H * a.cache.R * N;
-        if (rows > 0x7fffffffull) return cudaErrorInvalidValue;      // 256 GB and more of N = 128 memories
+        if (rows > 0x7fffffffull) return cudaErrorInvalidValue;      // 256 GB and more of memories
         const uint64_t dims[2] = {kP, rows}, strides[1] = {kP * 2};
-        const uint32_t box[2] = {kP, N};
+        const uint32_t box[2] = {kP, (uint32_t)M::kRows};
         if (!encode_tile_map_bf16(&prm.map, 2, a.cache.pages, dims, strides, box)) return cudaErrorInvalidValue;
     }
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int blocks = min(sms, kMaxBlocks);
-    if ((e = launch_dependent(kern, dim3(blocks), dim3(kThreads), smem, st, 1, prm)) != cudaSuccess) return e;
+    const int blocks = min(sms, kMaxRuns / M::kWarps);
+    if ((e = launch_dependent(kern, dim3(blocks), dim3(32 * M::kWarps), smem, st, 1, prm)) != cudaSuccess) return e;
     count_launches(1);
-    return launch_sma_paged_combine(a, blocks, TT, st);
+    return launch_sma_paged_combine(a, blocks * M::kWarps, TT, st);
 }
 
 }  // namespace
