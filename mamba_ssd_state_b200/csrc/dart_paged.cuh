@@ -52,8 +52,8 @@ struct SmaPagedArgs {
     int* status;
 };
 
-// Largest number of memories a sequence's table may name: 2^27 tokens of context at S = 256.
-constexpr long long kPagedMaxMemories = 1 << 19;
+// Largest number of memories a sequence's table may name: 2^26 tokens of context at S = 256.
+constexpr long long kPagedMaxMemories = 1 << 18;
 
 bool paged_supported(int N, int P, int mxfp4);
 cudaError_t launch_cache_write(const CacheCopyArgs& a, dart_dtype dt, cudaStream_t st);

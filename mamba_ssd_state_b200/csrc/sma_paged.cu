@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) sma_paged_kernel(SmaPagedArgs a) {
         }
         if (tid < kTT) s.count[tid] = tid < rows ? a.mem_count[t0 + tid] : -1;
         if (tid < 32) {
-            const int seen = w.units - 1;      // the most that a row of the tile sees
+            const int seen = w.memories();     // the most that a row of the tile sees
             const int bad = first_bad_memory(table, a.cache, seen);
             if (lane == 0) {
                 s.bad = bad;

@@ -2,7 +2,7 @@
 //
 // The packed tokens of a sequence are cut into tiles of TT rows.  An item is a
 // tile and a head; it reads the memories its rows may see (up to the largest
-// count among them), one unit each, and one unit stands for the item itself.
+// count among them), one unit each, and kItemUnits stand for the item itself.
 // The units in the order (tile, head, memory) are cut into equal runs, one for
 // every worker (a block, or a warp), whatever the batch looks like.  An item
 // that falls into several runs leaves one partial result (running maximum, sum,
@@ -27,6 +27,10 @@ struct PieceHeader {
     int h;
 };
 constexpr int kMaxRuns = 2048;   // runs of any of the kernels
+// What starting an item costs a worker, in memories: its loads wait for each
+// other while a memory of the ring is there already.  With 1, a batch that held
+// a sequence without memories took twice as long as its other items.
+constexpr int kItemUnits = 4;
 
 // Joins the pieces that the runs of a kernel with tiles of tt rows left.
 cudaError_t launch_sma_paged_combine(const SmaPagedArgs& a, int runs, int tt, cudaStream_t st);
@@ -38,7 +42,7 @@ int paged_sm_count();
 #ifdef __CUDACC__
 
 // Tiles of the batch in shared memory: tile k covers rows t0[k] .. of sequence
-// seq[k] and has pre[k+1] - pre[k] units a head, 1 + the memories it reads.
+// seq[k] and has pre[k+1] - pre[k] units a head, kItemUnits + the memories it reads.
 template <int CAP>
 struct TileList {
     int pre[CAP + 1];
@@ -113,7 +117,7 @@ __device__ __forceinline__ void build_tiles(const SmaPagedArgs& a, TileList<CAP>
                 bad |= c < -1 || c > limit;
                 most = max(most, usable_count(c, limit));
             }
-            ++most;
+            most += kItemUnits;
         }
         int total;
         const int at = sum + block_scan(most, L.scan, total);
@@ -131,33 +135,54 @@ struct Walk {
     int k, h, c;         // tile, head, unit of the item at u
     int units;           // units of the item
     int last;            // the piece: units [c, last) of the item
-    __device__ __forceinline__ int first_memory() const { return max(c - 1, 0); }
-    __device__ __forceinline__ int last_memory() const { return last - 1; }
+    __device__ __forceinline__ int memories() const { return units - kItemUnits; }   // of the item
+    __device__ __forceinline__ int first_memory() const { return max(c - kItemUnits, 0); }
+    __device__ __forceinline__ int last_memory() const { return last - kItemUnits; }
     __device__ __forceinline__ bool whole() const { return last - c == units; }
 };
 
-// Run i of G; runs of fewer than `least` units are not cut smaller.
+// The tile of unit u.
 template <int CAP>
-__device__ __forceinline__ Walk start_walk(const TileList<CAP>& L, int H, int i, int runs, int least) {
-    Walk w;
-    const long long W = (long long)L.pre[L.n] * H;
-    const long long G = min((long long)runs, (W + least - 1) / least);
-    w.u = i < G ? W * i / G : W;
-    w.end = i < G ? W * (i + 1) / G : W;
-    int lo = 0, hi = L.n - 1;              // the tile of unit u
+__device__ __forceinline__ int tile_of(const TileList<CAP>& L, int H, long long u) {
+    int lo = 0, hi = L.n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if ((long long)L.pre[mid] * H <= w.u) lo = mid; else hi = mid - 1;
+        if ((long long)L.pre[mid] * H <= u) lo = mid; else hi = mid - 1;
     }
-    w.k = lo;
-    w.units = 1;
-    w.h = w.c = 0;
-    if (w.u < w.end) {
-        w.units = L.pre[lo + 1] - L.pre[lo];
-        const long long r = w.u - (long long)L.pre[lo] * H;
+    return lo;
+}
+
+// Run i of `runs`; runs of fewer than `least` units are not cut smaller, and a
+// cut that falls into the units that stand for an item goes before them.
+template <int CAP>
+__device__ __forceinline__ Walk start_walk(const TileList<CAP>& L, int H, int i, int runs, int least) {
+    const long long W = (long long)L.pre[L.n] * H;
+    const long long G = min((long long)runs, (W + least - 1) / least);
+    Walk w;
+    auto cut = [&](long long u) {      // leaves w at the cut
+        w.u = u;
+        w.h = w.c = 0;
+        w.units = 1;
+        if (u >= W) return;
+        w.k = tile_of(L, H, u);
+        w.units = L.pre[w.k + 1] - L.pre[w.k];
+        const long long r = u - (long long)L.pre[w.k] * H;
         w.h = (int)(r / w.units);
         w.c = (int)(r % w.units);
+        if (w.c < kItemUnits) {
+            w.u -= w.c;
+            w.c = 0;
+        }
+    };
+    w.k = 0;
+    if (i >= G) {
+        cut(W);
+        w.end = W;
+        return w;
     }
+    cut(W * (i + 1) / G);
+    w.end = w.u;
+    cut(W * i / G);
     return w;
 }
 // The next piece; false at the end of the run.

@@ -245,7 +245,7 @@ struct Feed {
         // to the next part of the run that has memories to copy
         while ((more = next_piece(w))) {
             table = a.cache.table + (size_t)L.seq[w.k] * a.cache.width;
-            const int seen = w.units - 1, bad = first_bad_memory(table, a.cache, seen);
+            const int seen = w.memories(), bad = first_bad_memory(table, a.cache, seen);
             if (bad < seen && (threadIdx.x & 31) == 0) flag_status(a.status, kStatusDevice);
             c = w.first_memory();
             last = min(w.last_memory(), bad);
@@ -442,7 +442,15 @@ __global__ void __launch_bounds__(32 * M::kWarps, 1) sma_paged_mma_kernel(const 
     for (int i = 0; i < M::kStages; ++i) feed.fill(prm, s);
     for (; next_piece(w); advance(s.tiles, w, a.H)) {
         const int b = s.tiles.seq[w.k], t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, b, t0, TT);
-        const int bad = first_bad_memory(a.cache.table + (size_t)b * a.cache.width, a.cache, w.units - 1);
+        if (w.memories() == 0) {      // nothing to see: the readout is 0
+            for (int i = lane; i < rows * kP; i += 32) {
+                const int c = a.mem_count[t0 + i / kP];
+                const size_t at = ((size_t)(t0 + i / kP) * a.H + w.h) * kP + i % kP;
+                if (c == 0) a.out[at] = a.y_ssd ? a.y_ssd[at] : 0.f;
+            }
+            continue;
+        }
+        const int bad = first_bad_memory(a.cache.table + (size_t)b * a.cache.width, a.cache, w.memories());
         if (TT == 8 && rows > 4) {
             if constexpr (TT == 8) run_piece<T, M, N, TT, 2, PARTS>(prm, s, w, run, t0, rows, bad, feed, taken, wc, ok);
         } else {
