@@ -10,8 +10,6 @@
 // 2 x 8 products.  Scores are summed over the warp, the softmax runs online in
 // base 2, and v is folded into the lane's own columns, so that the eight warps
 // of a block meet only at the end of a piece.
-#include <atomic>
-
 #include "sm100.cuh"
 #include "sma_paged.cuh"
 
@@ -223,7 +221,8 @@ cudaError_t run(const SmaPagedArgs& a, cudaStream_t st) {
     auto kern = sma_paged_kernel<T, N, P>;
     const int smem = (int)sizeof(Smem<N, P>), sms = paged_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<unsigned long long> ready{0};   // devices whose kernel has its shared memory allowed
+    cudaError_t e = paged_allow_smem(reinterpret_cast<const void*>(kern), smem, ready);
     if (e != cudaSuccess) return e;
     const int blocks = min(2 * sms, kMaxRuns);
     kern<<<blocks, kThreads, smem, st>>>(a);
@@ -244,6 +243,17 @@ int paged_sm_count() {
         cache[dev].store(n, std::memory_order_relaxed);
     }
     return n;
+}
+
+cudaError_t paged_allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& ready) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 cudaError_t launch_sma_paged_combine(const SmaPagedArgs& a, int runs, int tt, cudaStream_t st) {

@@ -14,6 +14,8 @@
 // on the device), which costs less than a launch of its own would.
 #pragma once
 
+#include <atomic>
+
 #include "dart_paged.cuh"
 
 namespace dart {
@@ -38,6 +40,9 @@ cudaError_t launch_sma_paged_combine(const SmaPagedArgs& a, int runs, int tt, cu
 cudaError_t launch_sma_paged_mma(const SmaPagedArgs& a, dart_dtype dt, cudaStream_t st);
 // Multiprocessors of the current device, looked up once; 0 on failure.
 int paged_sm_count();
+// Allows a kernel its dynamic shared memory on the current device, once for each
+// (ready: one per kernel; threads that race set the same attribute twice).
+cudaError_t paged_allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& ready);
 
 #ifdef __CUDACC__
 

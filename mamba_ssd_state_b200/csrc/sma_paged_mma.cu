@@ -52,7 +52,7 @@ template <int N> struct Bf16Mem {
 };
 template <int N> struct Fp4Mem {
     static constexpr bool kFp4 = true;
-    static constexpr int kWarps = 8, kStages = 4, kPieces = 1;
+    static constexpr int kWarps = 12, kStages = 3, kPieces = 1;
     static constexpr uint32_t kCodeBytes = N * kP / 2, kScaleBytes = N * kP / 32;
     static constexpr uint32_t kStageBytes = kCodeBytes + kScaleBytes;
 };
@@ -370,15 +370,26 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const W
             l[j] = fmaf(l[j], f[j], wt[j]);
             mx[j] = mn;
         }
+        // most memories move no maximum, and most rows see all of them
+        if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+            for (int m = 0; m < 4; ++m)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int j = r & 1;
-                // 0 weight reads nothing, whatever the value is
-                const float v = wt[j] != 0.f ? wt[j] * acc[NT - 1][m][r] : 0.f;
-                o[m][r] = fmaf(o[m][r], f[j], v);
-            }
+                for (int r = 0; r < 4; ++r) o[m][r] *= f[r & 1];
+        }
+        if (__any_sync(0xffffffffu, wt[0] == 0.f || wt[1] == 0.f)) {
+            // 0 weight reads nothing, whatever the value is
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (wt[r & 1] != 0.f) o[m][r] = fmaf(wt[r & 1], acc[NT - 1][m][r], o[m][r]);
+        } else {
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[m][r] = fmaf(wt[r & 1], acc[NT - 1][m][r], o[m][r]);
+        }
     }
     // a whole item is written out, a part of one kept for the combine kernel
     const bool whole = w.whole();
@@ -480,7 +491,8 @@ cudaError_t run(const SmaPagedArgs& a, cudaStream_t st) {
         const uint32_t box[2] = {kP, (uint32_t)M::kRows};
         if (!encode_tile_map_bf16(&prm.map, 2, a.cache.pages, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<unsigned long long> ready{0};   // devices whose kernel has its shared memory allowed
+    cudaError_t e = paged_allow_smem(reinterpret_cast<const void*>(kern), smem, ready);
     if (e != cudaSuccess) return e;
     const int blocks = min(sms, kMaxRuns / M::kWarps);
     if ((e = launch_dependent(kern, dim3(blocks), dim3(32 * M::kWarps), smem, st, 1, prm)) != cudaSuccess) return e;

@@ -574,49 +574,67 @@ def decode_memlog_init(dt, A, chunk: int, memlog):
 # [npages,H,R,N,P] in the tokens' dtype, or uint8 codes [npages,H,R,P,N/2] with
 # scales uint8 [npages,H,R,P,N/32] (the 4-bit format of include/dart.h).
 # ---------------------------------------------------------------------------
-def _in_place(**tensors):
-    for name, t in tensors.items():
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor")
+def _need(name, t, shape, dtype, dev):
+    """A contiguous tensor of a given shape, type and device.  These calls serve single tokens: the checks that pass
+    are kept short, since they are most of what a call costs the host."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the pages on {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _counters(dev, length, **tensors):
-    """int32 device vectors of a given length."""
-    _in_place(**tensors)
-    for name, t in tensors.items():
-        if t.dtype != torch.int32:
-            raise TypeError(f"{name} must be int32, got {t.dtype}")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the pages on {dev}")
-        _shape(name, t, (length,))
+def _input(t, dev, dtype):
+    """A token tensor: copied to the device or made contiguous if need be."""
+    if t.dtype != dtype:
+        raise TypeError(f"expected {dtype}, got {t.dtype}")
+    return t if t.device == dev and t.is_contiguous() else t.to(dev, non_blocking=True).contiguous()
+
+
+def _call(fn, dev, *args):
+    """fn on dev and dev's current stream (the last argument)."""
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        _check(rc)
 
 
 def _paged(pages, scales, table, dtype, B, H, N, P) -> PagedCache:
     """The C description of a paged cache, after checking it against the shapes it has to hold."""
-    _in_place(pages=pages, table=table, **({} if scales is None else {"scales": scales}))
-    if table.dtype != torch.int32 or table.dim() != 2:
-        raise TypeError("table must be an int32 tensor [B, width]")
-    _shape("table", table, (B, table.shape[1]))
-    if pages.dim() != 5:
-        raise ValueError(f"pages: expected 5 dimensions, got shape {tuple(pages.shape)}")
-    npages, _, R = pages.shape[:3]
-    for t in (table, scales):
-        if t is not None and t.device != pages.device:
-            raise ValueError(f"table, scales and pages are on different devices ({t.device}, {pages.device})")
+    dev = pages.device
+    if dev.type != "cuda":
+        raise ValueError("pages must be a contiguous CUDA tensor")
+    if pages.dim() != 5 or table.dim() != 2:
+        raise ValueError(f"expected pages of 5 dimensions and a table of 2, got {tuple(pages.shape)} and {tuple(table.shape)}")
+    npages, _, R, _, _ = pages.shape
+    width = table.shape[1]
+    tp = _need("table", table, (B, width), torch.int32, dev)
     if pages.dtype == torch.uint8:
-        if scales is None or scales.dtype != torch.uint8:
+        if scales is None:
             raise TypeError("4-bit (uint8) pages need their uint8 scales")
-        _shape("pages", pages, (npages, H, R, P, N // 2))
-        _shape("scales", scales, (npages, H, R, P, N // 32))
-        fmt = DART_CACHE_MXFP4
-    else:
-        if scales is not None:
-            raise ValueError("scales belong to 4-bit (uint8) pages")
-        if pages.dtype != dtype:
-            raise TypeError(f"pages are {pages.dtype}, the inputs {dtype}")
-        _shape("pages", pages, (npages, H, R, N, P))
-        fmt = DART_CACHE_DTYPE
-    return PagedCache(fmt, npages, R, table.shape[1], _ptr(pages), _ptr(scales), _ptr(table))
+        return PagedCache(DART_CACHE_MXFP4, npages, R, width, _need("pages", pages, (npages, H, R, P, N // 2), torch.uint8, dev),
+                          _need("scales", scales, (npages, H, R, P, N // 32), torch.uint8, dev), tp)
+    if scales is not None:
+        raise ValueError("scales belong to 4-bit (uint8) pages")
+    return PagedCache(DART_CACHE_DTYPE, npages, R, width, _need("pages", pages, (npages, H, R, N, P), dtype, dev), None, tp)
+
+
+def _move_pages(fn, dense, name, first, count, pages, table, scales, order):
+    B, H, C, N, P = dense.shape
+    dev = pages.device
+    cache = _paged(pages, scales, table, dense.dtype, B, H, N, P)
+    dense_ptr = _need(name, dense, (B, H, C, N, P), dense.dtype, dev)
+    f, c = _need("first", first, (B,), torch.int32, dev), _need("count", count, (B,), torch.int32, dev)
+    dims = Dims(B, 0, H, P, N, 1, 1)
+    _call(fn, dev, ctypes.byref(dims), _dtype_code(dense.dtype), *order(dense_ptr, C, f, c, ctypes.byref(cache)))
 
 
 def dart_cache_write_paged(dH, first, count, pages, table, *, scales=None):
@@ -624,18 +642,8 @@ def dart_cache_write_paged(dH, first, count, pages, table, *, scales=None):
     i < count[b].  dH [B,H,C,N,P] (float32 or bfloat16, e.g. dart_ssd_chunk_scan's
     memories), first and count int32 [B], pages/scales in place; all on the
     device.  uint8 pages take 4-bit codes.  Returns (pages, scales)."""
-    lib = load()
-    _in_place(dH=dH)
-    B, H, C, N, P = dH.shape
-    dev = pages.device
-    cache = _paged(pages, scales, table, dH.dtype, B, H, N, P)
-    if dH.device != dev:
-        raise ValueError(f"dH is on {dH.device}, the pages on {dev}")
-    _counters(dev, B, first=first, count=count)
-    dims = Dims(B, 0, H, P, N, 1, 1)
-    with torch.cuda.device(dev):
-        _check(lib.dart_cache_write_paged(ctypes.byref(dims), _dtype_code(dH.dtype), _ptr(dH), C, _ptr(first),
-                                          _ptr(count), ctypes.byref(cache), _stream()))
+    _move_pages(load().dart_cache_write_paged, dH, "dH", first, count, pages, table, scales,
+                lambda d, C, f, c, cache: (d, C, f, c, cache))
     return pages, scales
 
 
@@ -643,18 +651,8 @@ def dart_cache_read_paged(pages, table, first, count, *, out, scales=None):
     """Memories out of pages: out[b, :, i] = memory first[b] + i of sequence b for
     i < count[b]; other entries of out [B,H,C,N,P] (float32 or bfloat16; the
     pages' dtype unless they hold 4-bit codes) are left as they are.  Returns out."""
-    lib = load()
-    _in_place(out=out)
-    B, H, C, N, P = out.shape
-    dev = pages.device
-    cache = _paged(pages, scales, table, out.dtype, B, H, N, P)
-    if out.device != dev:
-        raise ValueError(f"out is on {out.device}, the pages on {dev}")
-    _counters(dev, B, first=first, count=count)
-    dims = Dims(B, 0, H, P, N, 1, 1)
-    with torch.cuda.device(dev):
-        _check(lib.dart_cache_read_paged(ctypes.byref(dims), _dtype_code(out.dtype), ctypes.byref(cache), _ptr(first),
-                                         _ptr(count), _ptr(out), C, _stream()))
+    _move_pages(load().dart_cache_read_paged, out, "out", first, count, pages, table, scales,
+                lambda d, C, f, c, cache: (cache, f, c, d, C))
     return out
 
 
@@ -674,43 +672,40 @@ def dart_ssd_extend(x, dt, A, Bm, Cm, cu_tokens, state, dH_cur, pages, table, nc
     int32 [T] for dart_sma_paged.  Rows no sequence owns are not written."""
     lib = load()
     dev = pages.device
-    x, Bm, Cm = (_dev(v, dev, x.dtype) for v in (x, Bm, Cm))
-    dt, A = _dev(dt, dev, torch.float32), _dev(A, dev, torch.float32)
+    f32, i32 = torch.float32, torch.int32
+    x, Bm, Cm = (_input(v, dev, x.dtype) for v in (x, Bm, Cm))
+    dt, A = _input(dt, dev, f32), _input(A, dev, f32)
     T, H, P = x.shape
-    B, _, N, _ = state.shape
-    _shape("dt", dt, (T, H)); _shape("A", A, (H,))
+    B, _, N, _ = shape = state.shape
+    _shape("state", state, (B, H, N, P))
     G = _bc_groups("Bm", Bm, (T,), H)
     if Bm.shape[-1] != N or Cm.shape != Bm.shape:
         raise ValueError("Bm and Cm must both be [T,N] or [T,G,N] with the state's N")
+    cache = _paged(pages, scales, table, x.dtype, B, H, N, P)
     state_out = state if state_out is None else state_out
     dH_cur_out = dH_cur if dH_cur_out is None else dH_cur_out
-    for name, t in (("state", state), ("dH_cur", dH_cur), ("state_out", state_out), ("dH_cur_out", dH_cur_out)):
-        _in_place(**{name: t})
-        _shape(name, t, (B, H, N, P))
-        if t.dtype != torch.float32 or t.device != dev:
-            raise TypeError(f"{name} must be float32 on {dev}")
-    cache = _paged(pages, scales, table, x.dtype, B, H, N, P)
-    nchunks_out = torch.empty_like(nchunks) if nchunks_out is None else nchunks_out
-    pos_out = torch.empty_like(pos) if pos_out is None else pos_out
-    _counters(dev, B, nchunks=nchunks, pos=pos, nchunks_out=nchunks_out, pos_out=pos_out)
-    _counters(dev, B + 1, cu_tokens=cu_tokens)
+    if nchunks_out is None:
+        nchunks_out = torch.empty((B,), dtype=i32, device=dev)
+    if pos_out is None:
+        pos_out = torch.empty((B,), dtype=i32, device=dev)
     if y is None:
-        y = torch.empty((T, H, P), device=dev, dtype=torch.float32)
+        y = torch.empty((T, H, P), device=dev, dtype=f32)
     if mem_count is None:
-        mem_count = torch.empty((T,), device=dev, dtype=torch.int32)
-    _in_place(y=y)
-    _shape("y", y, (T, H, P))
-    if y.dtype != torch.float32 or y.device != dev:
-        raise TypeError(f"y must be float32 on {dev}")
-    _counters(dev, T, mem_count=mem_count)
+        mem_count = torch.empty((T,), device=dev, dtype=i32)
     dims = Dims(B, T, H, P, N, chunk, G)
-    with torch.cuda.device(dev):
-        _check(lib.dart_ssd_extend(ctypes.byref(dims), _dtype_code(x.dtype), _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm),
-                                   _ptr(Cm), _ptr(cu_tokens), _ptr(state), _ptr(state_out), _ptr(dH_cur),
-                                   _ptr(dH_cur_out), ctypes.byref(cache), _ptr(nchunks), _ptr(pos),
-                                   _ptr(nchunks_out), _ptr(pos_out), _ptr(y), _ptr(mem_count), _stream()))
+    _call(lib.dart_ssd_extend, dev, ctypes.byref(dims), _dtype_code(x.dtype), x.data_ptr(),
+          _need("dt", dt, (T, H), f32, dev), _need("A", A, (H,), f32, dev), Bm.data_ptr(), Cm.data_ptr(),
+          _need("cu_tokens", cu_tokens, (B + 1,), i32, dev),
+          _need("state", state, shape, f32, dev), _need("state_out", state_out, shape, f32, dev),
+          _need("dH_cur", dH_cur, shape, f32, dev), _need("dH_cur_out", dH_cur_out, shape, f32, dev),
+          ctypes.byref(cache), _need("nchunks", nchunks, (B,), i32, dev), _need("pos", pos, (B,), i32, dev),
+          _need("nchunks_out", nchunks_out, (B,), i32, dev), _need("pos_out", pos_out, (B,), i32, dev),
+          _need("y", y, (T, H, P), f32, dev), _need("mem_count", mem_count, (T,), i32, dev))
     return {"y": y, "state": state_out, "dH_cur": dH_cur_out, "nchunks": nchunks_out, "pos": pos_out,
             "mem_count": mem_count}
+
+
+_SMA_PAGED_WORKSPACE = {}   # bytes by headdim
 
 
 def dart_sma_paged(Q, E, Cm, cu_tokens, pages, table, mem_count, g: float, y_ssd=None, *, scales=None, out=None,
@@ -719,37 +714,38 @@ def dart_sma_paged(Q, E, Cm, cu_tokens, pages, table, mem_count, g: float, y_ssd
     [T,H,P] equal to y_ssd + g*o (or o when y_ssd is None), token t of sequence b
     seeing the sequence's first mem_count[t] memories (int32 [T], as
     dart_ssd_extend returns it; -1 leaves the row as it is).  Q[T,H,N], E[T,H,P],
-    Cm[T,N] or [T,G,N] in one dtype.  out may be y_ssd itself.  Rows no sequence
-    owns are not written."""
+    Cm[T,N] or [T,G,N] in one dtype.  out may be y_ssd itself.  workspace: uint8,
+    dart_sma_paged_workspace_bytes() of them; calls that may overlap need one
+    each.  Rows no sequence owns are not written."""
     lib = load()
     dev = pages.device
-    Q, E, Cm = (_dev(v, dev, Q.dtype) for v in (Q, E, Cm))
-    y_ssd = _dev(y_ssd, dev, torch.float32)
+    f32, dtype = torch.float32, Q.dtype
+    Q, E, Cm = _input(Q, dev, dtype), _input(E, dev, dtype), _input(Cm, dev, dtype)
     T, H, N = Q.shape
     P = E.shape[-1]
     B = table.shape[0]
-    _shape("E", E, (T, H, P))
+    if E.shape != (T, H, P):
+        raise ValueError(f"E: expected shape {(T, H, P)}, got {tuple(E.shape)}")
     G = _bc_groups("Cm", Cm, (T,), H)
-    _shape("Cm", Cm, (*Cm.shape[:-1], N))
-    cache = _paged(pages, scales, table, Q.dtype, B, H, N, P)
-    _counters(dev, B + 1, cu_tokens=cu_tokens)
-    _counters(dev, T, mem_count=mem_count)
+    if Cm.shape[-1] != N:
+        raise ValueError(f"Cm: expected {N} columns, got {Cm.shape[-1]}")
+    cache = _paged(pages, scales, table, dtype, B, H, N, P)
+    yp = None
     if y_ssd is not None:
-        _shape("y_ssd", y_ssd, (T, H, P))
+        y_ssd = _input(y_ssd, dev, f32)
+        yp = _need("y_ssd", y_ssd, (T, H, P), f32, dev)
     if out is None:
-        out = torch.empty((T, H, P), device=dev, dtype=torch.float32)
-    _in_place(out=out)
-    _shape("out", out, (T, H, P))
-    if out.dtype != torch.float32 or out.device != dev:
-        raise TypeError(f"out must be float32 on {dev}")
+        out = torch.empty((T, H, P), device=dev, dtype=f32)
     dims = Dims(B, T, H, P, N, 1, G)
     if workspace is None:
-        workspace = torch.empty(lib.dart_sma_paged_workspace_bytes(ctypes.byref(dims)), device=dev, dtype=torch.uint8)
-    with torch.cuda.device(dev):
-        _check(lib.dart_sma_paged(ctypes.byref(dims), _dtype_code(Q.dtype), _ptr(Q), _ptr(E), _ptr(Cm),
-                                  _ptr(cu_tokens), ctypes.byref(cache), _ptr(mem_count), float(g), _ptr(y_ssd),
-                                  _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                  _stream()))
+        n = _SMA_PAGED_WORKSPACE.get(P)
+        if n is None:
+            n = _SMA_PAGED_WORKSPACE[P] = lib.dart_sma_paged_workspace_bytes(ctypes.byref(dims))
+        workspace = torch.empty((n,), device=dev, dtype=torch.uint8)
+    _call(lib.dart_sma_paged, dev, ctypes.byref(dims), _dtype_code(dtype), Q.data_ptr(), E.data_ptr(), Cm.data_ptr(),
+          _need("cu_tokens", cu_tokens, (B + 1,), torch.int32, dev), ctypes.byref(cache),
+          _need("mem_count", mem_count, (T,), torch.int32, dev), float(g), yp, _need("out", out, (T, H, P), f32, dev),
+          _need("workspace", workspace, workspace.shape, torch.uint8, dev), workspace.numel())
     return out
 
 
