@@ -574,67 +574,67 @@ def decode_memlog_init(dt, A, chunk: int, memlog):
 # [npages,H,R,N,P] in the tokens' dtype, or uint8 codes [npages,H,R,P,N/2] with
 # scales uint8 [npages,H,R,P,N/32] (the 4-bit format of include/dart.h).
 # ---------------------------------------------------------------------------
-def _need(name, t, shape, dtype, dev):
-    """A contiguous tensor of a given shape, type and device.  These calls serve single tokens: the checks that pass
-    are kept short, since they are most of what a call costs the host."""
+def _need(name, t, shape, dtype, index):
+    """The address of a contiguous tensor of a given shape and type on CUDA device `index`.  These calls serve single
+    tokens: the check that passes is kept short, since checks are much of what a call costs the host."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the pages on {dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the pages on cuda:{index}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _input(t, dev, dtype):
+def _input(t, dtype, index):
     """A token tensor: copied to the device or made contiguous if need be."""
+    if t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+        return t
     if t.dtype != dtype:
         raise TypeError(f"expected {dtype}, got {t.dtype}")
-    return t if t.device == dev and t.is_contiguous() else t.to(dev, non_blocking=True).contiguous()
+    return t.to(torch.device("cuda", index), non_blocking=True).contiguous()
 
 
-def _call(fn, dev, *args):
-    """fn on dev and dev's current stream (the last argument)."""
-    index = dev.index
+def _call(fn, index, *args):
+    """fn on CUDA device `index` and its current stream (the last argument)."""
     if torch.cuda.current_device() == index:
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc:
         _check(rc)
 
 
-def _paged(pages, scales, table, dtype, B, H, N, P) -> PagedCache:
+def _paged(pages, scales, table, dtype, B, H, N, P, index) -> PagedCache:
     """The C description of a paged cache, after checking it against the shapes it has to hold."""
-    dev = pages.device
-    if dev.type != "cuda":
+    if index < 0:
         raise ValueError("pages must be a contiguous CUDA tensor")
     if pages.dim() != 5 or table.dim() != 2:
         raise ValueError(f"expected pages of 5 dimensions and a table of 2, got {tuple(pages.shape)} and {tuple(table.shape)}")
     npages, _, R, _, _ = pages.shape
     width = table.shape[1]
-    tp = _need("table", table, (B, width), torch.int32, dev)
-    if pages.dtype == torch.uint8:
+    tp = _need("table", table, (B, width), torch.int32, index)
+    if pages.dtype is torch.uint8:
         if scales is None:
             raise TypeError("4-bit (uint8) pages need their uint8 scales")
-        return PagedCache(DART_CACHE_MXFP4, npages, R, width, _need("pages", pages, (npages, H, R, P, N // 2), torch.uint8, dev),
-                          _need("scales", scales, (npages, H, R, P, N // 32), torch.uint8, dev), tp)
+        return PagedCache(DART_CACHE_MXFP4, npages, R, width, _need("pages", pages, (npages, H, R, P, N // 2), torch.uint8, index),
+                          _need("scales", scales, (npages, H, R, P, N // 32), torch.uint8, index), tp)
     if scales is not None:
         raise ValueError("scales belong to 4-bit (uint8) pages")
-    return PagedCache(DART_CACHE_DTYPE, npages, R, width, _need("pages", pages, (npages, H, R, N, P), dtype, dev), None, tp)
+    return PagedCache(DART_CACHE_DTYPE, npages, R, width, _need("pages", pages, (npages, H, R, N, P), dtype, index), None, tp)
 
 
-def _move_pages(fn, dense, name, first, count, pages, table, scales, order):
-    B, H, C, N, P = dense.shape
-    dev = pages.device
-    cache = _paged(pages, scales, table, dense.dtype, B, H, N, P)
-    dense_ptr = _need(name, dense, (B, H, C, N, P), dense.dtype, dev)
+def _move_pages(fn, write, dense, first, count, pages, table, scales):
+    B, H, C, N, P = shape = dense.shape
+    dev = pages.get_device()
+    cache = ctypes.byref(_paged(pages, scales, table, dense.dtype, B, H, N, P, dev))
+    d = _need("dH" if write else "out", dense, shape, dense.dtype, dev)
     f, c = _need("first", first, (B,), torch.int32, dev), _need("count", count, (B,), torch.int32, dev)
-    dims = Dims(B, 0, H, P, N, 1, 1)
-    _call(fn, dev, ctypes.byref(dims), _dtype_code(dense.dtype), *order(dense_ptr, C, f, c, ctypes.byref(cache)))
+    dims = ctypes.byref(Dims(B, 0, H, P, N, 1, 1))
+    _call(fn, dev, dims, _dtype_code(dense.dtype), *((d, C, f, c, cache) if write else (cache, f, c, d, C)))
 
 
 def dart_cache_write_paged(dH, first, count, pages, table, *, scales=None):
@@ -642,8 +642,7 @@ def dart_cache_write_paged(dH, first, count, pages, table, *, scales=None):
     i < count[b].  dH [B,H,C,N,P] (float32 or bfloat16, e.g. dart_ssd_chunk_scan's
     memories), first and count int32 [B], pages/scales in place; all on the
     device.  uint8 pages take 4-bit codes.  Returns (pages, scales)."""
-    _move_pages(load().dart_cache_write_paged, dH, "dH", first, count, pages, table, scales,
-                lambda d, C, f, c, cache: (d, C, f, c, cache))
+    _move_pages(load().dart_cache_write_paged, True, dH, first, count, pages, table, scales)
     return pages, scales
 
 
@@ -651,8 +650,7 @@ def dart_cache_read_paged(pages, table, first, count, *, out, scales=None):
     """Memories out of pages: out[b, :, i] = memory first[b] + i of sequence b for
     i < count[b]; other entries of out [B,H,C,N,P] (float32 or bfloat16; the
     pages' dtype unless they hold 4-bit codes) are left as they are.  Returns out."""
-    _move_pages(load().dart_cache_read_paged, out, "out", first, count, pages, table, scales,
-                lambda d, C, f, c, cache: (cache, f, c, d, C))
+    _move_pages(load().dart_cache_read_paged, False, out, first, count, pages, table, scales)
     return out
 
 
@@ -671,31 +669,25 @@ def dart_ssd_extend(x, dt, A, Bm, Cm, cu_tokens, state, dH_cur, pages, table, nc
     float32 [T,H,P], state, dH_cur, nchunks, pos (after the run) and mem_count
     int32 [T] for dart_sma_paged.  Rows no sequence owns are not written."""
     lib = load()
-    dev = pages.device
-    f32, i32 = torch.float32, torch.int32
-    x, Bm, Cm = (_input(v, dev, x.dtype) for v in (x, Bm, Cm))
-    dt, A = _input(dt, dev, f32), _input(A, dev, f32)
-    T, H, P = x.shape
-    B, _, N, _ = shape = state.shape
-    _shape("state", state, (B, H, N, P))
+    dev = pages.get_device()
+    f32, i32, dtype = torch.float32, torch.int32, x.dtype
+    B, H, N, P = shape = state.shape
+    cache = _paged(pages, scales, table, dtype, B, H, N, P, dev)
+    x, Bm, Cm = _input(x, dtype, dev), _input(Bm, dtype, dev), _input(Cm, dtype, dev)
+    dt, A = _input(dt, f32, dev), _input(A, f32, dev)
+    T = x.shape[0]
     G = _bc_groups("Bm", Bm, (T,), H)
     if Bm.shape[-1] != N or Cm.shape != Bm.shape:
         raise ValueError("Bm and Cm must both be [T,N] or [T,G,N] with the state's N")
-    cache = _paged(pages, scales, table, x.dtype, B, H, N, P)
     state_out = state if state_out is None else state_out
     dH_cur_out = dH_cur if dH_cur_out is None else dH_cur_out
-    if nchunks_out is None:
-        nchunks_out = torch.empty((B,), dtype=i32, device=dev)
-    if pos_out is None:
-        pos_out = torch.empty((B,), dtype=i32, device=dev)
-    if y is None:
-        y = torch.empty((T, H, P), device=dev, dtype=f32)
-    if mem_count is None:
-        mem_count = torch.empty((T,), device=dev, dtype=i32)
-    dims = Dims(B, T, H, P, N, chunk, G)
-    _call(lib.dart_ssd_extend, dev, ctypes.byref(dims), _dtype_code(x.dtype), x.data_ptr(),
-          _need("dt", dt, (T, H), f32, dev), _need("A", A, (H,), f32, dev), Bm.data_ptr(), Cm.data_ptr(),
-          _need("cu_tokens", cu_tokens, (B + 1,), i32, dev),
+    nchunks_out = torch.empty_like(nchunks) if nchunks_out is None else nchunks_out
+    pos_out = torch.empty_like(pos) if pos_out is None else pos_out
+    y = torch.empty_like(x, dtype=f32) if y is None else y
+    mem_count = cu_tokens.new_empty(T) if mem_count is None else mem_count
+    _call(lib.dart_ssd_extend, dev, ctypes.byref(Dims(B, T, H, P, N, chunk, G)), _dtype_code(dtype),
+          _need("x", x, (T, H, P), dtype, dev), _need("dt", dt, (T, H), f32, dev), _need("A", A, (H,), f32, dev),
+          Bm.data_ptr(), Cm.data_ptr(), _need("cu_tokens", cu_tokens, (B + 1,), i32, dev),
           _need("state", state, shape, f32, dev), _need("state_out", state_out, shape, f32, dev),
           _need("dH_cur", dH_cur, shape, f32, dev), _need("dH_cur_out", dH_cur_out, shape, f32, dev),
           ctypes.byref(cache), _need("nchunks", nchunks, (B,), i32, dev), _need("pos", pos, (B,), i32, dev),
@@ -714,38 +706,32 @@ def dart_sma_paged(Q, E, Cm, cu_tokens, pages, table, mem_count, g: float, y_ssd
     [T,H,P] equal to y_ssd + g*o (or o when y_ssd is None), token t of sequence b
     seeing the sequence's first mem_count[t] memories (int32 [T], as
     dart_ssd_extend returns it; -1 leaves the row as it is).  Q[T,H,N], E[T,H,P],
-    Cm[T,N] or [T,G,N] in one dtype.  out may be y_ssd itself.  workspace: uint8,
-    dart_sma_paged_workspace_bytes() of them; calls that may overlap need one
-    each.  Rows no sequence owns are not written."""
+    Cm[T,N] or [T,G,N] in one dtype.  out may be y_ssd itself.  workspace: a tensor of
+    dart_sma_paged_workspace_bytes bytes; calls that may overlap need one each.  Rows no sequence owns are not written."""
     lib = load()
-    dev = pages.device
-    f32, dtype = torch.float32, Q.dtype
-    Q, E, Cm = _input(Q, dev, dtype), _input(E, dev, dtype), _input(Cm, dev, dtype)
+    dev = pages.get_device()
+    f32, i32, dtype = torch.float32, torch.int32, Q.dtype
     T, H, N = Q.shape
     P = E.shape[-1]
     B = table.shape[0]
-    if E.shape != (T, H, P):
-        raise ValueError(f"E: expected shape {(T, H, P)}, got {tuple(E.shape)}")
+    cache = _paged(pages, scales, table, dtype, B, H, N, P, dev)
+    Q, E, Cm = _input(Q, dtype, dev), _input(E, dtype, dev), _input(Cm, dtype, dev)
     G = _bc_groups("Cm", Cm, (T,), H)
     if Cm.shape[-1] != N:
         raise ValueError(f"Cm: expected {N} columns, got {Cm.shape[-1]}")
-    cache = _paged(pages, scales, table, dtype, B, H, N, P)
-    yp = None
-    if y_ssd is not None:
-        y_ssd = _input(y_ssd, dev, f32)
-        yp = _need("y_ssd", y_ssd, (T, H, P), f32, dev)
-    if out is None:
-        out = torch.empty((T, H, P), device=dev, dtype=f32)
-    dims = Dims(B, T, H, P, N, 1, G)
+    shape = (T, H, P)
+    yp = None if y_ssd is None else _need("y_ssd", y_ssd, shape, f32, dev)
+    out = torch.empty_like(E, dtype=f32) if out is None else out
+    dims = ctypes.byref(Dims(B, T, H, P, N, 1, G))
     if workspace is None:
         n = _SMA_PAGED_WORKSPACE.get(P)
         if n is None:
-            n = _SMA_PAGED_WORKSPACE[P] = lib.dart_sma_paged_workspace_bytes(ctypes.byref(dims))
-        workspace = torch.empty((n,), device=dev, dtype=torch.uint8)
-    _call(lib.dart_sma_paged, dev, ctypes.byref(dims), _dtype_code(dtype), Q.data_ptr(), E.data_ptr(), Cm.data_ptr(),
-          _need("cu_tokens", cu_tokens, (B + 1,), torch.int32, dev), ctypes.byref(cache),
-          _need("mem_count", mem_count, (T,), torch.int32, dev), float(g), yp, _need("out", out, (T, H, P), f32, dev),
-          _need("workspace", workspace, workspace.shape, torch.uint8, dev), workspace.numel())
+            n = _SMA_PAGED_WORKSPACE[P] = lib.dart_sma_paged_workspace_bytes(dims)
+        workspace = table.new_empty(n // 4)
+    _call(lib.dart_sma_paged, dev, dims, _dtype_code(dtype), Q.data_ptr(), _need("E", E, shape, dtype, dev), Cm.data_ptr(),
+          _need("cu_tokens", cu_tokens, (B + 1,), i32, dev), ctypes.byref(cache),
+          _need("mem_count", mem_count, (T,), i32, dev), g, yp, _need("out", out, shape, f32, dev),
+          _need("workspace", workspace, workspace.shape, workspace.dtype, dev), workspace.numel() * workspace.element_size())
     return out
 
 
