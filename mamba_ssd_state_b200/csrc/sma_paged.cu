@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) sma_paged_kernel(SmaPagedArgs a) {
 
 // Block i joins the item that begins in run i and ends in a later one.
 template <int TT, int P>
-__global__ void __launch_bounds__(128) sma_paged_combine_kernel(SmaPagedArgs a, int runs) {
+__global__ void __launch_bounds__(512) sma_paged_combine_kernel(SmaPagedArgs a, int runs) {
     sm100::griddep_wait();
     const PieceHeader hd = *piece_header(a.part, blockIdx.x, 1);
     if (hd.state != 1) return;
@@ -257,23 +257,22 @@ cudaError_t paged_allow_smem(const void* kernel, int bytes, std::atomic<unsigned
 }
 
 cudaError_t launch_sma_paged_combine(const SmaPagedArgs& a, int runs, int tt, cudaStream_t st) {
-    cudaError_t e;
-    if (a.P == 64)
-        e = tt == 8 ? launch_dependent(sma_paged_combine_kernel<8, 64>, dim3(runs), dim3(128), 0, st, 1, a, runs)
-                    : launch_dependent(sma_paged_combine_kernel<4, 64>, dim3(runs), dim3(128), 0, st, 1, a, runs);
-    else
-        e = launch_dependent(sma_paged_combine_kernel<8, 16>, dim3(runs), dim3(128), 0, st, 1, a, runs);
+    auto kern = a.P != 64 ? sma_paged_combine_kernel<8, 16> : tt == 4 ? sma_paged_combine_kernel<4, 64>
+                : tt == 8 ? sma_paged_combine_kernel<8, 64> : sma_paged_combine_kernel<128, 64>;
+    const cudaError_t e = launch_dependent(kern, dim3(runs), dim3(tt == 128 ? 512 : 128), 0, st, 1, a, runs);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
 
 size_t sma_paged_workspace_bytes(int P) {
-    return 2 * (size_t)kMaxRuns * (sizeof(PieceHeader) + sizeof(float) * kTT * (2 + (size_t)P));
+    static_assert(kMaxTcRuns * 128 >= kMaxRuns * kTT, "rows of the pieces");
+    return 2 * (kMaxRuns * sizeof(PieceHeader) + kMaxTcRuns * 128 * sizeof(float) * (2 + (size_t)P));
 }
 long long sma_paged_tiles(int B, int T) { return B + (long long)T / 4; }   // of 4 rows, the smallest tiles
 long long sma_paged_max_tiles() { return kCap; }
 
 cudaError_t launch_sma_paged(const SmaPagedArgs& a, dart_dtype dt, cudaStream_t st) {
+    if (sma_paged_tc_applicable(a, dt)) return launch_sma_paged_tc(a, st);
     if (a.P == 64 && (a.cache.mxfp4 || dt == DART_BF16)) return launch_sma_paged_mma(a, dt, st);
     if (a.N == 128 && a.P == 64 && dt == DART_F32) return run<float, 128, 64>(a, st);
     if (a.N == 64 && a.P == 64 && dt == DART_F32) return run<float, 64, 64>(a, st);

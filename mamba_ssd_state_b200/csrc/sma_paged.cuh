@@ -34,10 +34,15 @@ constexpr int kMaxRuns = 2048;   // runs of any of the kernels
 // a sequence without memories took twice as long as its other items.
 constexpr int kItemUnits = 4;
 
+constexpr int kMaxTcRuns = 160;  // of the kernel with 128-row tiles
+
 // Joins the pieces that the runs of a kernel with tiles of tt rows left.
 cudaError_t launch_sma_paged_combine(const SmaPagedArgs& a, int runs, int tt, cudaStream_t st);
 // sma_paged_mma.cu: bfloat16 and 4-bit memories with P = 64, runs of few tokens.
 cudaError_t launch_sma_paged_mma(const SmaPagedArgs& a, dart_dtype dt, cudaStream_t st);
+// sma_paged_tc.cu: bfloat16 memories with P = 64, long runs.
+bool sma_paged_tc_applicable(const SmaPagedArgs& a, dart_dtype dt);
+cudaError_t launch_sma_paged_tc(const SmaPagedArgs& a, cudaStream_t st);
 // Multiprocessors of the current device, looked up once; 0 on failure.
 int paged_sm_count();
 // Allows a kernel its dynamic shared memory on the current device, once for each

@@ -1,0 +1,367 @@
+// sma_paged_tc.cu -- state-memory attention of long runs of new tokens (pieces of
+// a prompt) over paged bfloat16 memories, on tcgen05.
+//
+// The formulas are sma_paged_mma.cu's; the shape is the prefill kernel's
+// (sma_tc.cu): a tile of 128 rows of one (sequence, head) is the M of two MMAs a
+// batch of four memories, U = Q_T M and V = C_T M (N = 4 P = 256, K = dstate),
+// with the accumulators in TMEM (U in columns 0..255, V in 256..511).  Reading a
+// memory once for 128 tokens instead of 8 makes the run compute-bound:
+// 4 x 256 tokens over 100 memories took 470 us on warp-level products, where
+// every 8 tokens stream all memories through the SM again, and take 130 here.
+//
+// What differs from prefill: memories come from pages, a tile ends with its
+// sequence (rows behind it belong to others and are not written), every row has
+// its own count, and items are cut into equal runs of units (sma_paged.cuh), so
+// that a few long sequences fill the machine; an item that falls into several
+// runs is joined by the combine kernel.
+//
+// Roles (320 threads): warp 0 issues TMA, warp 1 the MMAs, warps 2-9 are four
+// pairs, one for each TMEM lane quadrant (32 rows); a pair splits the 64 value
+// columns, exchanges partial scores through shared memory and runs the same
+// online softmax.
+#include <string.h>
+
+#include "sm100.cuh"
+#include "sma_paged.cuh"
+#include "tensor_map.h"
+
+namespace dart {
+namespace {
+
+using namespace sm100;
+
+constexpr int kP = 64;
+constexpr int kRows = 128;         // rows of a tile (MMA M)
+constexpr int kCB = 4;             // memories of a batch (MMA N = 256)
+constexpr int kCap = 1024;         // tiles of a call
+constexpr int kLeast = 8;          // units below which a run is not cut
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr uint32_t kPanel = kRows * 64 * 2;      // 128 rows x 64 bfloat16, one swizzle panel
+constexpr uint32_t kTmemCols = 512, kColV = 256;
+constexpr int kHalfP = kP / 2;
+
+enum Bar { Q_FULL, Q_FREE, C_FULL, C_FREE, U_FULL, U_EMPTY, V_FULL, V_EMPTY, B_FULL0 };
+
+template <int N>
+struct Smem {
+    static constexpr int kStages = 2 * 128 / N;
+    static constexpr uint32_t kMemBytes = N * kP * 2, kStageBytes = kCB * kMemBytes;
+    uint8_t q[N / 64 * kPanel], c[N / 64 * kPanel];
+    uint8_t ring[kStages * kStageBytes];
+    float4 scores[2][2][kRows];                  // [batch parity][half][row]: partial scores of four memories
+    uint64_t bars[B_FULL0 + 2 * kStages];
+    uint32_t tmem;
+    int abort_flag;
+    TileList<kCap> tiles;
+};
+
+struct Params {
+    CUtensorMap map_q, map_c;     // (N, H, T) and (N, G, T), boxes (64, 1, 128)
+    CUtensorMap map_m;            // (P, rows of N), boxes of one memory
+    SmaPagedArgs a;
+};
+
+template <int N>
+__global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_constant__ Params prm) {
+    using S = Smem<N>;
+    extern __shared__ uint8_t raw[];
+    S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const SmaPagedArgs& a = prm.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto bar = [&](int i) { return smem_u32(&s.bars[i]); };
+    auto full = [&](int st) { return bar(B_FULL0 + st); };
+    auto empty = [&](int st) { return bar(B_FULL0 + S::kStages + st); };
+    if (tid == 0) {
+        for (int i = 0; i < B_FULL0 + 2 * S::kStages; ++i) mbar_init(bar(i), i == U_EMPTY || i == V_EMPTY ? kEpiWarps : 1);
+        s.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&s.tmem), kTmemCols);
+        tmem_relinquish();
+    }
+    griddep_wait();
+    if (tid < 2) piece_header(a.part, blockIdx.x, tid)->state = 0;
+    tc_fence_before();
+    build_tiles<kRows, kCap>(a, s.tiles);        // (orders the set-up above for all threads)
+    tc_fence_after();
+    const uint32_t tmem = s.tmem;
+    const WaitCtx wc{&s.abort_flag, a.status, 11};
+    bool ok = true;
+    Walk w;
+    w.u = w.end = 0;
+    if (s.tiles.n > 0) w = start_walk(s.tiles, a.H, blockIdx.x, gridDim.x, kLeast);
+    // memories [first, last) of the piece that can be read
+    auto table_of = [&]() { return a.cache.table + (size_t)s.tiles.seq[w.k] * a.cache.width; };
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA
+        uint32_t ph = 0;          // of Q_FREE and C_FREE
+        int it = 0, q_filled = 0;
+        for (; ok && next_piece(w); advance(s.tiles, w, a.H)) {
+            const int* table = table_of();
+            const int bad = first_bad_memory(table, a.cache, w.memories());
+            if (bad < w.memories() && lane == 0) flag_status(a.status, kStatusDevice);
+            const int first = w.first_memory(), last = min(w.last_memory(), bad);
+            if (first >= last) continue;
+            for (int c0 = first; c0 < last; c0 += kCB, ++it) {
+                const int nv = min(kCB, last - c0), st = it % S::kStages;
+                // lane i looks up memory i of the batch
+                const int c = c0 + (lane < nv ? lane : 0);
+                const size_t mem = memory_index(a.cache, a.H, table[c / a.cache.R], w.h, c % a.cache.R);
+                if (!(ok = mbar_wait_warp(empty(st), ((uint32_t)(it / S::kStages) & 1u) ^ 1u, wc, 3))) break;
+                if (lane == 0) mbar_expect_tx(full(st), (uint32_t)nv * S::kMemBytes);
+                __syncwarp();
+                if (lane < nv)
+                    tma_load_2d(smem_u32(s.ring + (size_t)st * S::kStageBytes + (size_t)lane * S::kMemBytes), &prm.map_m, full(st), 0,
+                                (int)(mem * N));
+                __syncwarp();
+                if (c0 == first) {
+                    const int t0 = s.tiles.t0[w.k];
+                    if (!(ok = mbar_wait_warp(bar(Q_FREE), ph ^ 1u, wc, 1))) break;
+                    if (lane == 0) {
+                        mbar_expect_tx(bar(Q_FULL), N / 64 * kPanel);
+                        for (int k = 0; k < N / 64; ++k) tma_load_3d(smem_u32(s.q + k * kPanel), &prm.map_q, bar(Q_FULL), 64 * k, w.h, t0);
+                    }
+                    ++q_filled;
+                    if (!(ok = mbar_wait_warp(bar(C_FREE), ph ^ 1u, wc, 2))) break;
+                    if (lane == 0) {
+                        mbar_expect_tx(bar(C_FULL), N / 64 * kPanel);
+                        const int grp = group_of(w.h, a.H, a.G);
+                        for (int k = 0; k < N / 64; ++k) tma_load_3d(smem_u32(s.c + k * kPanel), &prm.map_c, bar(C_FULL), 64 * k, grp, t0);
+                    }
+                    ph ^= 1u;
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            // a wait gave up: copies in flight are waited for (with a limit) before their shared memory goes
+            auto drain = [&](uint32_t b, uint32_t parity) { for (int k = 0; k < (1 << 20) && !mbar_try_wait(b, parity); ++k) {} };
+            for (int i = max(0, it - S::kStages); i < it; ++i) drain(full(i % S::kStages), (uint32_t)(i / S::kStages) & 1u);
+            if (q_filled > 0) {
+                drain(bar(Q_FULL), (uint32_t)(q_filled - 1) & 1u);
+                drain(bar(C_FULL), (uint32_t)(q_filled - 1) & 1u);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA
+        uint32_t ph = 0;
+        int it = 0;
+        for (; ok && next_piece(w); advance(s.tiles, w, a.H)) {
+            const int first = w.first_memory(), last = min(w.last_memory(), first_bad_memory(table_of(), a.cache, w.memories()));
+            if (first >= last) continue;
+            if (!(ok = mbar_wait_warp(bar(Q_FULL), ph, wc, 4))) break;
+            for (int c0 = first; c0 < last; c0 += kCB, ++it) {
+                const int nv = min(kCB, last - c0), st = it % S::kStages;
+                const bool end = c0 + kCB >= last;
+                const uint32_t idesc = idesc_bf16_f32(kRows, kP * nv, false, true);
+                const uint32_t b_base = smem_u32(s.ring + (size_t)st * S::kStageBytes);
+                auto product = [&](uint32_t d, const uint8_t* rows) {
+#pragma unroll
+                    for (int kk = 0; kk < N / 16; ++kk) {
+                        const uint64_t ad = smem_desc_sw128(smem_u32(rows) + (uint32_t)(kk >> 2) * kPanel + (uint32_t)(kk & 3) * 32, 16, 1024);
+                        const uint64_t bd = smem_desc_sw128(b_base + (uint32_t)kk * 2048, S::kMemBytes, 1024);
+                        mma_f16_ss(d, ad, bd, idesc, kk > 0 ? 1u : 0u);
+                    }
+                };
+                if (!(ok = mbar_wait_warp(full(st), (uint32_t)(it / S::kStages) & 1u, wc, 5))) break;
+                if (!(ok = mbar_wait_warp(bar(U_EMPTY), ((uint32_t)it & 1u) ^ 1u, wc, 6))) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    product(tmem, s.q);
+                    mma_commit(bar(U_FULL));
+                    if (end) mma_commit(bar(Q_FREE));
+                }
+                __syncwarp();
+                if (c0 == first && !(ok = mbar_wait_warp(bar(C_FULL), ph, wc, 7))) break;
+                if (!(ok = mbar_wait_warp(bar(V_EMPTY), ((uint32_t)it & 1u) ^ 1u, wc, 8))) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    product(tmem + kColV, s.c);
+                    mma_commit(bar(V_FULL));
+                    mma_commit(empty(st));
+                    if (end) mma_commit(bar(C_FREE));
+                }
+                __syncwarp();
+            }
+            ph ^= 1u;
+        }
+    } else {
+        // ------------------------------------------------------- epilogue
+        // The two warps of a pair run the same batches and the same named barrier
+        // for each, also after a failed wait (they then skip the work).
+        const int quad = warp & 3, half = (warp - 2) >> 2, col0 = half * kHalfP, row = quad * 32 + lane;
+        const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
+        const float sscale = kLog2e * rsqrtf((float)N);
+        int it = 0;
+        for (; next_piece(w); advance(s.tiles, w, a.H)) {
+            const int t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, s.tiles.seq[w.k], t0, kRows);
+            const int bad = first_bad_memory(table_of(), a.cache, w.memories());
+            const int first = w.first_memory(), last = min(w.last_memory(), bad);
+            const bool live = row < rows;
+            const int count = live ? a.mem_count[t0 + row] : -1;
+            const size_t at = ((size_t)(t0 + row) * a.H + w.h) * kP + col0;
+            float2 e2[kHalfP / 2], o2[kHalfP / 2];
+#pragma unroll
+            for (int q = 0; q < kHalfP / 8; ++q) {
+                uint4 v4 = make_uint4(0u, 0u, 0u, 0u);
+                if (live) v4 = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.E) + at) + q);
+                const uint32_t w4[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    e2[4 * q + r] = make_float2(__uint_as_float(w4[r] << 16), __uint_as_float(w4[r] & 0xffff0000u));
+            }
+#pragma unroll
+            for (int j = 0; j < kHalfP / 2; ++j) o2[j] = make_float2(0.f, 0.f);
+            float m = -INFINITY, l = 0.f;
+            for (int c0 = first; c0 < last; c0 += kCB, ++it) {
+                const int nv = min(kCB, last - c0);
+                const uint32_t ph = (uint32_t)it & 1u;
+                float part[kCB] = {0.f, 0.f, 0.f, 0.f};
+                if (ok) ok = mbar_wait_warp(bar(U_FULL), ph, wc, 9);
+                if (ok) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < kCB; ++c) {
+                        if (c < nv) {
+                            float u[kHalfP];
+                            tmem_ld_32x32b_x32(t_lane + (uint32_t)(c * kP + col0), u);
+                            tmem_ld_wait();
+                            float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+#pragma unroll
+                            for (int q = 0; q < kHalfP / 2; q += 2) {
+                                a0 = __ffma2_rn(make_float2(u[2 * q], u[2 * q + 1]), e2[q], a0);
+                                a1 = __ffma2_rn(make_float2(u[2 * q + 2], u[2 * q + 3]), e2[q + 1], a1);
+                            }
+                            part[c] = (a0.x + a1.x) + (a0.y + a1.y);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(U_EMPTY));
+                }
+                // scores: own half and the partner's
+                s.scores[it & 1][half][row] = make_float4(part[0], part[1], part[2], part[3]);
+                named_bar_sync(2 + quad, 64);
+                const float4 pp = s.scores[it & 1][1 - half][row];
+                const float other[kCB] = {pp.x, pp.y, pp.z, pp.w};
+                float sc[kCB], wt[kCB], mn = m;
+#pragma unroll
+                for (int c = 0; c < kCB; ++c) {
+                    // added in the same order by both warps, whose softmax has to be the same
+                    sc[c] = (half ? other[c] + part[c] : part[c] + other[c]) * sscale;
+                    if (c >= nv || c0 + c >= count) sc[c] = -INFINITY;     // not a memory this row sees
+                    mn = fmaxf(mn, sc[c]);
+                }
+                const bool none = mn == -INFINITY;     // only scores of -inf so far: they weigh nothing
+                const float alpha = none ? 1.f : exp2f(m - mn);
+#pragma unroll
+                for (int c = 0; c < kCB; ++c) wt[c] = none ? (sc[c] == sc[c] ? 0.f : sc[c]) : exp2f(sc[c] - mn);
+                l = l * alpha + (wt[0] + wt[1]) + (wt[2] + wt[3]);
+                m = mn;
+                const float2 alpha2 = make_float2(alpha, alpha);
+#pragma unroll
+                for (int q = 0; q < kHalfP / 2; ++q) o2[q] = __fmul2_rn(o2[q], alpha2);
+                if (ok) ok = mbar_wait_warp(bar(V_FULL), ph, wc, 10);
+                if (ok) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < kCB; ++c) {
+                        if (c < nv) {
+                            float v[kHalfP];
+                            tmem_ld_32x32b_x32(t_lane + kColV + (uint32_t)(c * kP + col0), v);
+                            tmem_ld_wait();
+                            if (wt[c] != 0.f) {        // 0 weight reads nothing, whatever the value is
+                                const float2 w2 = make_float2(wt[c], wt[c]);
+#pragma unroll
+                                for (int q = 0; q < kHalfP / 2; ++q)
+                                    o2[q] = __ffma2_rn(w2, make_float2(v[2 * q], v[2 * q + 1]), o2[q]);
+                            }
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(V_EMPTY));
+                }
+            }
+            // a whole item is written out, a part of one kept for the combine kernel
+            const bool left = count < 0 || count > bad;      // a row that is not to be computed
+            const int which = w.c > 0 ? 0 : 1;
+            if (!w.whole() && tid == 64)
+                *piece_header(a.part, blockIdx.x, which) = PieceHeader{w.last == w.units ? 2 : 1, t0, rows, w.h};
+            if (!live) continue;
+            if (w.whole()) {
+                if (left) continue;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                for (int q = 0; q < kHalfP / 4; ++q) {
+                    float4 r = make_float4(o2[2 * q].x * inv, o2[2 * q].y * inv, o2[2 * q + 1].x * inv, o2[2 * q + 1].y * inv);
+                    if (a.y_ssd) {
+                        const float4 y = reinterpret_cast<const float4*>(a.y_ssd + at)[q];
+                        r = make_float4(fmaf(a.g, r.x, y.x), fmaf(a.g, r.y, y.y), fmaf(a.g, r.z, y.z), fmaf(a.g, r.w, y.w));
+                    }
+                    reinterpret_cast<float4*>(a.out + at)[q] = r;
+                }
+            } else {
+                float* to = piece_rows<kRows, kP>(a.part, blockIdx.x, which) + row * (2 + kP);
+                if (half == 0) { to[0] = m; to[1] = left ? -1.f : l; }
+#pragma unroll
+                for (int q = 0; q < kHalfP / 2; ++q) reinterpret_cast<float2*>(to + 2 + col0)[q] = o2[q];
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int N>
+cudaError_t run(const SmaPagedArgs& a, cudaStream_t st) {
+    using S = Smem<N>;
+    static_assert(sizeof(S) + 1024 <= 232448, "shared memory");
+    auto kern = sma_paged_tc_kernel<N>;
+    const int smem = (int)sizeof(S) + 1024, sms = paged_sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    Params p;
+    memset(&p, 0, sizeof(p));
+    p.a = a;
+    const uint32_t box[3] = {64, 1, kRows};
+    {
+        const uint64_t dims[3] = {N, (uint64_t)a.H, (uint64_t)a.T}, strides[2] = {N * 2, (uint64_t)a.H * N * 2};
+        if (!encode_tile_map_bf16(&p.map_q, 3, a.Q, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    {
+        const uint64_t dims[3] = {N, (uint64_t)a.G, (uint64_t)a.T}, strides[2] = {N * 2, (uint64_t)a.G * N * 2};
+        if (!encode_tile_map_bf16(&p.map_c, 3, a.Cm, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    {
+        const uint64_t rows = (uint64_t)a.cache.npages * a.H * a.cache.R * N;
+        if (rows > 0x7fffffffull) return cudaErrorInvalidValue;      // 256 GB and more of memories
+        const uint64_t dims[2] = {kP, rows}, strides[1] = {kP * 2};
+        const uint32_t mbox[2] = {kP, N};
+        if (!encode_tile_map_bf16(&p.map_m, 2, a.cache.pages, dims, strides, mbox)) return cudaErrorInvalidValue;
+    }
+    static std::atomic<unsigned long long> ready{0};   // devices whose kernel has its shared memory allowed
+    cudaError_t e = paged_allow_smem(reinterpret_cast<const void*>(kern), smem, ready);
+    if (e != cudaSuccess) return e;
+    const int blocks = sms < kMaxTcRuns ? sms : kMaxTcRuns;
+    if ((e = launch_dependent(kern, dim3(blocks), dim3(kThreads), smem, st, 1, p)) != cudaSuccess) return e;
+    count_launches(1);
+    return launch_sma_paged_combine(a, blocks, kRows, st);
+}
+
+}  // namespace
+
+bool sma_paged_tc_applicable(const SmaPagedArgs& a, dart_dtype dt) {
+    // a tile of 128 rows costs about as much as two of 8 rows do on warp-level products
+    return dt == DART_BF16 && !a.cache.mxfp4 && a.P == kP && (a.N == 128 || a.N == 64) && a.T >= 16 * (long long)a.B &&
+           a.B + a.T / kRows <= kCap;
+}
+
+cudaError_t launch_sma_paged_tc(const SmaPagedArgs& a, cudaStream_t st) { return a.N == 128 ? run<128>(a, st) : run<64>(a, st); }
+
+}  // namespace dart
