@@ -187,33 +187,70 @@ __global__ void __launch_bounds__(kThreads) sma_paged_kernel(SmaPagedArgs a) {
     }
 }
 
-// Block i joins the item that begins in run i and ends in a later one.
+// Block (i, y) joins eight rows, from row 8 y on, of the item that begins in run i
+// and ends in a later one.  A thread has one column of one row, and where there
+// are fewer rows than eight, every n-th of the item's pieces: an item of one row
+// may be spread over all runs, and its pieces are then read by many.
+constexpr int kJoinThreads = 512;
+
 template <int TT, int P>
-__global__ void __launch_bounds__(512) sma_paged_combine_kernel(SmaPagedArgs a, int runs) {
+__global__ void __launch_bounds__(kJoinThreads) sma_paged_combine_kernel(SmaPagedArgs a, int runs) {
+    constexpr int SUB = kJoinThreads / P;     // threads of a column
+    constexpr int AHEAD = 4;                  // pieces read at a time
     sm100::griddep_wait();
     const PieceHeader hd = *piece_header(a.part, blockIdx.x, 1);
-    if (hd.state != 1) return;
-    int end = blockIdx.x + 1;                 // the run that has the item's last piece
-    while (end < runs && piece_header(a.part, end, 0)->state != 2) ++end;
-    for (int i = threadIdx.x; i < hd.rows * P; i += blockDim.x) {
-        const int t = i / P, p = i % P;
-        const float* row = piece_rows<TT, P>(a.part, blockIdx.x, 1) + t * (2 + P);
-        float m = row[0], l = row[1], o = row[2 + p];
-        if (l < 0.f) continue;
-        for (int j = blockIdx.x + 1; j <= end && j < runs; ++j) {
-            if (piece_header(a.part, j, 0)->state == 0) continue;
-            const float* r = piece_rows<TT, P>(a.part, j, 0) + t * (2 + P);
-            if (r[1] == 0.f) continue;        // saw nothing
-            const float mn = fmaxf(m, r[0]);
-            const float f = l == 0.f ? 0.f : exp2f(m - mn), k = exp2f(r[0] - mn);
-            l = fmaf(l, f, r[1] * k);
-            o = (f == 0.f ? 0.f : o * f) + r[2 + p] * k;
-            m = mn;
-        }
-        const size_t at = ((size_t)(hd.t0 + t) * a.H + hd.h) * P + p;
-        const float oo = l == 0.f ? 0.f : o / l;
-        a.out[at] = a.y_ssd ? fmaf(a.g, oo, a.y_ssd[at]) : oo;
+    const int r0 = 8 * blockIdx.y, rows = min(8, hd.rows - r0);
+    if (hd.state != 1 || rows <= 0) return;
+    const int lane = threadIdx.x & 31;
+    int end = runs;                           // the run that has the item's last piece
+    for (int j = blockIdx.x + 1; j < runs && end == runs; j += 32) {
+        const unsigned hit = __ballot_sync(0xffffffffu, j + lane < runs && piece_header(a.part, j + lane, 0)->state == 2);
+        if (hit) end = j + __ffs(hit) - 1;
     }
+    const int rp = rows > 4 ? 8 : rows > 2 ? 4 : rows, groups = SUB / rp;     // rows as a power of two
+    const int p = threadIdx.x % P, sub = threadIdx.x / P, t = sub % rp, grp = sub / rp;
+    __shared__ float sm[SUB][P], sl[SUB][P], so[SUB][P];
+    float m = -INFINITY, l = 0.f, o = 0.f;
+    auto add = [&](float m2, float l2, float o2) {
+        if (l2 == 0.f) return;                // saw nothing
+        const float mn = fmaxf(m, m2);
+        const float f = l == 0.f ? 0.f : exp2f(m - mn), k = exp2f(m2 - mn);
+        l = fmaf(l, f, l2 * k);
+        o = (f == 0.f ? 0.f : o * f) + o2 * k;
+        m = mn;
+    };
+    bool left = false;
+    if (t < rows) {
+        const size_t at = (size_t)(r0 + t) * (2 + P);
+        const float* own = piece_rows<TT, P>(a.part, blockIdx.x, 1) + at;
+        left = own[1] < 0.f;                  // a row that is not to be computed
+        if (grp == 0 && !left) add(own[0], own[1], own[2 + p]);
+        for (int j = blockIdx.x + 1 + grp; j <= end && j < runs && !left; j += AHEAD * groups) {
+            float m2[AHEAD], l2[AHEAD], o2[AHEAD];
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const int k = j + u * groups;
+                l2[u] = 0.f;
+                if (k <= end && k < runs && piece_header(a.part, k, 0)->state != 0) {
+                    const float* r = piece_rows<TT, P>(a.part, k, 0) + at;
+                    m2[u] = r[0];
+                    l2[u] = r[1];
+                    o2[u] = r[2 + p];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) add(m2[u], l2[u], o2[u]);
+        }
+    }
+    sm[sub][p] = m;
+    sl[sub][p] = l;
+    so[sub][p] = o;
+    __syncthreads();
+    if (grp != 0 || t >= rows || left) return;
+    for (int k = 1; k < groups; ++k) add(sm[sub + k * rp][p], sl[sub + k * rp][p], so[sub + k * rp][p]);
+    const size_t at = ((size_t)(hd.t0 + r0 + t) * a.H + hd.h) * P + p;
+    const float r = l == 0.f ? 0.f : o / l;
+    a.out[at] = a.y_ssd ? fmaf(a.g, r, a.y_ssd[at]) : r;
 }
 
 template <typename T, int N, int P>
@@ -258,8 +295,9 @@ cudaError_t paged_allow_smem(const void* kernel, int bytes, std::atomic<unsigned
 
 cudaError_t launch_sma_paged_combine(const SmaPagedArgs& a, int runs, int tt, cudaStream_t st) {
     auto kern = a.P != 64 ? sma_paged_combine_kernel<8, 16> : tt == 4 ? sma_paged_combine_kernel<4, 64>
-                : tt == 8 ? sma_paged_combine_kernel<8, 64> : sma_paged_combine_kernel<128, 64>;
-    const cudaError_t e = launch_dependent(kern, dim3(runs), dim3(tt == 128 ? 512 : 128), 0, st, 1, a, runs);
+                : tt == 8 ? sma_paged_combine_kernel<8, 64>
+                : tt == 128 ? sma_paged_combine_kernel<128, 64> : sma_paged_combine_kernel<256, 64>;
+    const cudaError_t e = launch_dependent(kern, dim3(runs, (tt + 7) / 8), dim3(kJoinThreads), 0, st, 1, a, runs);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }

@@ -15,6 +15,14 @@
 // that a few long sequences fill the machine; an item that falls into several
 // runs is joined by the combine kernel.
 //
+// CTA pairs (runs of more than 128 tokens on average): two CTAs of a cluster run
+// the two halves of a 256-row tile as M = 256 MMAs (cta_group::2).  Each loads
+// its own rows of Q and C and two memories of a batch, so an SM takes in half
+// the bytes for each product and its ring holds twice the batches: with single
+// CTAs the ring's latency bounds a batch (64 KB for every 2048 cycles of MMA is
+// 9 TB/s over all SMs).  CTA 0 issues the MMAs and owns the barriers they wait
+// on; the peer's copies complete on them and its epilogue arrives there.
+//
 // Roles (320 threads): warp 0 issues TMA, warp 1 the MMAs, warps 2-9 are four
 // pairs, one for each TMEM lane quadrant (32 rows); a pair splits the 64 value
 // columns, exchanges partial scores through shared memory and runs the same
@@ -31,7 +39,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kP = 64;
-constexpr int kRows = 128;         // rows of a tile (MMA M)
+constexpr int kRows = 128;         // rows of a CTA (MMA M, or half of it)
 constexpr int kCB = 4;             // memories of a batch (MMA N = 256)
 constexpr int kCap = 1024;         // tiles of a call
 constexpr int kLeast = 8;          // units below which a run is not cut
@@ -43,10 +51,11 @@ constexpr int kHalfP = kP / 2;
 
 enum Bar { Q_FULL, Q_FREE, C_FULL, C_FREE, U_FULL, U_EMPTY, V_FULL, V_EMPTY, B_FULL0 };
 
-template <int N>
+template <int N, bool kPair>
 struct Smem {
-    static constexpr int kStages = 2 * 128 / N;
-    static constexpr uint32_t kMemBytes = N * kP * 2, kStageBytes = kCB * kMemBytes;
+    static constexpr int kMem = kPair ? kCB / 2 : kCB;           // memories of a stage (this CTA's of a batch)
+    static constexpr int kStages = 8 / kMem * 128 / N;           // 128 KB
+    static constexpr uint32_t kMemBytes = N * kP * 2, kStageBytes = kMem * kMemBytes;
     uint8_t q[N / 64 * kPanel], c[N / 64 * kPanel];
     uint8_t ring[kStages * kStageBytes];
     float4 scores[2][2][kRows];                  // [batch parity][half][row]: partial scores of four memories
@@ -62,37 +71,47 @@ struct Params {
     SmaPagedArgs a;
 };
 
-template <int N>
+template <int N, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_constant__ Params prm) {
-    using S = Smem<N>;
+    using S = Smem<N, kPair>;
+    constexpr int TT = kPair ? 2 * kRows : kRows;
     extern __shared__ uint8_t raw[];
     S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const SmaPagedArgs& a = prm.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = kPair ? (int)cluster_ctarank() : 0;
+    const int run = kPair ? (int)blockIdx.x / 2 : (int)blockIdx.x, runs = kPair ? (int)gridDim.x / 2 : (int)gridDim.x;
     auto bar = [&](int i) { return smem_u32(&s.bars[i]); };
     auto full = [&](int st) { return bar(B_FULL0 + st); };
     auto empty = [&](int st) { return bar(B_FULL0 + S::kStages + st); };
+    auto lead = [&](uint32_t b) { return kPair ? mapa_shared(b, 0) : b; };      // the barrier in CTA 0
     if (tid == 0) {
-        for (int i = 0; i < B_FULL0 + 2 * S::kStages; ++i) mbar_init(bar(i), i == U_EMPTY || i == V_EMPTY ? kEpiWarps : 1);
+        for (int i = 0; i < B_FULL0 + 2 * S::kStages; ++i) mbar_init(bar(i), i == U_EMPTY || i == V_EMPTY ? kEpiWarps * (kPair ? 2 : 1) : 1);
         s.abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(&s.tmem), kTmemCols);
-        tmem_relinquish();
+        if constexpr (kPair) {
+            tmem_alloc_pair(smem_u32(&s.tmem), kTmemCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(&s.tmem), kTmemCols);
+            tmem_relinquish();
+        }
     }
     griddep_wait();
-    if (tid < 2) piece_header(a.part, blockIdx.x, tid)->state = 0;
+    if (tid < 2 && rank == 0) piece_header(a.part, run, tid)->state = 0;
+    build_tiles<TT, kCap>(a, s.tiles);
     tc_fence_before();
-    build_tiles<kRows, kCap>(a, s.tiles);        // (orders the set-up above for all threads)
+    if (kPair) cluster_sync();                   // both CTAs' barriers exist before any remote arrive or copy
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     const WaitCtx wc{&s.abort_flag, a.status, 11};
     bool ok = true;
     Walk w;
     w.u = w.end = 0;
-    if (s.tiles.n > 0) w = start_walk(s.tiles, a.H, blockIdx.x, gridDim.x, kLeast);
-    // memories [first, last) of the piece that can be read
+    if (s.tiles.n > 0) w = start_walk(s.tiles, a.H, run, runs, kLeast);
     auto table_of = [&]() { return a.cache.table + (size_t)s.tiles.seq[w.k] * a.cache.width; };
     if (warp == 0) {
         // ------------------------------------------------------------ TMA
@@ -106,36 +125,41 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
             if (first >= last) continue;
             for (int c0 = first; c0 < last; c0 += kCB, ++it) {
                 const int nv = min(kCB, last - c0), st = it % S::kStages;
-                // lane i looks up memory i of the batch
-                const int c = c0 + (lane < nv ? lane : 0);
+                // lane i looks up memory i of this CTA's
+                const int q0 = S::kMem * rank, mine = max(0, min(S::kMem, nv - q0));
+                const int c = c0 + (lane < mine ? q0 + lane : 0);
                 const size_t mem = memory_index(a.cache, a.H, table[c / a.cache.R], w.h, c % a.cache.R);
                 if (!(ok = mbar_wait_warp(empty(st), ((uint32_t)(it / S::kStages) & 1u) ^ 1u, wc, 3))) break;
-                if (lane == 0) mbar_expect_tx(full(st), (uint32_t)nv * S::kMemBytes);
+                if (lane == 0 && rank == 0) mbar_expect_tx(full(st), (uint32_t)nv * S::kMemBytes);
                 __syncwarp();
-                if (lane < nv)
-                    tma_load_2d(smem_u32(s.ring + (size_t)st * S::kStageBytes + (size_t)lane * S::kMemBytes), &prm.map_m, full(st), 0,
-                                (int)(mem * N));
+                if (lane < mine) {
+                    const uint32_t dst = smem_u32(s.ring + (size_t)st * S::kStageBytes + (size_t)lane * S::kMemBytes);
+                    if constexpr (kPair) tma_load_2d_pair(dst, &prm.map_m, lead(full(st)), 0, (int)(mem * N));
+                    else tma_load_2d(dst, &prm.map_m, full(st), 0, (int)(mem * N));
+                }
                 __syncwarp();
                 if (c0 == first) {
-                    const int t0 = s.tiles.t0[w.k];
+                    const int t0 = s.tiles.t0[w.k] + rank * kRows, grp = group_of(w.h, a.H, a.G);
+                    auto rows = [&](const uint8_t* to, const CUtensorMap* map, int b, int head) {
+                        if (rank == 0) mbar_expect_tx(bar(b), (kPair ? 2 : 1) * (N / 64) * kPanel);
+#pragma unroll
+                        for (int k = 0; k < N / 64; ++k) {
+                            if constexpr (kPair) tma_load_3d_pair(smem_u32(to + k * kPanel), map, lead(bar(b)), 64 * k, head, t0);
+                            else tma_load_3d(smem_u32(to + k * kPanel), map, bar(b), 64 * k, head, t0);
+                        }
+                    };
                     if (!(ok = mbar_wait_warp(bar(Q_FREE), ph ^ 1u, wc, 1))) break;
-                    if (lane == 0) {
-                        mbar_expect_tx(bar(Q_FULL), N / 64 * kPanel);
-                        for (int k = 0; k < N / 64; ++k) tma_load_3d(smem_u32(s.q + k * kPanel), &prm.map_q, bar(Q_FULL), 64 * k, w.h, t0);
-                    }
+                    if (lane == 0) rows(s.q, &prm.map_q, Q_FULL, w.h);
                     ++q_filled;
                     if (!(ok = mbar_wait_warp(bar(C_FREE), ph ^ 1u, wc, 2))) break;
-                    if (lane == 0) {
-                        mbar_expect_tx(bar(C_FULL), N / 64 * kPanel);
-                        const int grp = group_of(w.h, a.H, a.G);
-                        for (int k = 0; k < N / 64; ++k) tma_load_3d(smem_u32(s.c + k * kPanel), &prm.map_c, bar(C_FULL), 64 * k, grp, t0);
-                    }
+                    if (lane == 0) rows(s.c, &prm.map_c, C_FULL, grp);
                     ph ^= 1u;
                 }
             }
         }
-        if (!ok && lane == 0) {
-            // a wait gave up: copies in flight are waited for (with a limit) before their shared memory goes
+        if (!ok && rank == 0 && lane == 0) {
+            // a wait gave up: copies in flight (the peer's complete here too, and it stays until this CTA is done)
+            // are waited for, with a limit, before their shared memory goes
             auto drain = [&](uint32_t b, uint32_t parity) { for (int k = 0; k < (1 << 20) && !mbar_try_wait(b, parity); ++k) {} };
             for (int i = max(0, it - S::kStages); i < it; ++i) drain(full(i % S::kStages), (uint32_t)(i / S::kStages) & 1u);
             if (q_filled > 0) {
@@ -144,8 +168,12 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------------ MMA
+        auto commit = [&](uint32_t b) {
+            if constexpr (kPair) mma_commit_pair(b);
+            else mma_commit(b);
+        };
         uint32_t ph = 0;
         int it = 0;
         for (; ok && next_piece(w); advance(s.tiles, w, a.H)) {
@@ -155,14 +183,16 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
             for (int c0 = first; c0 < last; c0 += kCB, ++it) {
                 const int nv = min(kCB, last - c0), st = it % S::kStages;
                 const bool end = c0 + kCB >= last;
-                const uint32_t idesc = idesc_bf16_f32(kRows, kP * nv, false, true);
+                // a pair multiplies all four column blocks (the epilogue reads the valid ones): N splits over the CTAs
+                const uint32_t idesc = idesc_bf16_f32(TT, kPair ? kP * kCB : kP * nv, false, true);
                 const uint32_t b_base = smem_u32(s.ring + (size_t)st * S::kStageBytes);
                 auto product = [&](uint32_t d, const uint8_t* rows) {
 #pragma unroll
                     for (int kk = 0; kk < N / 16; ++kk) {
                         const uint64_t ad = smem_desc_sw128(smem_u32(rows) + (uint32_t)(kk >> 2) * kPanel + (uint32_t)(kk & 3) * 32, 16, 1024);
                         const uint64_t bd = smem_desc_sw128(b_base + (uint32_t)kk * 2048, S::kMemBytes, 1024);
-                        mma_f16_ss(d, ad, bd, idesc, kk > 0 ? 1u : 0u);
+                        if constexpr (kPair) mma_f16_ss_pair(d, ad, bd, idesc, kk > 0 ? 1u : 0u);
+                        else mma_f16_ss(d, ad, bd, idesc, kk > 0 ? 1u : 0u);
                     }
                 };
                 if (!(ok = mbar_wait_warp(full(st), (uint32_t)(it / S::kStages) & 1u, wc, 5))) break;
@@ -170,8 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
                 tc_fence_after();
                 if (lane == 0) {
                     product(tmem, s.q);
-                    mma_commit(bar(U_FULL));
-                    if (end) mma_commit(bar(Q_FREE));
+                    commit(bar(U_FULL));
+                    if (end) commit(bar(Q_FREE));
                 }
                 __syncwarp();
                 if (c0 == first && !(ok = mbar_wait_warp(bar(C_FULL), ph, wc, 7))) break;
@@ -179,15 +209,15 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
                 tc_fence_after();
                 if (lane == 0) {
                     product(tmem + kColV, s.c);
-                    mma_commit(bar(V_FULL));
-                    mma_commit(empty(st));
-                    if (end) mma_commit(bar(C_FREE));
+                    commit(bar(V_FULL));
+                    commit(empty(st));
+                    if (end) commit(bar(C_FREE));
                 }
                 __syncwarp();
             }
             ph ^= 1u;
         }
-    } else {
+    } else if (warp >= 2) {
         // ------------------------------------------------------- epilogue
         // The two warps of a pair run the same batches and the same named barrier
         // for each, also after a failed wait (they then skip the work).
@@ -196,12 +226,13 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
         const float sscale = kLog2e * rsqrtf((float)N);
         int it = 0;
         for (; next_piece(w); advance(s.tiles, w, a.H)) {
-            const int t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, s.tiles.seq[w.k], t0, kRows);
+            const int t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, s.tiles.seq[w.k], t0, TT);
+            const int tr = rank * kRows + row;         // row of the tile
             const int bad = first_bad_memory(table_of(), a.cache, w.memories());
             const int first = w.first_memory(), last = min(w.last_memory(), bad);
-            const bool live = row < rows;
-            const int count = live ? a.mem_count[t0 + row] : -1;
-            const size_t at = ((size_t)(t0 + row) * a.H + w.h) * kP + col0;
+            const bool live = tr < rows;
+            const int count = live ? a.mem_count[t0 + tr] : -1;
+            const size_t at = ((size_t)(t0 + tr) * a.H + w.h) * kP + col0;
             float2 e2[kHalfP / 2], o2[kHalfP / 2];
 #pragma unroll
             for (int q = 0; q < kHalfP / 8; ++q) {
@@ -239,7 +270,10 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(U_EMPTY));
+                    if (lane == 0) {
+                        if constexpr (kPair) mbar_arrive_cluster(lead(bar(U_EMPTY)));
+                        else mbar_arrive(bar(U_EMPTY));
+                    }
                 }
                 // scores: own half and the partner's
                 s.scores[it & 1][half][row] = make_float4(part[0], part[1], part[2], part[3]);
@@ -282,14 +316,17 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(V_EMPTY));
+                    if (lane == 0) {
+                        if constexpr (kPair) mbar_arrive_cluster(lead(bar(V_EMPTY)));
+                        else mbar_arrive(bar(V_EMPTY));
+                    }
                 }
             }
             // a whole item is written out, a part of one kept for the combine kernel
             const bool left = count < 0 || count > bad;      // a row that is not to be computed
             const int which = w.c > 0 ? 0 : 1;
-            if (!w.whole() && tid == 64)
-                *piece_header(a.part, blockIdx.x, which) = PieceHeader{w.last == w.units ? 2 : 1, t0, rows, w.h};
+            if (!w.whole() && tid == 64 && rank == 0)
+                *piece_header(a.part, run, which) = PieceHeader{w.last == w.units ? 2 : 1, t0, rows, w.h};
             if (!live) continue;
             if (w.whole()) {
                 if (left) continue;
@@ -304,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
                     reinterpret_cast<float4*>(a.out + at)[q] = r;
                 }
             } else {
-                float* to = piece_rows<kRows, kP>(a.part, blockIdx.x, which) + row * (2 + kP);
+                float* to = piece_rows<TT, kP>(a.part, run, which) + tr * (2 + kP);
                 if (half == 0) { to[0] = m; to[1] = left ? -1.f : l; }
 #pragma unroll
                 for (int q = 0; q < kHalfP / 2; ++q) reinterpret_cast<float2*>(to + 2 + col0)[q] = o2[q];
@@ -312,18 +349,44 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
         }
     }
     tc_fence_before();
-    __syncthreads();
+    if (kPair) cluster_sync();   // neither CTA leaves while the other may still reach its memory
+    else __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        if constexpr (kPair) tmem_dealloc_pair(tmem, kTmemCols);
+        else tmem_dealloc(tmem, kTmemCols);
     }
 }
 
-template <int N>
+// How many clusters of two can be resident (not every SM need pair up), once per device.
+cudaError_t resident_pairs(const void* kern, int sms, int smem, std::atomic<int> (&cache)[64], int& pairs) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    pairs = dev < 64 ? cache[dev].load(std::memory_order_relaxed) : 0;
+    if (pairs > 0) return cudaSuccess;
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2 * (unsigned)(sms / 2));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg)) != cudaSuccess) return e;
+    if (pairs <= 0) return cudaErrorInvalidConfiguration;
+    if (dev < 64) cache[dev].store(pairs, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+template <int N, bool kPair>
 cudaError_t run(const SmaPagedArgs& a, cudaStream_t st) {
-    using S = Smem<N>;
+    using S = Smem<N, kPair>;
     static_assert(sizeof(S) + 1024 <= 232448, "shared memory");
-    auto kern = sma_paged_tc_kernel<N>;
+    auto kern = sma_paged_tc_kernel<N, kPair>;
     const int smem = (int)sizeof(S) + 1024, sms = paged_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     Params p;
@@ -348,10 +411,15 @@ cudaError_t run(const SmaPagedArgs& a, cudaStream_t st) {
     static std::atomic<unsigned long long> ready{0};   // devices whose kernel has its shared memory allowed
     cudaError_t e = paged_allow_smem(reinterpret_cast<const void*>(kern), smem, ready);
     if (e != cudaSuccess) return e;
-    const int blocks = sms < kMaxTcRuns ? sms : kMaxTcRuns;
-    if ((e = launch_dependent(kern, dim3(blocks), dim3(kThreads), smem, st, 1, p)) != cudaSuccess) return e;
+    int runs = sms < kMaxTcRuns ? sms : kMaxTcRuns;
+    if constexpr (kPair) {
+        static std::atomic<int> cache[64];
+        if ((e = resident_pairs(reinterpret_cast<const void*>(kern), sms, smem, cache, runs)) != cudaSuccess) return e;
+        if (runs > kMaxTcRuns / 2) runs = kMaxTcRuns / 2;
+    }
+    if ((e = launch_dependent(kern, dim3(kPair ? 2 * runs : runs), dim3(kThreads), smem, st, kPair ? 2 : 1, p)) != cudaSuccess) return e;
     count_launches(1);
-    return launch_sma_paged_combine(a, blocks, kRows, st);
+    return launch_sma_paged_combine(a, runs, kPair ? 2 * kRows : kRows, st);
 }
 
 }  // namespace
@@ -362,6 +430,9 @@ bool sma_paged_tc_applicable(const SmaPagedArgs& a, dart_dtype dt) {
            a.B + a.T / kRows <= kCap;
 }
 
-cudaError_t launch_sma_paged_tc(const SmaPagedArgs& a, cudaStream_t st) { return a.N == 128 ? run<128>(a, st) : run<64>(a, st); }
+cudaError_t launch_sma_paged_tc(const SmaPagedArgs& a, cudaStream_t st) {
+    if (a.T > 128 * (long long)a.B) return a.N == 128 ? run<128, true>(a, st) : run<64, true>(a, st);
+    return a.N == 128 ? run<128, false>(a, st) : run<64, false>(a, st);
+}
 
 }  // namespace dart

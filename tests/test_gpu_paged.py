@@ -370,6 +370,64 @@ def test_attention_rows_with_bad_pages_or_counts_are_left(N, P, dtype, cache, H,
     assert rel_err(out[done], o[done]) <= TOL
 
 
+@pytest.mark.parametrize("N, P, dtype, cache, H, G", [v for v in SHAPES if v[3] != "f32" and v[1] == 64])
+@pytest.mark.parametrize("lens, mems, R", [([20, 33], [6, 5], 4), ([64, 0, 128, 1, 200], [9, 3, 2, 5, 13], 3), ([257], [50], 16),
+                                           ([300, 100, 260], [4, 1, 7], 2), ([129, 128], [0, 21], 5)])
+def test_attention_of_long_runs(N, P, dtype, cache, H, G, lens, mems, R):
+    """Runs that fill tiles of 128 and 256 rows and end inside them; a page of the last sequence is missing, and rows
+    whose count reaches it are left as they are, and so are those marked with -1."""
+    rng = np.random.default_rng(sum(lens) + sum(mems) + N)
+    memories = memories_of(rng, mems, H, N, P, cache, scale=0.5)
+    pool = Pool(memories, H, N, P, R, cache, rng)
+    T = sum(lens)
+    args, args64 = attention_inputs(rng, T + 3, H, G, N, P, dtype)
+    counts = [min(m, max(0, m - 2 + i * 3 // k)) for k, m in zip(lens, mems) for i in range(k)]
+    counts[3] = 0
+    o = ref.sma(*[v[:T] for v in args64], lens, memories, counts)
+    seen = np.array(counts)
+    bad = mems[-1] > R
+    if bad:
+        pool.table[len(lens) - 1, (mems[-1] - 1) // R] = -1
+        last = np.arange(T) >= T - lens[-1]
+        left = last & (seen > (mems[-1] - 1) // R * R)
+    else:
+        left = np.zeros(T, bool)
+    seen[T // 2] = -1
+    left[T // 2] = True
+    y, y64 = cast(rng.standard_normal((T + 3, H, P)) * 0.1, "f32")
+    want = np.where(left[:, None, None], 5.0, y64[:T] + 0.7 * o)
+    out = torch.full_like(y, 5.0)
+    call = lambda to: dart.dart_sma_paged(*args, cumulative(lens), pool.pages, pool.table, ints(*seen.tolist(), 9, 9, 9), 0.7, y,
+                                          scales=pool.scales, out=to)
+    call(out)
+    if bad:
+        with pytest.raises(dart.DartError):
+            dart.dart_sync_status()
+    else:
+        dart.dart_sync_status()
+    assert rel_err(out[:T], want) <= TOL and (out[T:] == 5.0).all()
+    again = torch.full_like(y, 5.0)
+    call(again)
+    assert torch.equal(again, out)
+    if bad:
+        with pytest.raises(dart.DartError):
+            dart.dart_sync_status()
+
+
+@pytest.mark.parametrize("N, P, dtype, cache, H, G", [v for v in SHAPES if v[3] == "bf16" and v[1] == 64])
+@pytest.mark.parametrize("lens", [[40], [150]])
+def test_long_runs_over_many_memories_are_shared_by_blocks(N, P, dtype, cache, H, G, lens):
+    rng = np.random.default_rng(N + H + lens[0])
+    memories = memories_of(rng, [700], H, N, P, cache, scale=0.5)
+    pool = Pool(memories, H, N, P, 16, cache, rng)
+    args, args64 = attention_inputs(rng, lens[0], H, G, N, P, dtype)
+    counts = [700 - (i % 5) for i in range(lens[0])]
+    counts[1], counts[2] = 3, 0
+    out = dart.dart_sma_paged(*args, cumulative(lens), pool.pages, pool.table, ints(*counts), 1.0, scales=pool.scales)
+    dart.dart_sync_status()
+    assert rel_err(out, ref.sma(*args64, lens, memories, counts)) <= TOL
+
+
 def test_a_shared_page_is_read_by_two_sequences():
     rng = np.random.default_rng(9)
     H, N, P, R = 2, 128, 64, 4
