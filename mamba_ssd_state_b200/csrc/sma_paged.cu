@@ -179,27 +179,25 @@ __global__ void __launch_bounds__(kThreads) sma_paged_kernel(SmaPagedArgs a) {
                 const float r = l == 0.f ? 0.f : o / l;
                 a.out[at] = a.y_ssd ? fmaf(a.g, r, a.y_ssd[at]) : r;
             } else {
-                float* row = piece_rows<kTT, P>(a.part, blockIdx.x, which) + t * (2 + P);
-                if (p == 0) { row[0] = mm; row[1] = left ? -1.f : l; }
-                row[2 + p] = o;
+                float* row = piece_rows<kTT, P>(a.part, blockIdx.x, which) + t * (P + 4);
+                if (p == 0) { row[P] = mm; row[P + 1] = left ? -1.f : l; }
+                row[p] = o;
             }
         }
     }
 }
 
-// Block (i, y) joins eight rows, from row 8 y on, of the item that begins in run i
-// and ends in a later one.  A thread has one column of one row, and where there
-// are fewer rows than eight, every n-th of the item's pieces: an item of one row
-// may be spread over all runs, and its pieces are then read by many.
-constexpr int kJoinThreads = 512;
-
-template <int TT, int P>
-__global__ void __launch_bounds__(kJoinThreads) sma_paged_combine_kernel(SmaPagedArgs a, int runs) {
-    constexpr int SUB = kJoinThreads / P;     // threads of a column
-    constexpr int AHEAD = 4;                  // pieces read at a time
+// Block (i, y) joins ROWS rows, from row ROWS y on, of the item that begins in
+// run i and ends in a later one (most blocks find none and leave).  A thread has four columns of one row,
+// and where there are fewer rows than threads for them, every n-th of the item's
+// pieces: an item of one row may be spread over all runs, and many read it then.
+template <int TT, int P, int ROWS>
+__global__ void __launch_bounds__(ROWS * P / 4) sma_paged_combine_kernel(SmaPagedArgs a, int runs) {
+    constexpr int COLS = P / 4, SUB = ROWS;                  // threads of a row, of a column
+    constexpr int AHEAD = 4;                                 // pieces read at a time
     sm100::griddep_wait();
     const PieceHeader hd = *piece_header(a.part, blockIdx.x, 1);
-    const int r0 = 8 * blockIdx.y, rows = min(8, hd.rows - r0);
+    const int r0 = ROWS * blockIdx.y, rows = min(ROWS, hd.rows - r0);
     if (hd.state != 1 || rows <= 0) return;
     const int lane = threadIdx.x & 31;
     int end = runs;                           // the run that has the item's last piece
@@ -207,50 +205,59 @@ __global__ void __launch_bounds__(kJoinThreads) sma_paged_combine_kernel(SmaPage
         const unsigned hit = __ballot_sync(0xffffffffu, j + lane < runs && piece_header(a.part, j + lane, 0)->state == 2);
         if (hit) end = j + __ffs(hit) - 1;
     }
-    const int rp = rows > 4 ? 8 : rows > 2 ? 4 : rows, groups = SUB / rp;     // rows as a power of two
-    const int p = threadIdx.x % P, sub = threadIdx.x / P, t = sub % rp, grp = sub / rp;
-    __shared__ float sm[SUB][P], sl[SUB][P], so[SUB][P];
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    auto add = [&](float m2, float l2, float o2) {
+    int rp = 1;                               // rows as a power of two
+    while (rp < rows) rp *= 2;
+    const int groups = SUB / rp, p = 4 * (threadIdx.x % COLS), sub = threadIdx.x / COLS, t = sub % rp, grp = sub / rp;
+    __shared__ float sm[SUB], sl[SUB];
+    __shared__ float4 so[SUB][COLS];
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float m2, float l2, const float4& o2) {
         if (l2 == 0.f) return;                // saw nothing
         const float mn = fmaxf(m, m2);
         const float f = l == 0.f ? 0.f : exp2f(m - mn), k = exp2f(m2 - mn);
         l = fmaf(l, f, l2 * k);
-        o = (f == 0.f ? 0.f : o * f) + o2 * k;
+        o = f == 0.f ? make_float4(o2.x * k, o2.y * k, o2.z * k, o2.w * k)
+                     : make_float4(o.x * f + o2.x * k, o.y * f + o2.y * k, o.z * f + o2.z * k, o.w * f + o2.w * k);
         m = mn;
     };
     bool left = false;
+    const size_t at = ((size_t)(hd.t0 + r0 + t) * a.H + hd.h) * P + p;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
     if (t < rows) {
-        const size_t at = (size_t)(r0 + t) * (2 + P);
-        const float* own = piece_rows<TT, P>(a.part, blockIdx.x, 1) + at;
-        left = own[1] < 0.f;                  // a row that is not to be computed
-        if (grp == 0 && !left) add(own[0], own[1], own[2 + p]);
+        const size_t off = (size_t)(r0 + t) * (P + 4);
+        const float* own = piece_rows<TT, P>(a.part, blockIdx.x, 1) + off;
+        if (grp == 0 && a.y_ssd) y = *reinterpret_cast<const float4*>(a.y_ssd + at);
+        left = own[P + 1] < 0.f;              // a row that is not to be computed
+        if (grp == 0 && !left) add(own[P], own[P + 1], *reinterpret_cast<const float4*>(own + p));
         for (int j = blockIdx.x + 1 + grp; j <= end && j < runs && !left; j += AHEAD * groups) {
-            float m2[AHEAD], l2[AHEAD], o2[AHEAD];
+            float m2[AHEAD], l2[AHEAD];
+            float4 o2[AHEAD];
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u) {
                 const int k = j + u * groups;
                 l2[u] = 0.f;
                 if (k <= end && k < runs && piece_header(a.part, k, 0)->state != 0) {
-                    const float* r = piece_rows<TT, P>(a.part, k, 0) + at;
-                    m2[u] = r[0];
-                    l2[u] = r[1];
-                    o2[u] = r[2 + p];
+                    const float* r = piece_rows<TT, P>(a.part, k, 0) + off;
+                    m2[u] = r[P];
+                    l2[u] = r[P + 1];
+                    o2[u] = *reinterpret_cast<const float4*>(r + p);
                 }
             }
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u) add(m2[u], l2[u], o2[u]);
         }
     }
-    sm[sub][p] = m;
-    sl[sub][p] = l;
-    so[sub][p] = o;
-    __syncthreads();
+    if (groups > 1) {
+        if (p == 0) { sm[sub] = m; sl[sub] = l; }
+        so[sub][p / 4] = o;
+        __syncthreads();
+        if (grp == 0)
+            for (int k = 1; k < groups; ++k) add(sm[sub + k * rp], sl[sub + k * rp], so[sub + k * rp][p / 4]);
+    }
     if (grp != 0 || t >= rows || left) return;
-    for (int k = 1; k < groups; ++k) add(sm[sub + k * rp][p], sl[sub + k * rp][p], so[sub + k * rp][p]);
-    const size_t at = ((size_t)(hd.t0 + r0 + t) * a.H + hd.h) * P + p;
-    const float r = l == 0.f ? 0.f : o / l;
-    a.out[at] = a.y_ssd ? fmaf(a.g, r, a.y_ssd[at]) : r;
+    const float f = l == 0.f ? 0.f : (a.y_ssd ? a.g : 1.f) / l;
+    *reinterpret_cast<float4*>(a.out + at) = make_float4(fmaf(f, o.x, y.x), fmaf(f, o.y, y.y), fmaf(f, o.z, y.z), fmaf(f, o.w, y.w));
 }
 
 template <typename T, int N, int P>
@@ -294,17 +301,18 @@ cudaError_t paged_allow_smem(const void* kernel, int bytes, std::atomic<unsigned
 }
 
 cudaError_t launch_sma_paged_combine(const SmaPagedArgs& a, int runs, int tt, cudaStream_t st) {
-    auto kern = a.P != 64 ? sma_paged_combine_kernel<8, 16> : tt == 4 ? sma_paged_combine_kernel<4, 64>
-                : tt == 8 ? sma_paged_combine_kernel<8, 64>
-                : tt == 128 ? sma_paged_combine_kernel<128, 64> : sma_paged_combine_kernel<256, 64>;
-    const cudaError_t e = launch_dependent(kern, dim3(runs, (tt + 7) / 8), dim3(kJoinThreads), 0, st, 1, a, runs);
+    const int rows = tt < 32 ? 8 : 32;
+    auto kern = a.P != 64 ? sma_paged_combine_kernel<8, 16, 8> : tt == 4 ? sma_paged_combine_kernel<4, 64, 8>
+                : tt == 8 ? sma_paged_combine_kernel<8, 64, 8>
+                : tt == 128 ? sma_paged_combine_kernel<128, 64, 32> : sma_paged_combine_kernel<256, 64, 32>;
+    const cudaError_t e = launch_dependent(kern, dim3(runs, (tt + rows - 1) / rows), dim3(rows * a.P / 4), 0, st, 1, a, runs);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
 
 size_t sma_paged_workspace_bytes(int P) {
     static_assert(kMaxTcRuns * 128 >= kMaxRuns * kTT, "rows of the pieces");
-    return 2 * (kMaxRuns * sizeof(PieceHeader) + kMaxTcRuns * 128 * sizeof(float) * (2 + (size_t)P));
+    return 2 * (kMaxRuns * sizeof(PieceHeader) + kMaxTcRuns * 128 * sizeof(float) * ((size_t)P + 4));
 }
 long long sma_paged_tiles(int B, int T) { return B + (long long)T / 4; }   // of 4 rows, the smallest tiles
 long long sma_paged_max_tiles() { return kCap; }

@@ -21,7 +21,8 @@
 namespace dart {
 
 // Workspace: per run a header for its first and its last piece, then the pieces,
-// rows of 2 + P floats.
+// rows of P + 4 floats: the weighted values, the maximum, the sum (-1 for a row
+// that is not to be computed) and two that keep rows 16-byte aligned.
 struct PieceHeader {
     int state;    // 0: no such piece, 1: more pieces follow, 2: the item ends here
     int t0;       // first token row of the tile
@@ -115,22 +116,26 @@ __device__ __forceinline__ void build_tiles(const SmaPagedArgs& a, TileList<CAP>
         n = min(CAP, n + total);
     }
     __syncthreads();
+    // the units of every tile: a thread reads the counts of a small one, a warp those of a large one
+    constexpr int BY = TT < 32 ? 1 : 32;
+    for (int k = tid / BY; k < n; k += threads / BY) {
+        const int t0 = L.t0[k], rows = tile_rows(a.cu, L.seq[k], t0, TT);
+        int most = 0;
+#pragma unroll 8
+        for (int r = tid % BY; r < rows; r += BY) {
+            const int c = a.mem_count[t0 + r];
+            bad |= c < -1 || c > limit;
+            most = max(most, usable_count(c, limit));
+        }
+        if (BY == 32) most = __reduce_max_sync(0xffffffffu, most);
+        if (tid % BY == 0) L.pre[k] = most + kItemUnits;
+    }
+    __syncthreads();
     int sum = 0;
     for (int k0 = 0; k0 < n; k0 += threads) {
         const int k = k0 + tid;
-        int most = 0;
-        if (k < n) {
-            const int t0 = L.t0[k], rows = tile_rows(a.cu, L.seq[k], t0, TT);
-#pragma unroll 8
-            for (int r = 0; r < rows; ++r) {
-                const int c = a.mem_count[t0 + r];
-                bad |= c < -1 || c > limit;
-                most = max(most, usable_count(c, limit));
-            }
-            most += kItemUnits;
-        }
         int total;
-        const int at = sum + block_scan(most, L.scan, total);
+        const int at = sum + block_scan(k < n ? L.pre[k] : 0, L.scan, total);
         if (k < n) L.pre[k] = at;
         sum += total;
     }
@@ -162,12 +167,19 @@ __device__ __forceinline__ int tile_of(const TileList<CAP>& L, int H, long long 
     return lo;
 }
 
+// a / b for a >= 0, b > 0, in 32 bits where they do (a 64-bit division takes about
+// a hundred instructions, and every worker starts with a few).
+__device__ __forceinline__ long long quick_div(long long a, long long b) {
+    if ((unsigned long long)(a | b) < (1ull << 32)) return (unsigned)a / (unsigned)b;
+    return a / b;
+}
+
 // Run i of `runs`; runs of fewer than `least` units are not cut smaller, and a
 // cut that falls into the units that stand for an item goes before them.
 template <int CAP>
 __device__ __forceinline__ Walk start_walk(const TileList<CAP>& L, int H, int i, int runs, int least) {
     const long long W = (long long)L.pre[L.n] * H;
-    const long long G = min((long long)runs, (W + least - 1) / least);
+    const long long G = W < (long long)runs * least ? quick_div(W + least - 1, least) : runs;
     Walk w;
     auto cut = [&](long long u) {      // leaves w at the cut
         w.u = u;
@@ -177,8 +189,8 @@ __device__ __forceinline__ Walk start_walk(const TileList<CAP>& L, int H, int i,
         w.k = tile_of(L, H, u);
         w.units = L.pre[w.k + 1] - L.pre[w.k];
         const long long r = u - (long long)L.pre[w.k] * H;
-        w.h = (int)(r / w.units);
-        w.c = (int)(r % w.units);
+        w.h = (int)quick_div(r, w.units);
+        w.c = (int)(r - (long long)w.h * w.units);
         if (w.c < kItemUnits) {
             w.u -= w.c;
             w.c = 0;
@@ -190,9 +202,10 @@ __device__ __forceinline__ Walk start_walk(const TileList<CAP>& L, int H, int i,
         w.end = W;
         return w;
     }
-    cut(W * (i + 1) / G);
+    const long long each = quick_div(W, G), more = W - each * G;      // the first `more` runs have one unit more
+    cut((i + 1) * each + min((long long)i + 1, more));
     w.end = w.u;
-    cut(W * i / G);
+    cut(i * each + min((long long)i, more));
     return w;
 }
 // The next piece; false at the end of the run.
@@ -220,7 +233,7 @@ __device__ __forceinline__ PieceHeader* piece_header(float* part, int run, int w
 }
 template <int TT, int P>
 __device__ __forceinline__ float* piece_rows(float* part, int run, int which) {
-    return part + 2 * kMaxRuns * (sizeof(PieceHeader) / sizeof(float)) + (size_t)(2 * run + which) * TT * (2 + P);
+    return part + 2 * kMaxRuns * (sizeof(PieceHeader) / sizeof(float)) + (size_t)(2 * run + which) * TT * (P + 4);
 }
 
 // First memory of sequence row `table` whose page is no page, among the first

@@ -414,12 +414,12 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const W
                     a.out[p] = a.y_ssd ? fmaf(a.g, v, a.y_ssd[p]) : v;
                 }
         } else {
-            float* row = piece_rows<TT, kP>(a.part, run, which) + t * (2 + kP);
-            if (g == 0) { row[0] = mx[j]; row[1] = left ? -1.f : l[j]; }
+            float* row = piece_rows<TT, kP>(a.part, run, which) + t * (kP + 4);
+            if (g == 0) { row[kP] = mx[j]; row[kP + 1] = left ? -1.f : l[j]; }
 #pragma unroll
             for (int m = 0; m < 4; ++m)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) row[2 + g + 16 * m + 8 * r] = o[m][2 * r + j] * vs[j];
+                for (int r = 0; r < 2; ++r) row[g + 16 * m + 8 * r] = o[m][2 * r + j] * vs[j];
         }
     }
 }

@@ -7,7 +7,7 @@
 // with the accumulators in TMEM (U in columns 0..255, V in 256..511).  Reading a
 // memory once for 128 tokens instead of 8 makes the run compute-bound:
 // 4 x 256 tokens over 100 memories took 470 us on warp-level products, where
-// every 8 tokens stream all memories through the SM again, and take 130 here.
+// every 8 tokens stream all memories through the SM again, and take 92 here.
 //
 // What differs from prefill: memories come from pages, a tile ends with its
 // sequence (rows behind it belong to others and are not written), every row has
@@ -71,6 +71,22 @@ struct Params {
     SmaPagedArgs a;
 };
 
+// v[j] of lane i and v[i] of lane j change places.
+__device__ __forceinline__ void transpose32(float* v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) {
+        const bool up = (lane & s) != 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if ((i & s) == 0) {
+                const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + s], s);
+                if (up) v[i] = got;
+                else v[i + s] = got;
+            }
+    }
+}
+
 template <int N, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_constant__ Params prm) {
     using S = Smem<N, kPair>;
@@ -119,6 +135,19 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
         int it = 0, q_filled = 0;
         for (; ok && next_piece(w); advance(s.tiles, w, a.H)) {
             const int* table = table_of();
+            {   // the rows that the epilogue starts and ends with, while it is still at the last piece
+                const int t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, s.tiles.seq[w.k], t0, TT);
+#pragma unroll
+                for (int r = rank * kRows + lane; r < (rank + 1) * kRows; r += 32)
+                    if (r < rows) {
+                        const size_t at = ((size_t)(t0 + r) * a.H + w.h) * kP;
+                        prefetch_l2(static_cast<const __nv_bfloat16*>(a.E) + at);
+                        if (a.y_ssd && w.whole()) {
+                            prefetch_l2(a.y_ssd + at);
+                            prefetch_l2(a.y_ssd + at + kP / 2);
+                        }
+                    }
+            }
             const int bad = first_bad_memory(table, a.cache, w.memories());
             if (bad < w.memories() && lane == 0) flag_status(a.status, kStatusDevice);
             const int first = w.first_memory(), last = min(w.last_memory(), bad);
@@ -228,17 +257,19 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
         for (; next_piece(w); advance(s.tiles, w, a.H)) {
             const int t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, s.tiles.seq[w.k], t0, TT);
             const int tr = rank * kRows + row;         // row of the tile
-            const int bad = first_bad_memory(table_of(), a.cache, w.memories());
-            const int first = w.first_memory(), last = min(w.last_memory(), bad);
             const bool live = tr < rows;
             const int count = live ? a.mem_count[t0 + tr] : -1;
             const size_t at = ((size_t)(t0 + tr) * a.H + w.h) * kP + col0;
             float2 e2[kHalfP / 2], o2[kHalfP / 2];
+            uint4 er[kHalfP / 8];
+#pragma unroll
+            for (int q = 0; q < kHalfP / 8; ++q)
+                er[q] = live ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.E) + at) + q) : make_uint4(0u, 0u, 0u, 0u);
+            const int bad = first_bad_memory(table_of(), a.cache, w.memories());
+            const int first = w.first_memory(), last = min(w.last_memory(), bad);
 #pragma unroll
             for (int q = 0; q < kHalfP / 8; ++q) {
-                uint4 v4 = make_uint4(0u, 0u, 0u, 0u);
-                if (live) v4 = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.E) + at) + q);
-                const uint32_t w4[4] = {v4.x, v4.y, v4.z, v4.w};
+                const uint32_t w4[4] = {er[q].x, er[q].y, er[q].z, er[q].w};
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     e2[4 * q + r] = make_float2(__uint_as_float(w4[r] << 16), __uint_as_float(w4[r] & 0xffff0000u));
@@ -327,24 +358,38 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
             const int which = w.c > 0 ? 0 : 1;
             if (!w.whole() && tid == 64 && rank == 0)
                 *piece_header(a.part, run, which) = PieceHeader{w.last == w.units ? 2 : 1, t0, rows, w.h};
-            if (!live) continue;
+            // Rows are written whole: the 32 rows x 32 columns of a warp change places, so that a lane has a column.
+            float* v = reinterpret_cast<float*>(o2);
             if (w.whole()) {
-                if (left) continue;
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float f = l == 0.f ? 0.f : (a.y_ssd ? a.g : 1.f) / l;
 #pragma unroll
-                for (int q = 0; q < kHalfP / 4; ++q) {
-                    float4 r = make_float4(o2[2 * q].x * inv, o2[2 * q].y * inv, o2[2 * q + 1].x * inv, o2[2 * q + 1].y * inv);
-                    if (a.y_ssd) {
-                        const float4 y = reinterpret_cast<const float4*>(a.y_ssd + at)[q];
-                        r = make_float4(fmaf(a.g, r.x, y.x), fmaf(a.g, r.y, y.y), fmaf(a.g, r.z, y.z), fmaf(a.g, r.w, y.w));
-                    }
-                    reinterpret_cast<float4*>(a.out + at)[q] = r;
+                for (int q = 0; q < kHalfP / 2; ++q) o2[q] = __fmul2_rn(o2[q], make_float2(f, f));
+            } else if (live && half == 0) {
+                float* to = piece_rows<TT, kP>(a.part, run, which) + tr * (kP + 4);
+                to[kP] = m;
+                to[kP + 1] = left ? -1.f : l;
+            }
+            transpose32(v);
+            const unsigned mask = __ballot_sync(0xffffffffu, live && !(w.whole() && left));
+            const int r0 = rank * kRows + quad * 32;
+            if (w.whole()) {
+                const size_t base = ((size_t)(t0 + r0) * a.H + w.h) * kP + col0 + lane;
+                const size_t stride = (size_t)a.H * kP;
+                if (a.y_ssd) {
+                    float y[32];      // all loads before the first store: out may be y_ssd itself
+#pragma unroll
+                    for (int r = 0; r < 32; ++r) y[r] = mask >> r & 1u ? a.y_ssd[base + r * stride] : 0.f;
+#pragma unroll
+                    for (int r = 0; r < 32; ++r) v[r] += y[r];
                 }
-            } else {
-                float* to = piece_rows<TT, kP>(a.part, run, which) + tr * (2 + kP);
-                if (half == 0) { to[0] = m; to[1] = left ? -1.f : l; }
 #pragma unroll
-                for (int q = 0; q < kHalfP / 2; ++q) reinterpret_cast<float2*>(to + 2 + col0)[q] = o2[q];
+                for (int r = 0; r < 32; ++r)
+                    if (mask >> r & 1u) a.out[base + r * stride] = v[r];
+            } else {
+                float* to = piece_rows<TT, kP>(a.part, run, which) + (size_t)r0 * (kP + 4) + col0 + lane;
+#pragma unroll
+                for (int r = 0; r < 32; ++r)
+                    if (mask >> r & 1u) to[r * (kP + 4)] = v[r];
             }
         }
     }
