@@ -7,6 +7,8 @@
 // 4-bit format, codes [npages, H, R, P, N/2] and scales [npages, H, R, P, N/32].
 #pragma once
 
+#include <atomic>
+
 #include "dart_common.cuh"
 
 namespace dart {
@@ -59,6 +61,14 @@ bool paged_supported(int N, int P, int mxfp4);
 cudaError_t launch_cache_write(const CacheCopyArgs& a, dart_dtype dt, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheCopyArgs& a, dart_dtype dt, cudaStream_t st);
 cudaError_t launch_ssd_extend(const ExtendArgs& a, dart_dtype dt, cudaStream_t st);
+// ssd_extend_mma.cu: bfloat16 tokens with P = 64, long runs.
+bool ssd_extend_mma_applicable(const ExtendArgs& a, dart_dtype dt);
+cudaError_t launch_ssd_extend_mma(const ExtendArgs& a, cudaStream_t st);
+// Multiprocessors of the current device, looked up once; 0 on failure.
+int paged_sm_count();
+// Allows a kernel its dynamic shared memory on the current device, once for each
+// (ready: one per kernel; threads that race set the same attribute twice).
+cudaError_t paged_allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& ready);
 size_t sma_paged_workspace_bytes(int P);
 // Tiles a call may come to, and the most a call may have.
 long long sma_paged_tiles(int B, int T);
@@ -97,19 +107,96 @@ __device__ __forceinline__ float mxfp4_pow2(int k) { return __int_as_float((k + 
 __device__ __forceinline__ float mxfp4_scale(unsigned s) {   // 2^(s-127), 2^-127 as a subnormal; 255 is NaN
     return __uint_as_float(s == 255u ? 0x7fffffffu : s == 0u ? 0x00400000u : s << 23);
 }
-// E2M1 code of v (already divided by the scale, |v| <= 6): nearest, ties to even.
-__device__ __forceinline__ unsigned mxfp4_code(float v) {
-    const float a = fabsf(v);
-    const float step = a < 2.f ? 0.5f : a < 4.f ? 1.f : 2.f;
-    const float near = rintf(a / step) * step;   // step is a power of two: the division is exact
-    const float c = near < 2.f ? 2.f * near : near < 4.f ? near + 2.f : 0.5f * near + 4.f;
-    return (unsigned)c | (__float_as_uint(v) >> 31 << 3);
+// Encodes the 8 values v[0 .. 7] (divided by their scale) as a word, the first in the lowest nibble.
+__device__ __forceinline__ uint32_t mxfp4_word(const float (&v)[8]) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(w) : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return w;
 }
-__device__ __forceinline__ float mxfp4_level(unsigned code) {
-    const unsigned m = code & 7u;
-    // 0.5 m below 1, else (1 + low/2) 2^(m/2 - 1)
-    const float v = m < 2u ? 0.5f * (float)m : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
-    return code & 8u ? -v : v;
+// The 32 values get(0 .. 31) of block k of a column: its four code words go to
+// word[q N/32], its scale is returned as a byte.
+template <int N, class Get>
+__device__ __forceinline__ unsigned mxfp4_block(Get get, uint32_t* word) {
+    float v[32], amax = 0.f;
+    bool finite = true;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+        v[r] = get(r);
+        amax = fmaxf(amax, fabsf(v[r]));
+        finite &= fabsf(v[r]) < INFINITY;
+    }
+    const int e = mxfp4_exponent(finite ? amax : 0.f);
+    const float inv = mxfp4_pow2(-e);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float u[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = v[16 * (j / 4) + 4 * q + j % 4] * inv;
+        word[q * (N / 32)] = finite ? mxfp4_word(u) : 0u;
+    }
+    return finite ? (unsigned)(e + 127) : 255u;
+}
+
+// ----------------------------------------------- what a run of tokens has to do
+struct ExtendPlan {
+    int t0, len;     // rows of the sequence's tokens; len 0 where there is nothing to do, or it cannot be done
+    int n, pos;      // memories and place in the chunk before the run
+};
+
+// Checks the run of sequence b: its rows, its counters, and that the pages of the
+// memories that close have room and are pages.  One block per sequence (`first`)
+// writes its counters and counts and flags what is wrong.  All threads of a block.
+__device__ __forceinline__ ExtendPlan plan_extend(const ExtendArgs& a, int b, bool first) {
+    const int tid = threadIdx.x, threads = blockDim.x;
+    ExtendPlan p;
+    int t1;
+    const bool range = token_range(a.cu, b, a.T, p.t0, t1);
+    p.n = a.nchunks[b];
+    p.pos = a.pos[b];
+    p.len = range ? t1 - p.t0 : 0;
+    const bool counters = p.n >= 0 && p.pos >= 0 && p.pos < a.S;
+    const long long closes = counters ? ((long long)p.pos + p.len) / a.S : 0;
+    const int R = a.cache.R;
+    const int* row = a.cache.table + (size_t)b * a.cache.width;
+    int bad = !range || !counters || p.n + closes > (long long)a.cache.width * R;
+    if (!bad && closes > 0)
+        for (int k = p.n / R + tid; k <= (int)((p.n + closes - 1) / R); k += threads) bad |= row[k] < 0 || row[k] >= a.cache.npages;
+    bad = __syncthreads_or(bad);
+    if (first) {
+        if (bad && tid == 0) flag_status(a.status, kStatusDevice);
+        if (tid == 0) {
+            a.nchunks_out[b] = bad ? p.n : (int)(p.n + closes);
+            a.pos_out[b] = bad ? p.pos : (int)((p.pos + (long long)p.len) - closes * a.S);
+        }
+        if (range)
+            for (int t = p.t0 + tid; t < t1; t += threads) a.mem_count[t] = bad ? -1 : (int)(p.n + ((long long)p.pos + (t - p.t0)) / a.S);
+    }
+    if (bad) p.len = 0;
+    return p;
+}
+
+// Columns p0 .. p0 + PS - 1 of a finished memory, from shared memory d [N][PS] to
+// slot `slot` of sequence b, head h.  All threads of a block.
+template <typename T, int N, int P, int PS>
+__device__ __forceinline__ void append_memory(const ExtendArgs& a, int b, int h, int slot, int p0, const float* d, int tid, int threads) {
+    const int R = a.cache.R;
+    const size_t mem = memory_index(a.cache, a.H, a.cache.table[(size_t)b * a.cache.width + slot / R], h, slot % R);
+    if (!a.cache.mxfp4) {
+        T* to = static_cast<T*>(a.cache.pages) + mem * (size_t)(N * P) + p0;
+        for (int i = tid; i < N * PS; i += threads) to[(size_t)(i / PS) * P + i % PS] = Elem<T>::from_f(d[i]);
+    } else if constexpr (N % 32 == 0) {
+        uint32_t* codes = static_cast<uint32_t*>(a.cache.pages) + mem * (size_t)(N * P / 8);
+        uint8_t* scales = a.cache.scales + mem * (size_t)(N * P / 32);
+        for (int i = tid; i < PS * (N / 32); i += threads) {
+            const int p = i % PS, k = i / PS;
+            scales[(p0 + p) * (N / 32) + k] =
+                (uint8_t)mxfp4_block<N>([&](int r) { return d[(32 * k + r) * PS + p]; }, codes + (size_t)(p0 + p) * (N / 8) + k);
+        }
+    }
 }
 #endif
 

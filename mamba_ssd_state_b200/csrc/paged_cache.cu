@@ -75,16 +75,6 @@ __device__ __forceinline__ void store2(__nv_bfloat16* p, float u, float v) {
 
 // A code word holds the 8 codes of column p with n = 32k + {0, 16} + 4q + j;
 // row p has N/8 of them, word q (N/32) + k.
-// Encodes the 8 values v[0 .. 7] (divided by their scale).
-__device__ __forceinline__ uint32_t code_word(const float (&v)[8]) {
-    uint32_t w;
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
-        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
-        : "=r"(w) : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
-    return w;
-}
 // The 8 values of a code word.
 __device__ __forceinline__ void code_values(uint32_t w, float (&v)[8]) {
     uint32_t r[4];
@@ -117,30 +107,8 @@ __global__ void __launch_bounds__(N) cache_write_mxfp4_kernel(CacheCopyArgs a) {
     int slot = 0;
     const int page = checked_page(a, b, i, slot);
     if (page < 0) return;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        float amax = 0.f;
-        bool finite = true;
-#pragma unroll
-        for (int r = 0; r < 32; ++r) {
-            const float f = fabsf(c ? v[r].y : v[r].x);
-            amax = fmaxf(amax, f);
-            finite &= f < INFINITY;
-        }
-        const int e = mxfp4_exponent(finite ? amax : 0.f);
-        const float inv = mxfp4_pow2(-e);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float u[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 f = v[16 * (j / 4) + 4 * q + j % 4];
-                u[j] = (c ? f.y : f.x) * inv;
-            }
-            codes[(p + c) * WS + q * K + k] = finite ? code_word(u) : 0u;
-        }
-        scales[(p + c) * K + k] = finite ? (uint8_t)(e + 127) : (uint8_t)255;
-    }
+    scales[p * K + k] = (uint8_t)mxfp4_block<N>([&](int r) { return v[r].x; }, codes + p * WS + k);
+    scales[(p + 1) * K + k] = (uint8_t)mxfp4_block<N>([&](int r) { return v[r].y; }, codes + (p + 1) * WS + k);
     __syncthreads();
     const size_t m = memory_index(a.cache, a.H, page, h, slot);
     uint4* cdst = static_cast<uint4*>(a.cache.pages) + m * (kP * W / 4);

@@ -14,8 +14,6 @@
 // on the device), which costs less than a launch of its own would.
 #pragma once
 
-#include <atomic>
-
 #include "dart_paged.cuh"
 
 namespace dart {
@@ -44,11 +42,6 @@ cudaError_t launch_sma_paged_mma(const SmaPagedArgs& a, dart_dtype dt, cudaStrea
 // sma_paged_tc.cu: bfloat16 memories with P = 64, long runs.
 bool sma_paged_tc_applicable(const SmaPagedArgs& a, dart_dtype dt);
 cudaError_t launch_sma_paged_tc(const SmaPagedArgs& a, cudaStream_t st);
-// Multiprocessors of the current device, looked up once; 0 on failure.
-int paged_sm_count();
-// Allows a kernel its dynamic shared memory on the current device, once for each
-// (ready: one per kernel; threads that race set the same attribute twice).
-cudaError_t paged_allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& ready);
 
 #ifdef __CUDACC__
 

@@ -1,0 +1,354 @@
+// ssd_extend_mma.cu -- runs of many new tokens (pieces of a prompt) through the
+// recurrence on tensor cores, bfloat16 inputs, P = 64.
+//
+// The rule is ssd_extend.cu's, evaluated in blocks of up to 64 tokens that end at
+// the end of a chunk.  With cum_t the sum of dt A up to token t of the block and
+// H, D the matrices before it,
+//   y_t = exp(cum_t) C_t^T H + sum_{s <= t} exp(cum_t - cum_s) dt_s (C_t . B_s) x_s,
+//   H' = exp(cum_end) H + S,  D' = exp(cum_end) D + S,
+//   S = sum_s B_s (exp(cum_end - cum_s) dt_s x_s)^T.
+// Token by token a thread needs 4 N P operations a token from the CUDA cores and
+// waits for shared memory at every one (four pieces of up to 256 tokens, 32
+// heads: 92 us); the products of a block keep the state in registers too and take
+// XXX us.  They are warp-level m16n8k16: the state is both the accumulator of one
+// block's S and, as it lies, the A operand of the next block's C^T H.
+//
+// float32 results from bfloat16 products: C, B and x are exact; H, the decayed
+// Gram matrix and the weighted x are float32 and go in as three bfloat16 parts
+// (24 bits), so every product is exact and every sum is in float32.  Decays are
+// exponentials of differences of prefix sums that are kept as two floats (their
+// difference is good to 2^-24 of itself however far the prefix has come).
+//
+// A block of 256 threads owns PS columns of one (sequence, head): warp w holds 16
+// of them and N PS / 128 rows of H^T and D^T.  The partial sums of y meet in
+// shared memory, in a fixed order.  The next tokens' B, C and x are on their way
+// (cp.async) while a block is computed.
+#include "dart_paged.cuh"
+#include "sm100.cuh"
+
+namespace dart {
+namespace {
+
+constexpr int kThreads = 256, kWarps = 8;
+constexpr int kTB = 64;       // tokens of a block
+constexpr int kP = 64;
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void ldsm(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {   // zeros where it is not
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+// u and v as three pairs of bfloat16 that add up to them (24 bits).
+__device__ __forceinline__ void split3(float u, float v, uint32_t (&r)[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(u, v);
+        r[i] = *reinterpret_cast<const uint32_t*>(&h);
+        u -= __low2float(h);
+        v -= __high2float(h);
+    }
+}
+
+template <int N, int PS>
+struct Smem {
+    static constexpr int kRowN = N + 8, kRowP = PS + 8;     // padded rows: ldmatrix rows fall into different banks
+    static constexpr int kPW = PS / 16, kNW = kWarps / kPW; // warps along the columns, along the rows of the state
+    __nv_bfloat16 B[2][kTB][kRowN], C[2][kTB][kRowN], x[2][kTB][kRowP];
+    __nv_bfloat16 wx[3][kTB][kRowP];
+    float y[2 + kNW][kTB][PS + 4];                           // partial sums; also D on its way to a page
+    float dt[2][kTB];
+    float hi[kTB], lo[kTB], grow[kTB], w[kTB];               // cum (base 2) in two parts, exp(cum), exp(cum_end - cum) dt
+    float total;                                             // exp(cum_end)
+};
+
+template <int N, int PS>
+__global__ void __launch_bounds__(kThreads, 1) ssd_extend_mma_kernel(ExtendArgs a) {
+    using T = __nv_bfloat16;
+    using S = Smem<N, PS>;
+    constexpr int NW = N / S::kNW, NT = NW / 8;              // rows of H held by a warp, as tiles of 8
+    extern __shared__ __align__(16) uint8_t raw[];
+    S& s = *reinterpret_cast<S*>(raw);
+    const int p0 = blockIdx.x * PS, h = blockIdx.y, b = blockIdx.z;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+    sm100::griddep_wait();
+    const int wp = warp % S::kPW, wn = warp / S::kPW;        // this warp's 16 columns and NW rows of the state
+    const size_t bh = (size_t)b * a.H + h;
+    // element (p, n) of H^T: columns p0 + 16 wp + g (+ 8), rows NW wn + 8 j + 2 q (+ 1)
+    const size_t at = (bh * N + NW * wn + 2 * q) * kP + p0 + 16 * wp + g;
+    float H[NT][4], D[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const size_t e = at + (8 * j + (r & 1)) * kP + 8 * (r >> 1);
+            H[j][r] = a.state[e];
+            D[j][r] = a.cur[e];
+        }
+    const ExtendPlan plan = plan_extend(a, b, p0 == 0 && h == 0);
+    auto store = [&]() {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const size_t e = at + (8 * j + (r & 1)) * kP + 8 * (r >> 1);
+                a.state_out[e] = H[j][r];
+                a.cur_out[e] = D[j][r];
+            }
+    };
+    if (plan.len == 0) {   // the sequence stays as it is
+        if (a.state_out != a.state || a.cur_out != a.cur) store();
+        return;
+    }
+    const int grp = group_of(h, a.H, a.G), t1 = plan.t0 + plan.len;
+    const float Ah = a.A[h];
+    auto fetch = [&](int base, int m, int buf) {
+        for (int i = tid; i < kTB * (N / 8); i += kThreads) {
+            const int r = i / (N / 8), c = 8 * (i % (N / 8));
+            const size_t e = ((size_t)(base + (r < m ? r : 0)) * a.G + grp) * N + c;
+            copy16(smem_addr(&s.B[buf][r][c]), static_cast<const T*>(a.Bm) + e, r < m);
+            copy16(smem_addr(&s.C[buf][r][c]), static_cast<const T*>(a.Cm) + e, r < m);
+        }
+        for (int i = tid; i < kTB * (PS / 8); i += kThreads) {
+            const int r = i / (PS / 8), c = 8 * (i % (PS / 8));
+            copy16(smem_addr(&s.x[buf][r][c]), static_cast<const T*>(a.x) + ((size_t)(base + (r < m ? r : 0)) * a.H + h) * kP + p0 + c, r < m);
+        }
+        if (tid < kTB) s.dt[buf][tid] = tid < m ? a.dt[(size_t)(base + tid) * a.H + h] : 0.f;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int slot = plan.n, left = a.S - plan.pos, buf = 0;       // tokens up to the end of the chunk
+    int m = min(min(kTB, plan.len), left);
+    fetch(plan.t0, m, 0);
+    for (int base = plan.t0; base < t1; buf ^= 1) {
+        const bool closes = m == left;
+        const int next = base + m, left2 = closes ? a.S : left - m, m2 = min(min(kTB, t1 - next), left2);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        if (m2 > 0) fetch(next, m2, buf ^ 1);
+        // ---- decays: warp 0 sums dt A log2(e) in float64, two tokens a lane
+        if (warp == 0) {
+            const double la = (double)Ah * 1.4426950408889634;
+            const double u = la * s.dt[buf][2 * lane], v = la * s.dt[buf][2 * lane + 1];
+            double c = u + v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double before = __shfl_up_sync(0xffffffffu, c, o);
+                if (lane >= o) c += before;
+            }
+            const double end = __shfl_sync(0xffffffffu, c, 31);   // tokens past m add nothing
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const double cum = i ? c : c - v;
+                const int t = 2 * lane + i;
+                s.hi[t] = (float)cum;
+                s.lo[t] = (float)(cum - (double)(float)cum);
+                s.grow[t] = exp2f((float)cum);
+                s.w[t] = exp2f((float)(end - cum)) * s.dt[buf][t];
+            }
+            if (lane == 0) s.total = exp2f((float)end);
+        }
+        __syncthreads();
+        // ---- the weighted x in three parts
+        for (int i = tid; i < kTB * (PS / 2); i += kThreads) {
+            const int r = i / (PS / 2), c = 2 * (i % (PS / 2));
+            const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&s.x[buf][r][c]);
+            uint32_t part[3];
+            split3(s.w[r] * __low2float(v), s.w[r] * __high2float(v), part);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t*>(&s.wx[k][r][c]) = part[k];
+        }
+        __syncthreads();
+        const int li = lane & 7, lm = lane >> 3;              // row and matrix of a ldmatrix address
+        // ---- inside the block: 16 rows t by 32 columns s of the decayed Gram matrix, times x
+        {
+            const int tt = 16 * (warp & 3), ss = 32 * (warp >> 2);
+            if (ss <= tt + 15) {
+                float G[4][4] = {};
+#pragma unroll
+                for (int k = 0; k < N / 16; ++k) {
+                    uint32_t ca[4];
+                    ldsm(smem_addr(&s.C[buf][tt + (lm & 1) * 8 + li][16 * k + (lm >> 1) * 8]), ca);
+#pragma unroll
+                    for (int j = 0; j < 4; j += 2) {
+                        if (ss + 8 * j > tt + 15) continue;
+                        uint32_t bb[4];      // tiles j and j + 1 of 8 columns
+                        ldsm(smem_addr(&s.B[buf][ss + 8 * j + (lm >> 1) * 8 + li][16 * k + (lm & 1) * 8]), bb);
+                        mma(G[j], ca, bb[0], bb[1]);
+                        mma(G[j + 1], ca, bb[2], bb[3]);
+                    }
+                }
+                // decay; G[j][r] is row tt + g + 8 (r / 2), column ss + 8 j + 2 q + r % 2
+                uint32_t A3[3][2][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; r += 2) {
+                        float v[2];
+                        const int t = tt + g + 4 * r;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int c = ss + 8 * j + 2 * q + i;
+                            v[i] = c <= t && c < m ? exp2f((s.hi[t] - s.hi[c]) + (s.lo[t] - s.lo[c])) * s.dt[buf][c] * G[j][r + i] : 0.f;
+                        }
+                        uint32_t part[3];
+                        split3(v[0], v[1], part);
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) A3[k][j >> 1][(j & 1) * 2 + (r >> 1)] = part[k];
+                    }
+                float Y[PS / 8][4] = {};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (ss + 16 * k > tt + 15) continue;
+#pragma unroll
+                    for (int j = 0; j < PS / 8; j += 2) {
+                        uint32_t xb[4];
+                        ldsm_t(smem_addr(&s.x[buf][ss + 16 * k + (lm & 1) * 8 + li][8 * j + (lm >> 1) * 8]), xb);
+#pragma unroll
+                        for (int i = 0; i < 3; ++i) {
+                            mma(Y[j], A3[i][k], xb[0], xb[1]);
+                            mma(Y[j + 1], A3[i][k], xb[2], xb[3]);
+                        }
+                    }
+                }
+                float(*y)[PS + 4] = s.y[warp >> 2];
+#pragma unroll
+                for (int j = 0; j < PS / 8; ++j) {
+                    *reinterpret_cast<float2*>(&y[tt + g][8 * j + 2 * q]) = make_float2(Y[j][0], Y[j][1]);
+                    *reinterpret_cast<float2*>(&y[tt + g + 8][8 * j + 2 * q]) = make_float2(Y[j][2], Y[j][3]);
+                }
+            }
+        }
+        // ---- from before the block: (H^T C^T) in columns t; the accumulator of H^T as it lies is the A operand
+        {
+            float Y[kTB / 8][4] = {};
+#pragma unroll
+            for (int k = 0; k < NT / 2; ++k) {
+                uint32_t part[4][3];
+                split3(H[2 * k][0], H[2 * k][1], part[0]);
+                split3(H[2 * k][2], H[2 * k][3], part[1]);
+                split3(H[2 * k + 1][0], H[2 * k + 1][1], part[2]);
+                split3(H[2 * k + 1][2], H[2 * k + 1][3], part[3]);
+#pragma unroll
+                for (int j = 0; j < kTB / 8; j += 2) {
+                    if (8 * j >= m) continue;
+                    uint32_t cb[4];
+                    ldsm(smem_addr(&s.C[buf][8 * j + (lm >> 1) * 8 + li][NW * wn + 16 * k + (lm & 1) * 8]), cb);
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {
+                        const uint32_t ha[4] = {part[0][i], part[1][i], part[2][i], part[3][i]};
+                        mma(Y[j], ha, cb[0], cb[1]);
+                        mma(Y[j + 1], ha, cb[2], cb[3]);
+                    }
+                }
+            }
+            float(*y)[PS + 4] = s.y[2 + wn];
+#pragma unroll
+            for (int j = 0; j < kTB / 8; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = 8 * j + 2 * q + (r & 1);
+                    y[t][16 * wp + g + 8 * (r >> 1)] = s.grow[t] * Y[j][r];
+                }
+        }
+        // ---- the state after the block
+        {
+            float U[NT][4] = {};
+#pragma unroll
+            for (int k = 0; k < kTB / 16; ++k) {
+                if (16 * k >= m) continue;
+                uint32_t xa[3][4];
+#pragma unroll
+                for (int i = 0; i < 3; ++i) ldsm_t(smem_addr(&s.wx[i][16 * k + (lm >> 1) * 8 + li][16 * wp + (lm & 1) * 8]), xa[i]);
+#pragma unroll
+                for (int j = 0; j < NT; j += 2) {
+                    uint32_t bb[4];
+                    ldsm_t(smem_addr(&s.B[buf][16 * k + (lm & 1) * 8 + li][NW * wn + 8 * j + (lm >> 1) * 8]), bb);
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {
+                        mma(U[j], xa[i], bb[0], bb[1]);
+                        mma(U[j + 1], xa[i], bb[2], bb[3]);
+                    }
+                }
+            }
+            const float total = s.total;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    H[j][r] = fmaf(total, H[j][r], U[j][r]);
+                    D[j][r] = fmaf(total, D[j][r], U[j][r]);
+                }
+        }
+        __syncthreads();
+        for (int i = tid; i < m * (PS / 4); i += kThreads) {
+            const int t = i / (PS / 4), c = 4 * (i % (PS / 4));
+            float4 v = *reinterpret_cast<const float4*>(&s.y[0][t][c]);
+            auto add = [&](int k) {
+                const float4 u = *reinterpret_cast<const float4*>(&s.y[k][t][c]);
+                v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+            };
+            if (t >= 32) add(1);      // before that, no column of the second half is seen
+#pragma unroll
+            for (int k = 0; k < S::kNW; ++k) add(2 + k);
+            *reinterpret_cast<float4*>(a.y + ((size_t)(base + t) * a.H + h) * kP + p0 + c) = v;
+        }
+        if (closes) {                  // D is the chunk's memory
+            __syncthreads();
+            float* d = &s.y[0][0][0];  // [N][PS]
+            static_assert(sizeof(s.y) >= sizeof(float) * N * PS, "D passes through y");
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    d[(NW * wn + 8 * j + 2 * q + (r & 1)) * PS + 16 * wp + g + 8 * (r >> 1)] = D[j][r];
+                    D[j][r] = 0.f;
+                }
+            __syncthreads();
+            append_memory<T, N, kP, PS>(a, b, h, slot, p0, d, tid, kThreads);
+            ++slot;
+        }
+        base = next;
+        left = left2;
+        m = m2;
+    }
+    store();
+}
+
+template <int N, int PS>
+cudaError_t run(const ExtendArgs& a, cudaStream_t st) {
+    auto kern = ssd_extend_mma_kernel<N, PS>;
+    const int smem = (int)sizeof(Smem<N, PS>);
+    static_assert(sizeof(Smem<N, PS>) <= 232448, "shared memory");
+    static std::atomic<unsigned long long> ready{0};   // devices whose kernel has its shared memory allowed
+    cudaError_t e = paged_allow_smem(reinterpret_cast<const void*>(kern), smem, ready);
+    if (e != cudaSuccess) return e;
+    if ((e = launch_dependent(kern, dim3(kP / PS, a.H, a.B), dim3(kThreads), smem, st, 1, a)) == cudaSuccess) count_launches(1);
+    return e;
+}
+
+}  // namespace
+
+bool ssd_extend_mma_applicable(const ExtendArgs& a, dart_dtype dt) {
+    // blocks of 64 tokens that end with their chunk: XXX
+    return dt == DART_BF16 && a.P == kP && (a.N == 128 || a.N == 64) && a.S >= 32 && a.T >= 16 * (long long)a.B;
+}
+
+cudaError_t launch_ssd_extend_mma(const ExtendArgs& a, cudaStream_t st) {
+    // half the columns a block where whole ones would leave half of the machine idle
+    const bool half = 2ll * a.B * a.H <= paged_sm_count();
+    if (a.N == 128) return half ? run<128, 32>(a, st) : run<128, 64>(a, st);
+    return half ? run<64, 32>(a, st) : run<64, 64>(a, st);
+}
+
+}  // namespace dart

@@ -255,6 +255,42 @@ def test_extend(N, P, dtype, cache, H, G, lens, pos, S, R):
     assert torch.equal(again["y"][:T], y[:T])
 
 
+@pytest.mark.parametrize("N, H, G", [(128, 32, 1), (128, 2, 2), (64, 40, 8), (64, 1, 1)])
+@pytest.mark.parametrize("cache", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("lens, pos, S", [([70, 0, 130, 5], [5, 1, 31, 30], 32), ([64, 65, 1], [0, 0, 99], 100), ([200], [250], 256)])
+def test_extend_of_long_runs(N, H, G, cache, lens, pos, S):
+    """Blocks of 64 tokens, full, partial and cut by the ends of chunks; some tokens forget nearly everything (dt A down
+    to -80), others hardly anything.  float32 sums of up to 200 terms and differences of sums of logarithms: TOL."""
+    rng = np.random.default_rng(sum(lens) + N + H)
+    B, P = len(lens), 64
+    n = [1] * B
+    have = memories_of(rng, n, H, N, P, cache)
+    pool = Pool(have, H, N, P, 3, cache, rng, room=max((p + t) // S for p, t in zip(pos, lens)))
+    args, args64 = extend_inputs(rng, lens, H, G, N, P, "bf16", trailing=2)
+    dt64 = args64[1] * np.where(rng.uniform(size=args64[1].shape) < 0.03, 50.0, 1.0)
+    dt, dt64 = cast(dt64, "f32")
+    args, args64 = (args[0], dt, *args[2:]), (args64[0], dt64, *args64[2:])
+    s, c, s64, c64 = states(rng, B, H, N, P)
+    y = torch.full((sum(lens) + 2, H, P), 9.0, device="cuda")
+    call = lambda so, co, to: dart.dart_ssd_extend(*args, cumulative(lens), s, c, pool.pages, pool.table, ints(*n), ints(*pos), S,
+                                                   scales=pool.scales, state_out=so, dH_cur_out=co, y=to)
+    got = call(torch.empty_like(s), torch.empty_like(c), y)
+    dart.dart_sync_status()
+    yr, sr, cr, nr, pr, counts, app = ref.extend(*args64, lens, s64, c64, n, pos, S)
+    T = sum(lens)
+    assert rel_err(y[:T], yr[:T]) <= TOL and (y[T:] == 9.0).all()
+    assert rel_err(got["state"], sr) <= TOL and rel_err(got["dH_cur"], cr) <= TOL
+    assert got["nchunks"].tolist() == nr and got["pos"].tolist() == pr and got["mem_count"][:T].tolist() == counts
+    for b in range(B):
+        assert np.array_equal(pool.memory(b, 0), have[b][0])
+        for j, mem in enumerate(app[b]):
+            page, slot = pool.table_np[b, (1 + j) // 3], (1 + j) % 3
+            check_memory(pool.memory(b, 1 + j), mem, cache, None if pool.scales is None else pool.scales[page, :, slot].cpu().numpy())
+    again = call(s, c, torch.zeros_like(y))         # in place, and the same bits
+    dart.dart_sync_status()
+    assert torch.equal(again["y"][:T], y[:T]) and torch.equal(s, got["state"]) and torch.equal(c, got["dH_cur"])
+
+
 def test_extend_leaves_what_it_cannot_do():
     """Full tables, bad pages and bad counters: the sequence keeps its state and counters, its tokens are marked."""
     rng = np.random.default_rng(6)
