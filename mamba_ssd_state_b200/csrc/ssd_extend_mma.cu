@@ -67,10 +67,11 @@ struct Smem {
     static constexpr int kPW = PS / 16, kNW = kWarps / kPW; // warps along the columns, along the rows of the state
     __nv_bfloat16 B[2][kTB][kRowN], C[2][kTB][kRowN], x[2][kTB][kRowP];
     __nv_bfloat16 wx[3][kTB][kRowP];
-    float y[2 + kNW][kTB][PS + 4];                           // partial sums; also D on its way to a page
+    float y[2 + kNW][kTB][PS + 4];                           // partial sums
+    float d[N * PS];                                         // D on its way to a page
     float dt[2][kTB];
-    float hi[kTB], lo[kTB], grow[kTB], w[kTB];               // cum (base 2) in two parts, exp(cum), exp(cum_end - cum) dt
-    float total;                                             // exp(cum_end)
+    // of the block in each buffer: cum (base 2) in two parts, exp(cum), exp(cum_end - cum) dt, exp(cum_end)
+    float hi[2][kTB], lo[2][kTB], grow[2][kTB], w[2][kTB], total[2];
 };
 
 template <int N, int PS>
@@ -124,51 +125,86 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_extend_mma_kernel(ExtendArgs 
             const int r = i / (PS / 8), c = 8 * (i % (PS / 8));
             copy16(smem_addr(&s.x[buf][r][c]), static_cast<const T*>(a.x) + ((size_t)(base + (r < m ? r : 0)) * a.H + h) * kP + p0 + c, r < m);
         }
-        if (tid < kTB) s.dt[buf][tid] = tid < m ? a.dt[(size_t)(base + tid) * a.H + h] : 0.f;
+        if (warp == 4)       // which sums them up
+#pragma unroll
+            for (int t = lane; t < kTB; t += 32)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(&s.dt[buf][t])),
+                             "l"(a.dt + (size_t)(base + (t < m ? t : 0)) * a.H + h), "r"(t < m ? 4 : 0) : "memory");
         asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // Decays of the block in a buffer, by one warp: sums of dt A log2(e) in float64, two tokens a lane.
+    auto decays = [&](int k) {
+        const double la = (double)Ah * 1.4426950408889634;
+        const double u = la * s.dt[k][2 * lane], v = la * s.dt[k][2 * lane + 1];
+        double c = u + v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double before = __shfl_up_sync(0xffffffffu, c, o);
+            if (lane >= o) c += before;
+        }
+        const double end = __shfl_sync(0xffffffffu, c, 31);   // tokens past the block's add nothing
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const double cum = i ? c : c - v;
+            const int t = 2 * lane + i;
+            s.hi[k][t] = (float)cum;
+            s.lo[k][t] = (float)(cum - (double)(float)cum);
+            s.grow[k][t] = exp2f((float)cum);
+            s.w[k][t] = exp2f((float)(end - cum)) * s.dt[k][t];
+        }
+        if (lane == 0) s.total[k] = exp2f((float)end);
     };
     int slot = plan.n, left = a.S - plan.pos, buf = 0;       // tokens up to the end of the chunk
     int m = min(min(kTB, plan.len), left);
     fetch(plan.t0, m, 0);
+    auto wait_copies = [&]() { asm volatile("cp.async.wait_group 0;" ::: "memory"); };
+    if (warp == 4) {
+        wait_copies();
+        __syncwarp();
+        decays(0);
+    }
+    // y of m tokens from row `base` on, and the memory that closed with the last one
+    auto finish = [&](int base, int m, bool closed) {
+        constexpr int COLS = PS / 4, ROWS = kThreads / COLS;      // threads of a row, rows at a time
+        const int c = 4 * (tid % COLS), r0 = tid / COLS;
+        float* to = a.y + ((size_t)(base + r0) * a.H + h) * kP + p0 + c;
+#pragma unroll
+        for (int u = 0; u < kTB / ROWS; ++u) {
+            const int t = r0 + u * ROWS;
+            if (t < m) {
+                float4 v[2 + S::kNW];
+#pragma unroll
+                for (int k = 0; k < 2 + S::kNW; ++k) v[k] = *reinterpret_cast<const float4*>(&s.y[k][t][c]);
+                if (t < 32) v[1] = make_float4(0.f, 0.f, 0.f, 0.f);      // no column of the second half is seen
+#pragma unroll
+                for (int k = 1; k < 2 + S::kNW; ++k) v[0] = make_float4(v[0].x + v[k].x, v[0].y + v[k].y, v[0].z + v[k].z, v[0].w + v[k].w);
+                *reinterpret_cast<float4*>(to + (size_t)u * ROWS * a.H * kP) = v[0];
+            }
+        }
+        if (closed) {
+            append_memory<T, N, kP, PS>(a, b, h, slot, p0, s.d, tid, kThreads);
+            ++slot;
+        }
+    };
+    int done = 0;                     // tokens of the block before, whose y is still in parts
+    bool closed = false;
     for (int base = plan.t0; base < t1; buf ^= 1) {
         const bool closes = m == left;
         const int next = base + m, left2 = closes ? a.S : left - m, m2 = min(min(kTB, t1 - next), left2);
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        wait_copies();
         __syncthreads();
-        if (m2 > 0) fetch(next, m2, buf ^ 1);
-        // ---- decays: warp 0 sums dt A log2(e) in float64, two tokens a lane
-        if (warp == 0) {
-            const double la = (double)Ah * 1.4426950408889634;
-            const double u = la * s.dt[buf][2 * lane], v = la * s.dt[buf][2 * lane + 1];
-            double c = u + v;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double before = __shfl_up_sync(0xffffffffu, c, o);
-                if (lane >= o) c += before;
-            }
-            const double end = __shfl_sync(0xffffffffu, c, 31);   // tokens past m add nothing
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const double cum = i ? c : c - v;
-                const int t = 2 * lane + i;
-                s.hi[t] = (float)cum;
-                s.lo[t] = (float)(cum - (double)(float)cum);
-                s.grow[t] = exp2f((float)cum);
-                s.w[t] = exp2f((float)(end - cum)) * s.dt[buf][t];
-            }
-            if (lane == 0) s.total = exp2f((float)end);
-        }
-        __syncthreads();
+        if (done > 0) finish(base - done, done, closed);
         // ---- the weighted x in three parts
         for (int i = tid; i < kTB * (PS / 2); i += kThreads) {
             const int r = i / (PS / 2), c = 2 * (i % (PS / 2));
             const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&s.x[buf][r][c]);
             uint32_t part[3];
-            split3(s.w[r] * __low2float(v), s.w[r] * __high2float(v), part);
+            split3(s.w[buf][r] * __low2float(v), s.w[buf][r] * __high2float(v), part);
 #pragma unroll
             for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t*>(&s.wx[k][r][c]) = part[k];
         }
         __syncthreads();
+        if (m2 > 0) fetch(next, m2, buf ^ 1);
         const int li = lane & 7, lm = lane >> 3;              // row and matrix of a ldmatrix address
         // ---- inside the block: 16 rows t by 32 columns s of the decayed Gram matrix, times x
         {
@@ -199,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_extend_mma_kernel(ExtendArgs 
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const int c = ss + 8 * j + 2 * q + i;
-                            v[i] = c <= t && c < m ? exp2f((s.hi[t] - s.hi[c]) + (s.lo[t] - s.lo[c])) * s.dt[buf][c] * G[j][r + i] : 0.f;
+                            v[i] = c <= t && c < m ? exp2f((s.hi[buf][t] - s.hi[buf][c]) + (s.lo[buf][t] - s.lo[buf][c])) * s.dt[buf][c] * G[j][r + i] : 0.f;
                         }
                         uint32_t part[3];
                         split3(v[0], v[1], part);
@@ -210,16 +246,13 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_extend_mma_kernel(ExtendArgs 
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     if (ss + 16 * k > tt + 15) continue;
+                    uint32_t xb[PS / 16][4];
 #pragma unroll
-                    for (int j = 0; j < PS / 8; j += 2) {
-                        uint32_t xb[4];
-                        ldsm_t(smem_addr(&s.x[buf][ss + 16 * k + (lm & 1) * 8 + li][8 * j + (lm >> 1) * 8]), xb);
+                    for (int j = 0; j < PS / 16; ++j) ldsm_t(smem_addr(&s.x[buf][ss + 16 * k + (lm & 1) * 8 + li][16 * j + (lm >> 1) * 8]), xb[j]);
 #pragma unroll
-                        for (int i = 0; i < 3; ++i) {
-                            mma(Y[j], A3[i][k], xb[0], xb[1]);
-                            mma(Y[j + 1], A3[i][k], xb[2], xb[3]);
-                        }
-                    }
+                    for (int i = 0; i < 3; ++i)      // products of one part after the other: neighbours do not wait for each other
+#pragma unroll
+                        for (int j = 0; j < PS / 8; ++j) mma(Y[j], A3[i][k], xb[j >> 1][2 * (j & 1)], xb[j >> 1][2 * (j & 1) + 1]);
                 }
                 float(*y)[PS + 4] = s.y[warp >> 2];
 #pragma unroll
@@ -239,17 +272,14 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_extend_mma_kernel(ExtendArgs 
                 split3(H[2 * k][2], H[2 * k][3], part[1]);
                 split3(H[2 * k + 1][0], H[2 * k + 1][1], part[2]);
                 split3(H[2 * k + 1][2], H[2 * k + 1][3], part[3]);
+                uint32_t cb[kTB / 16][4];
 #pragma unroll
-                for (int j = 0; j < kTB / 8; j += 2) {
-                    if (8 * j >= m) continue;
-                    uint32_t cb[4];
-                    ldsm(smem_addr(&s.C[buf][8 * j + (lm >> 1) * 8 + li][NW * wn + 16 * k + (lm & 1) * 8]), cb);
+                for (int j = 0; j < kTB / 16; ++j) ldsm(smem_addr(&s.C[buf][16 * j + (lm >> 1) * 8 + li][NW * wn + 16 * k + (lm & 1) * 8]), cb[j]);
 #pragma unroll
-                    for (int i = 0; i < 3; ++i) {
-                        const uint32_t ha[4] = {part[0][i], part[1][i], part[2][i], part[3][i]};
-                        mma(Y[j], ha, cb[0], cb[1]);
-                        mma(Y[j + 1], ha, cb[2], cb[3]);
-                    }
+                for (int i = 0; i < 3; ++i) {
+                    const uint32_t ha[4] = {part[0][i], part[1][i], part[2][i], part[3][i]};
+#pragma unroll
+                    for (int j = 0; j < kTB / 8; ++j) mma(Y[j], ha, cb[j >> 1][2 * (j & 1)], cb[j >> 1][2 * (j & 1) + 1]);
                 }
             }
             float(*y)[PS + 4] = s.y[2 + wn];
@@ -258,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_extend_mma_kernel(ExtendArgs 
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int t = 8 * j + 2 * q + (r & 1);
-                    y[t][16 * wp + g + 8 * (r >> 1)] = s.grow[t] * Y[j][r];
+                    y[t][16 * wp + g + 8 * (r >> 1)] = s.grow[buf][t] * Y[j][r];
                 }
         }
         // ---- the state after the block
@@ -270,18 +300,15 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_extend_mma_kernel(ExtendArgs 
                 uint32_t xa[3][4];
 #pragma unroll
                 for (int i = 0; i < 3; ++i) ldsm_t(smem_addr(&s.wx[i][16 * k + (lm >> 1) * 8 + li][16 * wp + (lm & 1) * 8]), xa[i]);
+                uint32_t bb[NT / 2][4];
 #pragma unroll
-                for (int j = 0; j < NT; j += 2) {
-                    uint32_t bb[4];
-                    ldsm_t(smem_addr(&s.B[buf][16 * k + (lm & 1) * 8 + li][NW * wn + 8 * j + (lm >> 1) * 8]), bb);
+                for (int j = 0; j < NT / 2; ++j) ldsm_t(smem_addr(&s.B[buf][16 * k + (lm & 1) * 8 + li][NW * wn + 16 * j + (lm >> 1) * 8]), bb[j]);
 #pragma unroll
-                    for (int i = 0; i < 3; ++i) {
-                        mma(U[j], xa[i], bb[0], bb[1]);
-                        mma(U[j + 1], xa[i], bb[2], bb[3]);
-                    }
-                }
+                for (int i = 0; i < 3; ++i)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) mma(U[j], xa[i], bb[j >> 1][2 * (j & 1)], bb[j >> 1][2 * (j & 1) + 1]);
             }
-            const float total = s.total;
+            const float total = s.total[buf];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -290,38 +317,28 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_extend_mma_kernel(ExtendArgs 
                     D[j][r] = fmaf(total, D[j][r], U[j][r]);
                 }
         }
-        __syncthreads();
-        for (int i = tid; i < m * (PS / 4); i += kThreads) {
-            const int t = i / (PS / 4), c = 4 * (i % (PS / 4));
-            float4 v = *reinterpret_cast<const float4*>(&s.y[0][t][c]);
-            auto add = [&](int k) {
-                const float4 u = *reinterpret_cast<const float4*>(&s.y[k][t][c]);
-                v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
-            };
-            if (t >= 32) add(1);      // before that, no column of the second half is seen
-#pragma unroll
-            for (int k = 0; k < S::kNW; ++k) add(2 + k);
-            *reinterpret_cast<float4*>(a.y + ((size_t)(base + t) * a.H + h) * kP + p0 + c) = v;
-        }
         if (closes) {                  // D is the chunk's memory
-            __syncthreads();
-            float* d = &s.y[0][0][0];  // [N][PS]
-            static_assert(sizeof(s.y) >= sizeof(float) * N * PS, "D passes through y");
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    d[(NW * wn + 8 * j + 2 * q + (r & 1)) * PS + 16 * wp + g + 8 * (r >> 1)] = D[j][r];
+                    s.d[(NW * wn + 8 * j + 2 * q + (r & 1)) * PS + 16 * wp + g + 8 * (r >> 1)] = D[j][r];
                     D[j][r] = 0.f;
                 }
-            __syncthreads();
-            append_memory<T, N, kP, PS>(a, b, h, slot, p0, d, tid, kThreads);
-            ++slot;
         }
+        if (warp == 4 && m2 > 0) {     // ahead of the others: it has no part in the Gram matrix
+            wait_copies();
+            __syncwarp();
+            decays(buf ^ 1);
+        }
+        done = m;
+        closed = closes;
         base = next;
         left = left2;
         m = m2;
     }
+    __syncthreads();
+    finish(t1 - done, done, closed);
     store();
 }
 
