@@ -28,6 +28,8 @@
 // scale in float32 before it is added, so a scale costs 4 multiply-adds for
 // every 2 products and no bit.
 #include <cuda_fp16.h>
+#include <float.h>
+#include <limits.h>
 #include <string.h>
 
 #include "sm100.cuh"
@@ -77,19 +79,25 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 __device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
+}
+// 2^x, good to 2^-22; 0 below 2^-126.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 // The four bytes of w, two codes each, as pairs of float16.
 __device__ __forceinline__ void widen_codes(uint32_t w, uint32_t (&r)[4]) {
@@ -111,21 +119,51 @@ template <typename M, int N, int PARTS>
 struct Column {
     uint32_t b[PARTS][N / 16][2];
 
-    // src: the row of Q or C, nullptr for an unused column.  Returns the power of
-    // two that the column was multiplied by (its lanes are those of equal lane / 4).
+    // The values of a row of Q or C as they are (zeros for an unused column,
+    // src == nullptr): loads that wait for nothing.
     template <typename T>
-    __device__ __forceinline__ float load(const T* src) {
-        const int q = threadIdx.x & 3;
-        float amax = 0.f;
+    struct Raw {
         float f[N / 16][4];
+        __device__ __forceinline__ void load(const T* src) {
+            const int q = threadIdx.x & 3;
+#pragma unroll
+            for (int i = 0; i < N / 16; ++i) {
+                if constexpr (M::kFp4) {          // rows 16i + 4q ..
+                    load4(src ? src + 16 * i + 4 * q : nullptr, f[i]);
+                } else {                          // rows 16i + 2q, + 1, and 8 further on
+                    load2(src ? src + 16 * i + 2 * q : nullptr, f[i]);
+                    load2(src ? src + 16 * i + 2 * q + 8 : nullptr, f[i] + 2);
+                }
+            }
+        }
+        static __device__ __forceinline__ void load2(const T* p, float* to) {
+            static_assert(sizeof(T) == 2, "bfloat16 memories have bfloat16 tokens");
+            const uint32_t u = p ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
+            to[0] = __uint_as_float(u << 16);
+            to[1] = __uint_as_float(u & 0xffff0000u);
+        }
+        static __device__ __forceinline__ void load4(const T* p, float* to) {
+            if constexpr (sizeof(T) == 4) {
+                const float4 u = p ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                to[0] = u.x; to[1] = u.y; to[2] = u.z; to[3] = u.w;
+            } else {
+                const uint2 u = p ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0u, 0u);
+                to[0] = __uint_as_float(u.x << 16); to[1] = __uint_as_float(u.x & 0xffff0000u);
+                to[2] = __uint_as_float(u.y << 16); to[3] = __uint_as_float(u.y & 0xffff0000u);
+            }
+        }
+    };
+
+    // Takes the values in.  Returns the power of two that the column was multiplied
+    // by (its lanes are those of equal lane / 4).
+    template <typename T>
+    __device__ __forceinline__ float take(const Raw<T>& raw) {
+        const auto& f = raw.f;
+        float amax = 0.f;
 #pragma unroll
         for (int i = 0; i < N / 16; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = M::kFp4 ? 16 * i + 4 * q + j : 16 * i + 2 * q + (j & 1) + 8 * (j >> 1);
-                f[i][j] = src ? ldf(src + n) : 0.f;
-                amax = fmaxf(amax, fabsf(f[i][j]));
-            }
+            for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fabsf(f[i][j]));
         float scale = 1.f;
         if constexpr (M::kFp4) {
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
@@ -159,7 +197,7 @@ struct Column {
 };
 
 // acc[t][m] += (piece of a memory in `stage`)^T times the columns.  Returns
-// whether the memory is free of NaN blocks (bfloat16 carries its own).
+// whether this lane's rows of it are free of NaN blocks (bfloat16 carries its own).
 template <typename M, int N, int NT, int PARTS, int PIECE>
 __device__ __forceinline__ bool multiply(const uint8_t* stage, const Column<M, N, PARTS> (&col)[NT], float (&acc)[NT][4][4]) {
     const int lane = threadIdx.x & 31;
@@ -178,56 +216,76 @@ __device__ __forceinline__ bool multiply(const uint8_t* stage, const Column<M, N
         }
         return true;
     } else {
-        constexpr int K = N / 32;
+        // Products that do not wait for each other stand together: MG groups of 16
+        // columns of the memory, as many as the registers take.
+        constexpr int K = N / 32, MG = NT == 1 ? 4 : 2;
         const int g = lane >> 2, q = lane & 3;
         const uint8_t* scales = stage + M::kCodeBytes;
         uint32_t nan = 0;
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const int p = 16 * m + g;
-            uint32_t lo[K], hi[K], slo, shi;
-            if constexpr (K == 4) {
-                const uint4 u = *reinterpret_cast<const uint4*>(stage + p * (N / 2) + q * 16);
-                const uint4 v = *reinterpret_cast<const uint4*>(stage + (p + 8) * (N / 2) + q * 16);
-                lo[0] = u.x; lo[1] = u.y; lo[2] = u.z; lo[3] = u.w;
-                hi[0] = v.x; hi[1] = v.y; hi[2] = v.z; hi[3] = v.w;
-                slo = *reinterpret_cast<const uint32_t*>(scales + p * 4);
-                shi = *reinterpret_cast<const uint32_t*>(scales + (p + 8) * 4);
-            } else {
-                const uint2 u = *reinterpret_cast<const uint2*>(stage + p * (N / 2) + q * 8);
-                const uint2 v = *reinterpret_cast<const uint2*>(stage + (p + 8) * (N / 2) + q * 8);
-                lo[0] = u.x; lo[1] = u.y;
-                hi[0] = v.x; hi[1] = v.y;
-                slo = *reinterpret_cast<const uint16_t*>(scales + p * 2);
-                shi = *reinterpret_cast<const uint16_t*>(scales + (p + 8) * 2);
-            }
-            nan |= __vcmpeq4(slo, 0xffffffffu) | __vcmpeq4(shi, 0xffffffffu);
+        for (int m0 = 0; m0 < 4; m0 += MG) {
+            uint32_t w[MG][2][K], sc[MG][2];       // code words and scale bytes of two rows of a group
+#pragma unroll
+            for (int m = 0; m < MG; ++m)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int p = 16 * (m0 + m) + g + 8 * r;
+                    if constexpr (K == 4) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(stage + p * (N / 2) + q * 16);
+                        w[m][r][0] = u.x; w[m][r][1] = u.y; w[m][r][2] = u.z; w[m][r][3] = u.w;
+                        sc[m][r] = *reinterpret_cast<const uint32_t*>(scales + p * 4);
+                    } else {
+                        const uint2 u = *reinterpret_cast<const uint2*>(stage + p * (N / 2) + q * 8);
+                        w[m][r][0] = u.x; w[m][r][1] = u.y;
+                        sc[m][r] = *reinterpret_cast<const uint16_t*>(scales + p * 2);
+                    }
+                    nan |= __vcmpeq4(sc[m][r], 0xffffffffu);
+                }
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                uint32_t ra[4], rb[4];
-                widen_codes(lo[k], ra);
-                widen_codes(hi[k], rb);
-                const uint32_t a0[4] = {ra[0], rb[0], ra[1], rb[1]}, a1[4] = {ra[2], rb[2], ra[3], rb[3]};
-                // 2^(s - 127) of the two rows (2^-127 counts as 0)
-                const float s0 = __uint_as_float((k < 3 ? slo << (23 - 8 * k) : slo >> 1) & 0x7f800000u);
-                const float s1 = __uint_as_float((k < 3 ? shi << (23 - 8 * k) : shi >> 1) & 0x7f800000u);
+                uint32_t a0[MG][4], a1[MG][4];     // the two k steps of a block
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    float d[4];
-                    mma_f16_first(d, a0, col[t].b[0][2 * k]);
-                    mma_f16(d, a1, col[t].b[0][2 * k + 1]);
-                    if constexpr (PARTS == 2) {
-                        mma_f16(d, a0, col[t].b[1][2 * k]);
-                        mma_f16(d, a1, col[t].b[1][2 * k + 1]);
+                for (int m = 0; m < MG; ++m) {
+                    uint32_t u[4], v[4];
+                    widen_codes(w[m][0][k], u);
+                    widen_codes(w[m][1][k], v);
+                    a0[m][0] = u[0]; a0[m][1] = v[0]; a0[m][2] = u[1]; a0[m][3] = v[1];
+                    a1[m][0] = u[2]; a1[m][1] = v[2]; a1[m][2] = u[3]; a1[m][3] = v[3];
+                }
+                float d[NT][MG][4];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int m = 0; m < MG; ++m) mma_f16_first(d[t][m], a0[m], col[t].b[0][2 * k]);
+#pragma unroll
+                for (int h = 0; h < PARTS; ++h) {
+                    if (h > 0) {
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int m = 0; m < MG; ++m) mma_f16(d[t][m], a0[m], col[t].b[h][2 * k]);
                     }
-                    acc[t][m][0] = fmaf(d[0], s0, acc[t][m][0]);
-                    acc[t][m][1] = fmaf(d[1], s0, acc[t][m][1]);
-                    acc[t][m][2] = fmaf(d[2], s1, acc[t][m][2]);
-                    acc[t][m][3] = fmaf(d[3], s1, acc[t][m][3]);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int m = 0; m < MG; ++m) mma_f16(d[t][m], a1[m], col[t].b[h][2 * k + 1]);
+                }
+#pragma unroll
+                for (int m = 0; m < MG; ++m) {
+                    // 2^(s - 127) of the two rows (2^-127 counts as 0)
+                    const float s0 = __uint_as_float((k < 3 ? sc[m][0] << (23 - 8 * k) : sc[m][0] >> 1) & 0x7f800000u);
+                    const float s1 = __uint_as_float((k < 3 ? sc[m][1] << (23 - 8 * k) : sc[m][1] >> 1) & 0x7f800000u);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        acc[t][m0 + m][0] = fmaf(d[t][m][0], s0, acc[t][m0 + m][0]);
+                        acc[t][m0 + m][1] = fmaf(d[t][m][1], s0, acc[t][m0 + m][1]);
+                        acc[t][m0 + m][2] = fmaf(d[t][m][2], s1, acc[t][m0 + m][2]);
+                        acc[t][m0 + m][3] = fmaf(d[t][m][3], s1, acc[t][m0 + m][3]);
+                    }
                 }
             }
         }
-        return !__any_sync(0xffffffffu, nan != 0);
+        return nan == 0;
     }
 }
 
@@ -236,20 +294,31 @@ __device__ __forceinline__ bool multiply(const uint8_t* stage, const Column<M, N
 template <typename M, int N, int TT>
 struct Feed {
     Walk w;
-    const int* table;
+    const int* table;        // the sequence's
     int c, last, piece;      // next memory and piece of it, end of the memories of this part of the run
+    int slot, idx;           // where memory c is: slot of the page table[idx]
+    int page, ahead;         // table[idx] and, loaded long before it is needed, the next entry
     int issued;              // stages filled
     bool more;
 
+    __device__ __forceinline__ void look_ahead(int R) { ahead = (idx + 1) * R < last ? table[idx + 1] : 0; }
     __device__ __forceinline__ void start(const SmaPagedArgs& a, const TileList<kCap>& L) {
         // to the next part of the run that has memories to copy
         while ((more = next_piece(w))) {
             table = a.cache.table + (size_t)L.seq[w.k] * a.cache.width;
-            const int seen = w.memories(), bad = first_bad_memory(table, a.cache, seen);
-            if (bad < seen && (threadIdx.x & 31) == 0) flag_status(a.status, kStatusDevice);
+            const int seen = w.memories();
             c = w.first_memory();
-            last = min(w.last_memory(), bad);
+            last = w.last_memory();
             piece = 0;
+            if (c < last) {
+                idx = c / a.cache.R;
+                slot = c - idx * a.cache.R;
+                page = table[idx];
+                look_ahead(a.cache.R);
+            }
+            const int bad = first_bad_memory(table, a.cache, seen);
+            if (bad < seen && (threadIdx.x & 31) == 0) flag_status(a.status, kStatusDevice);
+            last = min(last, bad);
             if (c < last) return;
             advance(L, w, a.H);
         }
@@ -259,7 +328,7 @@ struct Feed {
         const SmaPagedArgs& a = prm.a;
         const int st = issued % M::kStages, warp = threadIdx.x >> 5;
         if ((threadIdx.x & 31) == 0) {
-            const size_t mem = memory_index(a.cache, a.H, table[c / a.cache.R], w.h, c % a.cache.R);
+            const size_t mem = memory_index(a.cache, a.H, page, w.h, slot);
             const uint32_t full = smem_u32(&s.full[warp][st]), dst = smem_u32(s.ring[warp][st]);
             mbar_expect_tx(full, M::kStageBytes);
             if constexpr (M::kFp4) {
@@ -275,6 +344,11 @@ struct Feed {
             if (++c == last) {
                 advance(s.tiles, w, a.H);
                 start(a, s.tiles);
+            } else if (++slot == a.cache.R) {
+                slot = 0;
+                page = ahead;
+                ++idx;
+                look_ahead(a.cache.R);
             }
         }
     }
@@ -283,7 +357,7 @@ struct Feed {
 // One piece of the run.  NT = 1: columns 0-3 of the tile are Q and 4-7 C of up to
 // 4 tokens; NT = 2: a tile each of up to 8.
 template <typename T, typename M, int N, int TT, int NT, int PARTS>
-__device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const Walk& w, int run, int t0, int rows, int bad,
+__device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const Walk& w, int run, int t0, int rows,
                                           Feed<M, N, TT>& feed, int& taken, const WaitCtx& wc, bool& ok) {
     const SmaPagedArgs& a = prm.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
@@ -294,37 +368,49 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const W
     Column<M, N, PARTS> col[NT];
     // this lane's two tokens, as columns of the results, and what their scores and values are to be multiplied by
     const int tk = NT == 2 ? 2 * q : 2 * (q & 1);
-    float qs[2], vs[2];
-    if constexpr (NT == 2) {
-        const float sq = col[0].load(q_row(g)), sv = col[1].load(c_row(g));
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            qs[j] = 1.f / __shfl_sync(0xffffffffu, sq, 4 * (tk + j));
-            vs[j] = 1.f / __shfl_sync(0xffffffffu, sv, 4 * (tk + j));
-        }
-    } else {
-        const float sc = col[0].load(g < 4 ? q_row(g) : c_row(g - 4));
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            qs[j] = 1.f / __shfl_sync(0xffffffffu, sc, 4 * (tk + j));
-            vs[j] = 1.f / __shfl_sync(0xffffffffu, sc, 4 * (4 + tk + j));
-        }
-    }
-    const float sscale = kLog2e * rsqrtf((float)N);
     float e[4][4];        // E of (token, column) as the results are laid out
-    int count[2];
+    int count[2];         // of the two tokens
+    float qs[2], vs[2];
+    {   // all loads first
+        typename Column<M, N, PARTS>::template Raw<T> raw[NT];
+        if constexpr (NT == 2) {
+            raw[0].load(q_row(g));
+            raw[1].load(c_row(g));
+        } else {
+            raw[0].load(g < 4 ? q_row(g) : c_row(g - 4));
+        }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        qs[j] *= sscale;
-        count[j] = tk + j < rows ? a.mem_count[t0 + tk + j] : 0;
+        for (int j = 0; j < 2; ++j) {
+            count[j] = tk + j < rows ? a.mem_count[t0 + tk + j] : -1;
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+            for (int m = 0; m < 4; ++m)
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-                e[m][2 * r + j] = tk + j < rows && (NT == 2 || q < 2)
-                                      ? ldf(E + ((size_t)(t0 + tk + j) * a.H + w.h) * kP + 16 * m + g + 8 * r) : 0.f;
+                for (int r = 0; r < 2; ++r)
+                    e[m][2 * r + j] = tk + j < rows && (NT == 2 || q < 2)
+                                          ? ldf(E + ((size_t)(t0 + tk + j) * a.H + w.h) * kP + 16 * m + g + 8 * r) : 0.f;
+        }
+        float scale[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) scale[t] = col[t].take(raw[t]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            qs[j] = kLog2e * rsqrtf((float)N) / __shfl_sync(0xffffffffu, scale[0], 4 * (tk + j));
+            vs[j] = 1.f / __shfl_sync(0xffffffffu, scale[NT - 1], 4 * ((NT == 2 ? 0 : 4) + tk + j));
+        }
     }
-    float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[4][4];
+    const int bad = first_bad_memory(a.cache.table + (size_t)s.tiles.seq[w.k] * a.cache.width, a.cache, w.memories());
+    int fewest = INT_MAX; // memories that every row of the tile sees (rows that are not to be computed apart)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (count[j] >= 0 && count[j] <= bad) fewest = min(fewest, count[j]);
+    fewest = __reduce_min_sync(0xffffffffu, fewest);
+    // Scores: the lanes of a column (equal lane % 4) hold parts of those of its two
+    // tokens; the even of lane / 4 take the first one's, the odd the second's.
+    const int mine = g & 1;
+    const float qm = mine ? qs[1] : qs[0];
+    // lanes that have the weights of this lane's tokens (the C columns take those of the Q columns)
+    const int from = NT == 2 ? q : q & 1;
+    float mx = -FLT_MAX, l = 0.f, o[4][4];      // of token tk + mine; o of both
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
@@ -351,46 +437,52 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const W
         };
         take(Piece<0>{});
         if constexpr (M::kPieces == 2) take(Piece<1>{});
-        float f[2], wt[2];
+        float v[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            float v = 0.f;
+            v[j] = 0.f;
 #pragma unroll
-            for (int m = 0; m < 4; ++m) v = fmaf(acc[0][m][j], e[m][j], fmaf(acc[0][m][2 + j], e[m][2 + j], v));
-            v += __shfl_xor_sync(0xffffffffu, v, 4);
-            v += __shfl_xor_sync(0xffffffffu, v, 8);
-            v += __shfl_xor_sync(0xffffffffu, v, 16);
-            if (NT == 1) v = __shfl_sync(0xffffffffu, v, lane & ~2);   // the C columns take the scores of the Q columns
-            float sc = clean ? v * qs[j] : __int_as_float(0x7fffffff);
-            if (c >= count[j]) sc = -INFINITY;
-            const float mn = fmaxf(mx[j], sc);
-            const bool none = mn == -INFINITY;      // nothing seen yet, or only scores of -inf: they weigh nothing
-            f[j] = none ? 1.f : exp2f(mx[j] - mn);
-            wt[j] = none ? (sc == sc ? 0.f : sc) : exp2f(sc - mn);
-            l[j] = fmaf(l[j], f[j], wt[j]);
-            mx[j] = mn;
+            for (int m = 0; m < 4; ++m) v[j] = fmaf(acc[0][m][j], e[m][j], fmaf(acc[0][m][2 + j], e[m][2 + j], v[j]));
         }
-        // most memories move no maximum, and most rows see all of them
-        if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+        float sc = (mine ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, mine ? v[0] : v[1], 4);
+        if (!clean) sc = __int_as_float(0x7fffffff);
+        sc += __shfl_xor_sync(0xffffffffu, sc, 8);
+        sc += __shfl_xor_sync(0xffffffffu, sc, 16);
+        sc *= qm;
+        const bool all = c < fewest;                // every row sees this memory
+        if (!all && c >= (mine ? count[1] : count[0])) sc = -INFINITY;
+        if (__any_sync(0xffffffffu, sc > mx)) {     // few memories move a maximum
+            const float mn = fmaxf(mx, sc), f = exp2_fast(mx - mn);
+            l *= f;
+            mx = mn;
+            const float f0 = __shfl_sync(0xffffffffu, f, from), f1 = __shfl_sync(0xffffffffu, f, from + 4);
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[m][r] *= f[r & 1];
+            for (int m = 0; m < 4; ++m) {
+                o[m][0] *= f0; o[m][1] *= f1; o[m][2] *= f0; o[m][3] *= f1;
+            }
         }
-        if (__any_sync(0xffffffffu, wt[0] == 0.f || wt[1] == 0.f)) {
-            // 0 weight reads nothing, whatever the value is
+        const float wm = exp2_fast(sc - mx);
+        l += wm;
+        const float w0 = __shfl_sync(0xffffffffu, wm, from), w1 = __shfl_sync(0xffffffffu, wm, from + 4);
+        if (all) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (wt[r & 1] != 0.f) o[m][r] = fmaf(wt[r & 1], acc[NT - 1][m][r], o[m][r]);
+            for (int m = 0; m < 4; ++m) {
+                o[m][0] = fmaf(w0, acc[NT - 1][m][0], o[m][0]);
+                o[m][1] = fmaf(w1, acc[NT - 1][m][1], o[m][1]);
+                o[m][2] = fmaf(w0, acc[NT - 1][m][2], o[m][2]);
+                o[m][3] = fmaf(w1, acc[NT - 1][m][3], o[m][3]);
+            }
         } else {
+            // what a row does not see it does not read, whatever the value is
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[m][r] = fmaf(wt[r & 1], acc[NT - 1][m][r], o[m][r]);
+            for (int m = 0; m < 4; ++m) {
+                if (w0 != 0.f) { o[m][0] = fmaf(w0, acc[NT - 1][m][0], o[m][0]); o[m][2] = fmaf(w0, acc[NT - 1][m][2], o[m][2]); }
+                if (w1 != 0.f) { o[m][1] = fmaf(w1, acc[NT - 1][m][1], o[m][1]); o[m][3] = fmaf(w1, acc[NT - 1][m][3], o[m][3]); }
+            }
         }
     }
+    const float ml[2] = {__shfl_sync(0xffffffffu, mx, from), __shfl_sync(0xffffffffu, mx, from + 4)};
+    const float ll[2] = {__shfl_sync(0xffffffffu, l, from), __shfl_sync(0xffffffffu, l, from + 4)};
     // a whole item is written out, a part of one kept for the combine kernel
     const bool whole = w.whole();
     const int which = w.c > 0 ? 0 : 1;
@@ -404,18 +496,19 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const W
         if (whole) {
             if (left) continue;
             const size_t at = ((size_t)(t0 + t) * a.H + w.h) * kP + g;
-            const float inv = l[j] == 0.f ? 0.f : vs[j] / l[j];
+            const float f = ll[j] == 0.f ? 0.f : (a.y_ssd ? a.g : 1.f) * vs[j] / ll[j];
+            float y[4][2];      // all loads before the first store: out may be y_ssd itself
 #pragma unroll
             for (int m = 0; m < 4; ++m)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const size_t p = at + 16 * m + 8 * r;
-                    const float v = o[m][2 * r + j] * inv;
-                    a.out[p] = a.y_ssd ? fmaf(a.g, v, a.y_ssd[p]) : v;
-                }
+                for (int r = 0; r < 2; ++r) y[m][r] = a.y_ssd ? a.y_ssd[at + 16 * m + 8 * r] : 0.f;
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) a.out[at + 16 * m + 8 * r] = fmaf(f, o[m][2 * r + j], y[m][r]);
         } else {
             float* row = piece_rows<TT, kP>(a.part, run, which) + t * (kP + 4);
-            if (g == 0) { row[kP] = mx[j]; row[kP + 1] = left ? -1.f : l[j]; }
+            if (g == 0) { row[kP] = ml[j]; row[kP + 1] = left ? -1.f : ll[j]; }
 #pragma unroll
             for (int m = 0; m < 4; ++m)
 #pragma unroll
@@ -461,11 +554,10 @@ __global__ void __launch_bounds__(32 * M::kWarps, 1) sma_paged_mma_kernel(const 
             }
             continue;
         }
-        const int bad = first_bad_memory(a.cache.table + (size_t)b * a.cache.width, a.cache, w.memories());
         if (TT == 8 && rows > 4) {
-            if constexpr (TT == 8) run_piece<T, M, N, TT, 2, PARTS>(prm, s, w, run, t0, rows, bad, feed, taken, wc, ok);
+            if constexpr (TT == 8) run_piece<T, M, N, TT, 2, PARTS>(prm, s, w, run, t0, rows, feed, taken, wc, ok);
         } else {
-            run_piece<T, M, N, TT, 1, PARTS>(prm, s, w, run, t0, rows, bad, feed, taken, wc, ok);
+            run_piece<T, M, N, TT, 1, PARTS>(prm, s, w, run, t0, rows, feed, taken, wc, ok);
         }
     }
     // Every copy has been waited for, unless a wait gave up: what is in flight then
