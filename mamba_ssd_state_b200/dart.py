@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -57,6 +58,12 @@ class PagedCache(ctypes.Structure):
 
 
 DART_CACHE_DTYPE, DART_CACHE_MXFP4 = 0, 1
+
+# dart_dims and dart_paged_cache as bytes: what the calls that serve single tokens
+# pass, in a fifth of the time that filling a ctypes structure takes
+_pack_dims = struct.Struct("7i").pack
+_pack_cache = struct.Struct("4i3P").pack
+assert struct.calcsize("7i") == ctypes.sizeof(Dims) and struct.calcsize("4i3P") == ctypes.sizeof(PagedCache)
 
 _P = ctypes.c_void_p
 _lib = None
@@ -123,7 +130,7 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
     lib.dart_decode_step_noalloc.restype = ctypes.c_int
     lib.dart_decode_step_noalloc.argtypes = ([D, ctypes.c_int] + [_P] * 7 + [ctypes.c_float] + [_P] * 3
                                              + [ctypes.c_int] + [_P] * 4)
-    K = ctypes.POINTER(PagedCache)
+    D = K = _P       # packed by struct, or byref of the structures above
     lib.dart_cache_write_paged.restype = ctypes.c_int
     lib.dart_cache_write_paged.argtypes = [D, ctypes.c_int, _P, ctypes.c_int, _P, _P, K, _P]
     lib.dart_cache_read_paged.restype = ctypes.c_int
@@ -588,6 +595,15 @@ def _need(name, t, shape, dtype, index):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _groups(name, t, T, H) -> int:
+    """_bc_groups for packed tokens, [T,G,N] first."""
+    if t.dim() == 3:
+        rows, G, _ = t.shape
+        if rows == T and G >= 1 and H % G == 0:
+            return G
+    return _bc_groups(name, t, (T,), H)
+
+
 def _input(t, dtype, index):
     """A token tensor: copied to the device or made contiguous if need be."""
     if t.dtype is dtype and t.get_device() == index and t.is_contiguous():
@@ -608,33 +624,33 @@ def _call(fn, index, *args):
         _check(rc)
 
 
-def _paged(pages, scales, table, dtype, B, H, N, P, index) -> PagedCache:
+def _paged(pages, scales, table, dtype, B, H, N, P, index) -> bytes:
     """The C description of a paged cache, after checking it against the shapes it has to hold."""
     if index < 0:
         raise ValueError("pages must be a contiguous CUDA tensor")
-    if pages.dim() != 5 or table.dim() != 2:
-        raise ValueError(f"expected pages of 5 dimensions and a table of 2, got {tuple(pages.shape)} and {tuple(table.shape)}")
-    npages, _, R, _, _ = pages.shape
+    shape = pages.shape
+    if len(shape) != 5 or table.dim() != 2:
+        raise ValueError(f"expected pages of 5 dimensions and a table of 2, got {tuple(shape)} and {tuple(table.shape)}")
+    npages, _, R, _, _ = shape
     width = table.shape[1]
     tp = _need("table", table, (B, width), torch.int32, index)
     if pages.dtype is torch.uint8:
         if scales is None:
             raise TypeError("4-bit (uint8) pages need their uint8 scales")
-        return PagedCache(DART_CACHE_MXFP4, npages, R, width, _need("pages", pages, (npages, H, R, P, N // 2), torch.uint8, index),
-                          _need("scales", scales, (npages, H, R, P, N // 32), torch.uint8, index), tp)
+        return _pack_cache(DART_CACHE_MXFP4, npages, R, width, _need("pages", pages, (npages, H, R, P, N // 2), torch.uint8, index),
+                           _need("scales", scales, (npages, H, R, P, N // 32), torch.uint8, index), tp)
     if scales is not None:
         raise ValueError("scales belong to 4-bit (uint8) pages")
-    return PagedCache(DART_CACHE_DTYPE, npages, R, width, _need("pages", pages, (npages, H, R, N, P), dtype, index), None, tp)
+    return _pack_cache(DART_CACHE_DTYPE, npages, R, width, _need("pages", pages, (npages, H, R, N, P), dtype, index), 0, tp)
 
 
 def _move_pages(fn, write, dense, first, count, pages, table, scales):
     B, H, C, N, P = shape = dense.shape
-    dev = pages.get_device()
-    cache = ctypes.byref(_paged(pages, scales, table, dense.dtype, B, H, N, P, dev))
-    d = _need("dH" if write else "out", dense, shape, dense.dtype, dev)
+    dev, dtype = pages.get_device(), dense.dtype
+    cache = _paged(pages, scales, table, dtype, B, H, N, P, dev)
+    d = _need("dH" if write else "out", dense, shape, dtype, dev)
     f, c = _need("first", first, (B,), torch.int32, dev), _need("count", count, (B,), torch.int32, dev)
-    dims = ctypes.byref(Dims(B, 0, H, P, N, 1, 1))
-    _call(fn, dev, dims, _dtype_code(dense.dtype), *((d, C, f, c, cache) if write else (cache, f, c, d, C)))
+    _call(fn, dev, _pack_dims(B, 0, H, P, N, 1, 1), _dtype_code(dtype), *((d, C, f, c, cache) if write else (cache, f, c, d, C)))
 
 
 def dart_cache_write_paged(dH, first, count, pages, table, *, scales=None):
@@ -676,23 +692,46 @@ def dart_ssd_extend(x, dt, A, Bm, Cm, cu_tokens, state, dH_cur, pages, table, nc
     x, Bm, Cm = _input(x, dtype, dev), _input(Bm, dtype, dev), _input(Cm, dtype, dev)
     dt, A = _input(dt, f32, dev), _input(A, f32, dev)
     T = x.shape[0]
-    G = _bc_groups("Bm", Bm, (T,), H)
+    G = _groups("Bm", Bm, T, H)
     if Bm.shape[-1] != N or Cm.shape != Bm.shape:
         raise ValueError("Bm and Cm must both be [T,N] or [T,G,N] with the state's N")
-    state_out = state if state_out is None else state_out
-    dH_cur_out = dH_cur if dH_cur_out is None else dH_cur_out
-    nchunks_out = torch.empty_like(nchunks) if nchunks_out is None else nchunks_out
-    pos_out = torch.empty_like(pos) if pos_out is None else pos_out
-    y = torch.empty_like(x, dtype=f32) if y is None else y
-    mem_count = cu_tokens.new_empty(T) if mem_count is None else mem_count
-    _call(lib.dart_ssd_extend, dev, ctypes.byref(Dims(B, T, H, P, N, chunk, G)), _dtype_code(dtype),
-          _need("x", x, (T, H, P), dtype, dev), _need("dt", dt, (T, H), f32, dev), _need("A", A, (H,), f32, dev),
-          Bm.data_ptr(), Cm.data_ptr(), _need("cu_tokens", cu_tokens, (B + 1,), i32, dev),
-          _need("state", state, shape, f32, dev), _need("state_out", state_out, shape, f32, dev),
-          _need("dH_cur", dH_cur, shape, f32, dev), _need("dH_cur_out", dH_cur_out, shape, f32, dev),
-          ctypes.byref(cache), _need("nchunks", nchunks, (B,), i32, dev), _need("pos", pos, (B,), i32, dev),
-          _need("nchunks_out", nchunks_out, (B,), i32, dev), _need("pos_out", pos_out, (B,), i32, dev),
-          _need("y", y, (T, H, P), f32, dev), _need("mem_count", mem_count, (T,), i32, dev))
+    if x.shape != (T, H, P) or dt.shape != (T, H) or A.shape != (H,):
+        raise ValueError(f"x, dt and A: expected {(T, H, P)}, {(T, H)} and {(H,)}, got {tuple(x.shape)}, {tuple(dt.shape)} and {tuple(A.shape)}")
+    sp, cp = _need("state", state, shape, f32, dev), _need("dH_cur", dH_cur, shape, f32, dev)
+    np_, pp = _need("nchunks", nchunks, (B,), i32, dev), _need("pos", pos, (B,), i32, dev)
+    cup = _need("cu_tokens", cu_tokens, (B + 1,), i32, dev)
+    # what is not given: in place, or made like a tensor that was checked
+    so, co = sp, cp
+    if state_out is None:
+        state_out = state
+    else:
+        so = _need("state_out", state_out, shape, f32, dev)
+    if dH_cur_out is None:
+        dH_cur_out = dH_cur
+    else:
+        co = _need("dH_cur_out", dH_cur_out, shape, f32, dev)
+    if nchunks_out is None:
+        nchunks_out = torch.empty_like(nchunks)
+        nop = nchunks_out.data_ptr()
+    else:
+        nop = _need("nchunks_out", nchunks_out, (B,), i32, dev)
+    if pos_out is None:
+        pos_out = torch.empty_like(pos)
+        pop = pos_out.data_ptr()
+    else:
+        pop = _need("pos_out", pos_out, (B,), i32, dev)
+    if y is None:
+        y = torch.empty_like(x, dtype=f32)
+        yp = y.data_ptr()
+    else:
+        yp = _need("y", y, (T, H, P), f32, dev)
+    if mem_count is None:
+        mem_count = cu_tokens.new_empty(T)
+        mp = mem_count.data_ptr()
+    else:
+        mp = _need("mem_count", mem_count, (T,), i32, dev)
+    _call(lib.dart_ssd_extend, dev, _pack_dims(B, T, H, P, N, chunk, G), _dtype_code(dtype), x.data_ptr(), dt.data_ptr(),
+          A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), cup, sp, so, cp, co, cache, np_, pp, nop, pop, yp, mp)
     return {"y": y, "state": state_out, "dH_cur": dH_cur_out, "nchunks": nchunks_out, "pos": pos_out,
             "mem_count": mem_count}
 
@@ -716,22 +755,30 @@ def dart_sma_paged(Q, E, Cm, cu_tokens, pages, table, mem_count, g: float, y_ssd
     B = table.shape[0]
     cache = _paged(pages, scales, table, dtype, B, H, N, P, dev)
     Q, E, Cm = _input(Q, dtype, dev), _input(E, dtype, dev), _input(Cm, dtype, dev)
-    G = _bc_groups("Cm", Cm, (T,), H)
+    G = _groups("Cm", Cm, T, H)
     if Cm.shape[-1] != N:
         raise ValueError(f"Cm: expected {N} columns, got {Cm.shape[-1]}")
     shape = (T, H, P)
     yp = None if y_ssd is None else _need("y_ssd", y_ssd, shape, f32, dev)
-    out = torch.empty_like(E, dtype=f32) if out is None else out
-    dims = ctypes.byref(Dims(B, T, H, P, N, 1, G))
+    if E.shape != shape:
+        raise ValueError(f"E: expected shape {shape}, got {tuple(E.shape)}")
+    if out is None:
+        out = torch.empty_like(E, dtype=f32)
+        op = out.data_ptr()
+    else:
+        op = _need("out", out, shape, f32, dev)
+    dims = _pack_dims(B, T, H, P, N, 1, G)
     if workspace is None:
         n = _SMA_PAGED_WORKSPACE.get(P)
         if n is None:
             n = _SMA_PAGED_WORKSPACE[P] = lib.dart_sma_paged_workspace_bytes(dims)
         workspace = table.new_empty(n // 4)
-    _call(lib.dart_sma_paged, dev, dims, _dtype_code(dtype), Q.data_ptr(), _need("E", E, shape, dtype, dev), Cm.data_ptr(),
-          _need("cu_tokens", cu_tokens, (B + 1,), i32, dev), ctypes.byref(cache),
-          _need("mem_count", mem_count, (T,), i32, dev), g, yp, _need("out", out, shape, f32, dev),
-          _need("workspace", workspace, workspace.shape, workspace.dtype, dev), workspace.numel() * workspace.element_size())
+        wp = workspace.data_ptr()
+    else:
+        n = workspace.numel() * workspace.element_size()
+        wp = _need("workspace", workspace, workspace.shape, workspace.dtype, dev)
+    _call(lib.dart_sma_paged, dev, dims, _dtype_code(dtype), Q.data_ptr(), E.data_ptr(), Cm.data_ptr(),
+          _need("cu_tokens", cu_tokens, (B + 1,), i32, dev), cache, _need("mem_count", mem_count, (T,), i32, dev), g, yp, op, wp, n)
     return out
 
 
