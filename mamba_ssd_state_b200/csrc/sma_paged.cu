@@ -5,92 +5,131 @@
 //   u = Q_t^T M_c,  v = C_t^T M_c,  s = u . E_t / sqrt(N),
 //   o = sum_c softmax_c(s) v_c,  out = y_ssd + g o        (o = 0 with none visible).
 //
-// A warp takes a memory at a time, a lane two of its columns: it streams the
-// rows past up to 8 tokens held as pairs, so a value is loaded once for
-// 2 x 8 products.  Scores are summed over the warp, the softmax runs online in
-// base 2, and v is folded into the lane's own columns, so that the eight warps
-// of a block meet only at the end of a piece.
+// Every warp is a worker of its own, with its run of units and its ring of stages
+// (16 rows of a memory each, copied ahead over the ends of items): a lane has two
+// columns of a row, and a value is used for U and V of up to 8 tokens, whose Q
+// and C stand in the warp's own shared memory.  Scores are summed over the warp,
+// the softmax runs online in base 2, and v is folded into the lane's columns.
+// (With eight warps to a piece and loads straight from global memory, 7 runs of
+// 5 float32 tokens over 45 memories of 8 heads took 32 us; this takes 30.)
 #include "sm100.cuh"
 #include "sma_paged.cuh"
 
+#include <float.h>
+
 namespace dart {
 namespace {
+
+using namespace sm100;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTT = 8;        // tokens of a tile
 constexpr int kCap = 4096;    // tiles of a call
-constexpr int kLeast = 8;     // units below which a run is not cut
+constexpr int kLeast = 1;     // units below which a run is not cut
 
-template <int N, int P>
-struct Smem {
-    TileList<kCap> tiles;
-    float qc[N][2 * kTT];              // Q (times log2(e) / sqrt(N)) and C of the tile's tokens
-    float m[kWarps][kTT], l[kWarps][kTT];
-    float o[kWarps][kTT][P];
-    int count[kTT], bad;
-};
+struct Params { SmaPagedArgs a; };
 
-// Rows of a memory as (n, two columns) for this lane, eight at a time.
 template <typename T, int N, int P>
-struct Rows {
-    static constexpr int LPR = P / 2, RPW = 32 / LPR;      // lanes of a row, rows of a warp load
-    static constexpr int STEPS = N / RPW, BATCH = STEPS < 8 ? STEPS : 8;
-    const T* at;
-    __device__ Rows(const PagedCache& c, size_t mem, int lane)
-        : at(static_cast<const T*>(c.pages) + mem * (size_t)(N * P) + (lane / LPR) * P + 2 * (lane % LPR)) {}
-    __device__ __forceinline__ static int row(int step, int lane) { return step * RPW + lane / LPR; }
-    __device__ __forceinline__ void load(int step, float2 (&v)[BATCH]) {
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            const T* p = at + (size_t)(step + i) * RPW * P;
-            if constexpr (sizeof(T) == 4) {
-                v[i] = __ldcs(reinterpret_cast<const float2*>(p));
-            } else {
-                const unsigned w = __ldcs(reinterpret_cast<const unsigned*>(p));
-                v[i] = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-            }
-        }
+struct Dense {
+    static constexpr int kRows = 16, kStages = N == 128 ? 3 : 4, kPieces = N / kRows;      // rows of a stage
+    static constexpr uint32_t kStageBytes = kRows * P * sizeof(T);
+    static __device__ __forceinline__ void copy(const Params& prm, size_t mem, int piece, uint32_t dst, uint32_t full) {
+        bulk_load(dst, static_cast<const T*>(prm.a.cache.pages) + (mem * N + piece * kRows) * P, kStageBytes, full);
     }
 };
 
-// This warp's memories of a piece for the first NT tokens of the tile.
-template <typename T, int N, int P, int NT>
-__device__ __forceinline__ void run_piece(const SmaPagedArgs& a, Smem<N, P>& s, const Walk& w, const int* table, const float2 (&e)[kTT]) {
-    using R = Rows<T, N, P>;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+template <typename M, int N>
+struct Smem {
+    alignas(16) uint8_t ring[kWarps][M::kStages][M::kStageBytes];
+    alignas(16) float qc[kWarps][N][2 * kTT];      // Q (times log2(e) / sqrt(N)) and C of a tile's tokens
+    uint64_t full[kWarps][M::kStages];
+    int abort_flag;
+    TileList<kCap> tiles;
+};
+
+// A piece of a run for the first NT tokens of the tile.
+template <typename T, int N, int P, int NT, typename M>
+__device__ __forceinline__ void run_piece(const Params& prm, Smem<M, N>& s, const Walk& w, int run, int t0, int rows,
+                                          Feed<M, kCap>& feed, int& taken, const WaitCtx& wc, bool& ok) {
+    constexpr int LPR = P / 2, RPW = 32 / LPR;      // lanes of a row, rows of the warp at a time
+    const SmaPagedArgs& a = prm.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = group_of(w.h, a.H, a.G);
+    const float qscale = kLog2e * rsqrtf((float)N);
+    float(*qc)[2 * kTT] = s.qc[warp];
+    int count[NT];
+    float2 e[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const bool live = t < rows;
+        const size_t tok = (size_t)(t0 + t);
+        count[t] = live ? a.mem_count[t0 + t] : -1;
+        e[t] = make_float2(0.f, 0.f);
+        if (live) {
+            const T* src = static_cast<const T*>(a.E) + (tok * a.H + w.h) * P + 2 * (lane % LPR);
+            e[t] = make_float2(ldf(src), ldf(src + 1));
+        }
+#pragma unroll
+        for (int n = lane; n < N; n += 32) {
+            qc[n][t] = live ? qscale * ldf(static_cast<const T*>(a.Q) + (tok * a.H + w.h) * N + n) : 0.f;
+            qc[n][kTT + t] = live ? ldf(static_cast<const T*>(a.Cm) + (tok * a.G + grp) * N + n) : 0.f;
+        }
+    }
+    const int bad = first_bad_memory(a.cache.table + (size_t)s.tiles.seq[w.k] * a.cache.width, a.cache, w.memories());
+    __syncwarp();
     float m[NT], l[NT];
     float2 o[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) { m[t] = -INFINITY; l[t] = 0.f; o[t] = make_float2(0.f, 0.f); }
-    const int last = min(w.last_memory(), s.bad);
-    for (int c = w.first_memory() + warp; c < last; c += kWarps) {
-        R rows(a.cache, memory_index(a.cache, a.H, table[c / a.cache.R], w.h, c % a.cache.R), lane);
+    for (int t = 0; t < NT; ++t) { m[t] = -FLT_MAX; l[t] = 0.f; o[t] = make_float2(0.f, 0.f); }
+    const int last = min(w.last_memory(), bad);
+    for (int c = w.first_memory(); c < last; ++c) {
         float2 u[NT], v[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) u[t] = v[t] = make_float2(0.f, 0.f);
-        for (int st = 0; st < R::STEPS; st += R::BATCH) {
-            float2 x[R::BATCH];
-            rows.load(st, x);
+#pragma unroll 1
+        for (int k = 0; k < M::kPieces; ++k) {
+            const int st = taken % M::kStages;
+            if (ok) ok = mbar_wait_warp(smem_u32(&s.full[warp][st]), (uint32_t)(taken / M::kStages) & 1u, wc, 1);
+            ++taken;
+            if (!ok) continue;
+            const T* rows_s = reinterpret_cast<const T*>(s.ring[warp][st]) + (lane / LPR) * P + 2 * (lane % LPR);
 #pragma unroll
-            for (int i = 0; i < R::BATCH; ++i) {
-                const float* qc = s.qc[R::row(st + i, lane)];
+            for (int r = 0; r < M::kRows / RPW; ++r) {
+                float2 x;
+                if constexpr (sizeof(T) == 4) {
+                    x = *reinterpret_cast<const float2*>(rows_s + r * RPW * P);
+                } else {
+                    const unsigned b = *reinterpret_cast<const unsigned*>(rows_s + r * RPW * P);
+                    x = make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+                }
+                const float* f = qc[k * M::kRows + r * RPW + lane / LPR];
+                alignas(16) float fq[(NT + 3) / 4 * 4], fc[(NT + 3) / 4 * 4];
+#pragma unroll
+                for (int t = 0; t < NT; t += 4) {
+                    if constexpr (NT == 1) {
+                        fq[0] = f[0];
+                        fc[0] = f[kTT];
+                    } else {
+                        *reinterpret_cast<float4*>(fq + t) = *reinterpret_cast<const float4*>(f + t);
+                        *reinterpret_cast<float4*>(fc + t) = *reinterpret_cast<const float4*>(f + kTT + t);
+                    }
+                }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    u[t].x = fmaf(qc[t], x[i].x, u[t].x);
-                    u[t].y = fmaf(qc[t], x[i].y, u[t].y);
-                    v[t].x = fmaf(qc[kTT + t], x[i].x, v[t].x);
-                    v[t].y = fmaf(qc[kTT + t], x[i].y, v[t].y);
+                    u[t].x = fmaf(fq[t], x.x, u[t].x);
+                    u[t].y = fmaf(fq[t], x.y, u[t].y);
+                    v[t].x = fmaf(fc[t], x.x, v[t].x);
+                    v[t].y = fmaf(fc[t], x.y, v[t].y);
                 }
             }
+            __syncwarp();        // every lane has read the stage
+            feed.fill(prm, s.tiles, s.ring[warp], s.full[warp]);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const float sc = warp_sum(fmaf(u[t].x, e[t].x, u[t].y * e[t].y));
-            if (c < s.count[t]) {                     // the row sees this memory (same for the whole warp)
-                const float mn = fmaxf(m[t], sc);
-                const bool none = mn == -INFINITY;    // only scores of -inf so far: they weigh nothing
-                const float al = none ? 1.f : exp2f(m[t] - mn), wt = none ? (sc == sc ? 0.f : sc) : exp2f(sc - mn);
+            if (c < count[t]) {                       // the row sees this memory (same for the whole warp)
+                const float mn = fmaxf(m[t], sc), al = exp2f(m[t] - mn), wt = exp2f(sc - mn);
                 l[t] = fmaf(l[t], al, wt);
                 m[t] = mn;
                 if (wt != 0.f) {                      // 0 weight reads nothing, whatever the value is
@@ -100,91 +139,67 @@ __device__ __forceinline__ void run_piece(const SmaPagedArgs& a, Smem<N, P>& s, 
             }
         }
     }
-    // a lane's o holds the rows it read: sum over the lanes of the same columns
+    // a whole item is written out, a part of one kept for the combine kernel
+    const int which = w.c > 0 ? 0 : 1;
+    if (!w.whole() && lane == 0) *piece_header(a.part, run, which) = PieceHeader{w.last == w.units ? 2 : 1, t0, rows, w.h};
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
+        // a lane's o holds the rows it read: sum over the lanes of the same columns
 #pragma unroll
-        for (int off = P / 2; off < 32; off <<= 1) {
+        for (int off = LPR; off < 32; off <<= 1) {
             o[t].x += __shfl_xor_sync(0xffffffffu, o[t].x, off);
             o[t].y += __shfl_xor_sync(0xffffffffu, o[t].y, off);
         }
-        if (lane < P / 2) *reinterpret_cast<float2*>(&s.o[warp][t][2 * lane]) = o[t];
-        if (lane == 0) { s.m[warp][t] = m[t]; s.l[warp][t] = l[t]; }
+        if (t >= rows || lane >= LPR) continue;
+        const bool left = count[t] < 0 || count[t] > bad;      // a row that is not to be computed
+        if (w.whole()) {
+            if (left) continue;
+            const size_t at = ((size_t)(t0 + t) * a.H + w.h) * P + 2 * lane;
+            const float f = l[t] == 0.f ? 0.f : (a.y_ssd ? a.g : 1.f) / l[t];
+            const float2 y = a.y_ssd ? *reinterpret_cast<const float2*>(a.y_ssd + at) : make_float2(0.f, 0.f);
+            *reinterpret_cast<float2*>(a.out + at) = make_float2(fmaf(f, o[t].x, y.x), fmaf(f, o[t].y, y.y));
+        } else {
+            float* row = piece_rows<kTT, P>(a.part, run, which) + t * (P + 4);
+            *reinterpret_cast<float2*>(row + 2 * lane) = o[t];
+            if (lane == 0) { row[P] = m[t]; row[P + 1] = left ? -1.f : l[t]; }
+        }
     }
+    __syncwarp();        // qc is read no more
 }
 
 template <typename T, int N, int P>
-__global__ void __launch_bounds__(kThreads) sma_paged_kernel(SmaPagedArgs a) {
-    extern __shared__ __align__(16) uint8_t raw[];
-    Smem<N, P>& s = *reinterpret_cast<Smem<N, P>*>(raw);
-    const int tid = threadIdx.x, lane = tid & 31;
-    build_tiles<kTT, kCap>(a, s.tiles);
-    if (tid < 2) piece_header(a.part, blockIdx.x, tid)->state = 0;
-    if (s.tiles.n == 0) return;
-    const float qscale = kLog2e * rsqrtf((float)N);
-    __syncthreads();
-    for (Walk w = start_walk(s.tiles, a.H, blockIdx.x, gridDim.x, kLeast); next_piece(w); advance(s.tiles, w, a.H)) {
-        const int b = s.tiles.seq[w.k], t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, b, t0, kTT);
-        const int* table = a.cache.table + (size_t)b * a.cache.width;
-        __syncthreads();
-        const int grp = group_of(w.h, a.H, a.G);
-        for (int i = tid; i < kTT * N; i += kThreads) {
-            const int t = i / N, n = i % N;
-            const bool live = t < rows;
-            s.qc[n][t] = live ? qscale * ldf(static_cast<const T*>(a.Q) + ((size_t)(t0 + t) * a.H + w.h) * N + n) : 0.f;
-            s.qc[n][kTT + t] = live ? ldf(static_cast<const T*>(a.Cm) + ((size_t)(t0 + t) * a.G + grp) * N + n) : 0.f;
-        }
-        if (tid < kTT) s.count[tid] = tid < rows ? a.mem_count[t0 + tid] : -1;
-        if (tid < 32) {
-            const int seen = w.memories();     // the most that a row of the tile sees
-            const int bad = first_bad_memory(table, a.cache, seen);
-            if (lane == 0) {
-                s.bad = bad;
-                if (bad < seen) flag_status(a.status, kStatusDevice);
-            }
-        }
-        float2 e[kTT];
-#pragma unroll
-        for (int t = 0; t < kTT; ++t) {
-            e[t] = make_float2(0.f, 0.f);
-            if (t < rows) {
-                const T* src = static_cast<const T*>(a.E) + ((size_t)(t0 + t) * a.H + w.h) * P + 2 * (lane % (P / 2));
-                e[t] = make_float2(ldf(src), ldf(src + 1));
-            }
-        }
-        __syncthreads();
-        if (rows == 1) run_piece<T, N, P, 1>(a, s, w, table, e);
-        else if (rows <= 4) run_piece<T, N, P, 4>(a, s, w, table, e);
-        else run_piece<T, N, P, 8>(a, s, w, table, e);
-        __syncthreads();
-        // join the warps: a whole item is written out, a part of one kept for the combine kernel
-        const int which = w.c > 0 ? 0 : 1;
-        if (!w.whole() && tid == 0)
-            *piece_header(a.part, blockIdx.x, which) = PieceHeader{w.last == w.units ? 2 : 1, t0, rows, w.h};
-        for (int i = tid; i < rows * P; i += kThreads) {
-            const int t = i / P, p = i % P;
-            float mm = -INFINITY, l = 0.f, o = 0.f;
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, s.m[k][t]);
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                const float f = s.l[k][t] == 0.f ? 0.f : exp2f(s.m[k][t] - mm);
-                l = fmaf(s.l[k][t], f, l);
-                if (f != 0.f) o = fmaf(s.o[k][t][p], f, o);
-            }
-            const bool left = s.count[t] < 0 || s.count[t] > s.bad;   // a row that is not to be computed
-            if (w.whole()) {
-                if (left) continue;
-                const size_t at = ((size_t)(t0 + t) * a.H + w.h) * P + p;
-                const float r = l == 0.f ? 0.f : o / l;
-                a.out[at] = a.y_ssd ? fmaf(a.g, r, a.y_ssd[at]) : r;
-            } else {
-                float* row = piece_rows<kTT, P>(a.part, blockIdx.x, which) + t * (P + 4);
-                if (p == 0) { row[P] = mm; row[P + 1] = left ? -1.f : l; }
-                row[p] = o;
-            }
-        }
+__global__ void __launch_bounds__(kThreads, 1) sma_paged_kernel(const __grid_constant__ Params prm) {
+    using M = Dense<T, N, P>;
+    extern __shared__ __align__(128) uint8_t raw[];
+    Smem<M, N>& s = *reinterpret_cast<Smem<M, N>*>(raw);
+    const SmaPagedArgs& a = prm.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < kWarps * M::kStages; ++i) mbar_init(smem_u32(&s.full[0][0] + i), 1);
+        s.abort_flag = 0;
+        fence_mbar_init();
     }
+    // neighbours in the order of units go to different blocks: a few units spread over all of them
+    const int runs = gridDim.x * kWarps, run = warp * gridDim.x + blockIdx.x;
+    griddep_wait();
+    if (lane < 2) piece_header(a.part, run, lane)->state = 0;
+    __syncwarp();
+    build_tiles<kTT, kCap>(a, s.tiles);
+    if (s.tiles.n == 0) return;
+    const WaitCtx wc{&s.abort_flag, a.status, 12};
+    bool ok = true;
+    int taken = 0;
+    Walk w = start_walk(s.tiles, a.H, run, runs, kLeast);
+    Feed<M, kCap> feed;
+    feed.begin(a, s.tiles, w);
+    for (int i = 0; i < M::kStages; ++i) feed.fill(prm, s.tiles, s.ring[warp], s.full[warp]);
+    for (; next_piece(w); advance(s.tiles, w, a.H)) {
+        const int t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, s.tiles.seq[w.k], t0, kTT);
+        if (rows == 1) run_piece<T, N, P, 1>(prm, s, w, run, t0, rows, feed, taken, wc, ok);
+        else if (rows <= 4) run_piece<T, N, P, 4>(prm, s, w, run, t0, rows, feed, taken, wc, ok);
+        else run_piece<T, N, P, 8>(prm, s, w, run, t0, rows, feed, taken, wc, ok);
+    }
+    if (!ok) feed.drain(s.full[warp]);      // else every copy has been waited for
 }
 
 // Block (i, y) joins ROWS rows, from row ROWS y on, of the item that begins in
@@ -194,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) sma_paged_kernel(SmaPagedArgs a) {
 template <int TT, int P, int ROWS>
 __global__ void __launch_bounds__(ROWS * P / 4) sma_paged_combine_kernel(SmaPagedArgs a, int runs) {
     constexpr int COLS = P / 4, SUB = ROWS;                  // threads of a row, of a column
-    constexpr int AHEAD = 4;                                 // pieces read at a time
+    constexpr int AHEAD = 8;                                 // pieces read at a time
     sm100::griddep_wait();
     const PieceHeader hd = *piece_header(a.part, blockIdx.x, 1);
     const int r0 = ROWS * blockIdx.y, rows = min(ROWS, hd.rows - r0);
@@ -263,16 +278,17 @@ __global__ void __launch_bounds__(ROWS * P / 4) sma_paged_combine_kernel(SmaPage
 template <typename T, int N, int P>
 cudaError_t run(const SmaPagedArgs& a, cudaStream_t st) {
     auto kern = sma_paged_kernel<T, N, P>;
-    const int smem = (int)sizeof(Smem<N, P>), sms = paged_sm_count();
+    constexpr int smem = (int)sizeof(Smem<Dense<T, N, P>, N>);
+    static_assert(smem <= 232448, "shared memory");
+    const int sms = paged_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     static std::atomic<unsigned long long> ready{0};   // devices whose kernel has its shared memory allowed
     cudaError_t e = paged_allow_smem(reinterpret_cast<const void*>(kern), smem, ready);
     if (e != cudaSuccess) return e;
-    const int blocks = min(2 * sms, kMaxRuns);
-    kern<<<blocks, kThreads, smem, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int blocks = min(sms, kMaxRuns / kWarps);
+    if ((e = launch_dependent(kern, dim3(blocks), dim3(kThreads), smem, st, 1, Params{a})) != cudaSuccess) return e;
     count_launches(1);
-    return launch_sma_paged_combine(a, blocks, kTT, st);
+    return launch_sma_paged_combine(a, blocks * kWarps, kTT, st);
 }
 
 }  // namespace

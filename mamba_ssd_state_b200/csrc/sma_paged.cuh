@@ -15,6 +15,7 @@
 #pragma once
 
 #include "dart_paged.cuh"
+#include "sm100.cuh"
 
 namespace dart {
 
@@ -168,7 +169,7 @@ __device__ __forceinline__ long long quick_div(long long a, long long b) {
 }
 
 // Run i of `runs`; runs of fewer than `least` units are not cut smaller, and a
-// cut that falls into the units that stand for an item goes before them.
+// cut that would leave a run with an item but none of its memories goes before it.
 template <int CAP>
 __device__ __forceinline__ Walk start_walk(const TileList<CAP>& L, int H, int i, int runs, int least) {
     const long long W = (long long)L.pre[L.n] * H;
@@ -184,7 +185,7 @@ __device__ __forceinline__ Walk start_walk(const TileList<CAP>& L, int H, int i,
         const long long r = u - (long long)L.pre[w.k] * H;
         w.h = (int)quick_div(r, w.units);
         w.c = (int)(r - (long long)w.h * w.units);
-        if (w.c < kItemUnits) {
+        if (w.c <= kItemUnits) {           // no memory before the cut
             w.u -= w.c;
             w.c = 0;
         }
@@ -240,6 +241,79 @@ __device__ __forceinline__ int first_bad_memory(const int* table, const PagedCac
     }
     return count;
 }
+
+// What a warp that works by itself copies: the memories of its run, piece by
+// piece, into the stages of its ring, ahead of what it multiplies and over the
+// ends of items.  M says how a memory is kept: kStages, kStageBytes, kPieces
+// pieces of a memory, and copy(params, memory, piece, shared address, barrier).
+template <typename M, int CAP>
+struct Feed {
+    Walk w;
+    const int* table;        // the sequence's
+    int c, last, piece;      // next memory and piece of it, end of the memories of this part of the run
+    int slot, idx;           // where memory c is: slot of the page table[idx]
+    int page, ahead;         // table[idx] and, loaded long before it is needed, the next entry
+    int issued;              // stages filled
+    bool more;
+
+    __device__ __forceinline__ void begin(const SmaPagedArgs& a, const TileList<CAP>& L, const Walk& walk) {
+        w = walk;
+        issued = 0;
+        start(a, L);
+    }
+    __device__ __forceinline__ void look_ahead(int R) { ahead = (idx + 1) * R < last ? table[idx + 1] : 0; }
+    __device__ __forceinline__ void start(const SmaPagedArgs& a, const TileList<CAP>& L) {
+        // to the next part of the run that has memories to copy
+        while ((more = next_piece(w))) {
+            table = a.cache.table + (size_t)L.seq[w.k] * a.cache.width;
+            const int seen = w.memories();
+            c = w.first_memory();
+            last = w.last_memory();
+            piece = 0;
+            if (c < last) {
+                idx = c / a.cache.R;
+                slot = c - idx * a.cache.R;
+                page = table[idx];
+                look_ahead(a.cache.R);
+            }
+            const int bad = first_bad_memory(table, a.cache, seen);
+            if (bad < seen && (threadIdx.x & 31) == 0) flag_status(a.status, kStatusDevice);
+            last = min(last, bad);
+            if (c < last) return;
+            advance(L, w, a.H);
+        }
+    }
+    template <typename Params, typename Stage>
+    __device__ __forceinline__ void fill(const Params& prm, const TileList<CAP>& L, Stage* ring, uint64_t* full) {
+        if (!more) return;
+        const SmaPagedArgs& a = prm.a;
+        const int st = issued % M::kStages;
+        if ((threadIdx.x & 31) == 0) {
+            const uint32_t bar = sm100::smem_u32(full + st);
+            sm100::mbar_expect_tx(bar, M::kStageBytes);
+            M::copy(prm, memory_index(a.cache, a.H, page, w.h, slot), piece, sm100::smem_u32(ring + st), bar);
+        }
+        ++issued;
+        if (++piece == M::kPieces) {
+            piece = 0;
+            if (++c == last) {
+                advance(L, w, a.H);
+                start(a, L);
+            } else if (++slot == a.cache.R) {
+                slot = 0;
+                page = ahead;
+                ++idx;
+                look_ahead(a.cache.R);
+            }
+        }
+    }
+    // After a wait gave up: what is in flight is waited for (with a limit) before its shared memory goes.
+    __device__ __forceinline__ void drain(uint64_t* full) const {
+        if ((threadIdx.x & 31) != 0) return;
+        for (int i = max(0, issued - M::kStages); i < issued; ++i)
+            for (int k = 0; k < (1 << 20) && !sm100::mbar_try_wait(sm100::smem_u32(full + i % M::kStages), (uint32_t)(i / M::kStages) & 1u); ++k) {}
+    }
+};
 
 #endif
 

@@ -45,18 +45,30 @@ constexpr int kP = 64;
 constexpr int kCap = 4096;                      // tiles of a call
 constexpr int kLeast = 1;                       // units below which a run is not cut
 
+struct Params {
+    CUtensorMap map;      // bfloat16 memories: (P, rows of N), boxes of one memory
+    SmaPagedArgs a;
+};
+
 // What a memory is kept as, and the stages it passes through: kPieces of them.
 template <int N> struct Bf16Mem {
     static constexpr bool kFp4 = false;
     static constexpr int kWarps = 8, kStages = 2;             // 128 KB of copies in flight
     static constexpr int kRows = 64, kPieces = N / kRows;     // rows of a stage
     static constexpr uint32_t kStageBytes = kRows * kP * 2;
+    static __device__ __forceinline__ void copy(const Params& prm, size_t mem, int piece, uint32_t dst, uint32_t full) {
+        tma_load_2d(dst, &prm.map, full, 0, (int)(mem * N) + piece * kRows);
+    }
 };
 template <int N> struct Fp4Mem {
     static constexpr bool kFp4 = true;
     static constexpr int kWarps = 12, kStages = 3, kPieces = 1;
     static constexpr uint32_t kCodeBytes = N * kP / 2, kScaleBytes = N * kP / 32;
     static constexpr uint32_t kStageBytes = kCodeBytes + kScaleBytes;
+    static __device__ __forceinline__ void copy(const Params& prm, size_t mem, int, uint32_t dst, uint32_t full) {
+        bulk_load(dst, static_cast<const uint8_t*>(prm.a.cache.pages) + mem * kCodeBytes, kCodeBytes, full);
+        bulk_load(dst + kCodeBytes, prm.a.cache.scales + mem * kScaleBytes, kScaleBytes, full);
+    }
 };
 
 template <typename M>
@@ -69,10 +81,6 @@ struct Smem {
 
 template <int I> struct Piece { static constexpr int value = I; };
 
-struct Params {
-    CUtensorMap map;      // bfloat16 memories: (P, rows of N), boxes of one memory
-    SmaPagedArgs a;
-};
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -289,76 +297,11 @@ __device__ __forceinline__ bool multiply(const uint8_t* stage, const Column<M, N
     }
 }
 
-// What a worker copies: the memories of its run, piece by piece, ahead of the
-// part of it that multiplies.
-template <typename M, int N, int TT>
-struct Feed {
-    Walk w;
-    const int* table;        // the sequence's
-    int c, last, piece;      // next memory and piece of it, end of the memories of this part of the run
-    int slot, idx;           // where memory c is: slot of the page table[idx]
-    int page, ahead;         // table[idx] and, loaded long before it is needed, the next entry
-    int issued;              // stages filled
-    bool more;
-
-    __device__ __forceinline__ void look_ahead(int R) { ahead = (idx + 1) * R < last ? table[idx + 1] : 0; }
-    __device__ __forceinline__ void start(const SmaPagedArgs& a, const TileList<kCap>& L) {
-        // to the next part of the run that has memories to copy
-        while ((more = next_piece(w))) {
-            table = a.cache.table + (size_t)L.seq[w.k] * a.cache.width;
-            const int seen = w.memories();
-            c = w.first_memory();
-            last = w.last_memory();
-            piece = 0;
-            if (c < last) {
-                idx = c / a.cache.R;
-                slot = c - idx * a.cache.R;
-                page = table[idx];
-                look_ahead(a.cache.R);
-            }
-            const int bad = first_bad_memory(table, a.cache, seen);
-            if (bad < seen && (threadIdx.x & 31) == 0) flag_status(a.status, kStatusDevice);
-            last = min(last, bad);
-            if (c < last) return;
-            advance(L, w, a.H);
-        }
-    }
-    __device__ __forceinline__ void fill(const Params& prm, Smem<M>& s) {
-        if (!more) return;
-        const SmaPagedArgs& a = prm.a;
-        const int st = issued % M::kStages, warp = threadIdx.x >> 5;
-        if ((threadIdx.x & 31) == 0) {
-            const size_t mem = memory_index(a.cache, a.H, page, w.h, slot);
-            const uint32_t full = smem_u32(&s.full[warp][st]), dst = smem_u32(s.ring[warp][st]);
-            mbar_expect_tx(full, M::kStageBytes);
-            if constexpr (M::kFp4) {
-                bulk_load(dst, static_cast<const uint8_t*>(a.cache.pages) + mem * M::kCodeBytes, M::kCodeBytes, full);
-                bulk_load(dst + M::kCodeBytes, a.cache.scales + mem * M::kScaleBytes, M::kScaleBytes, full);
-            } else {
-                tma_load_2d(dst, &prm.map, full, 0, (int)(mem * N) + piece * M::kRows);
-            }
-        }
-        ++issued;
-        if (++piece == M::kPieces) {
-            piece = 0;
-            if (++c == last) {
-                advance(s.tiles, w, a.H);
-                start(a, s.tiles);
-            } else if (++slot == a.cache.R) {
-                slot = 0;
-                page = ahead;
-                ++idx;
-                look_ahead(a.cache.R);
-            }
-        }
-    }
-};
-
 // One piece of the run.  NT = 1: columns 0-3 of the tile are Q and 4-7 C of up to
 // 4 tokens; NT = 2: a tile each of up to 8.
 template <typename T, typename M, int N, int TT, int NT, int PARTS>
 __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const Walk& w, int run, int t0, int rows,
-                                          Feed<M, N, TT>& feed, int& taken, const WaitCtx& wc, bool& ok) {
+                                          Feed<M, kCap>& feed, int& taken, const WaitCtx& wc, bool& ok) {
     const SmaPagedArgs& a = prm.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
     const int grp = group_of(w.h, a.H, a.G);
@@ -433,7 +376,7 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const W
             if (!ok) return;
             clean &= multiply<M, N, NT, PARTS, decltype(piece)::value>(s.ring[warp][st], col, acc);
             __syncwarp();        // every lane has read the stage
-            feed.fill(prm, s);
+            feed.fill(prm, s.tiles, s.ring[warp], s.full[warp]);
         };
         take(Piece<0>{});
         if constexpr (M::kPieces == 2) take(Piece<1>{});
@@ -538,12 +481,10 @@ __global__ void __launch_bounds__(32 * M::kWarps, 1) sma_paged_mma_kernel(const 
     const WaitCtx wc{&s.abort_flag, a.status, 10};
     bool ok = true;
     int taken = 0;
-    Feed<M, N, TT> feed;
-    feed.w = start_walk(s.tiles, a.H, run, runs, kLeast);
-    feed.issued = 0;
-    Walk w = feed.w;
-    feed.start(a, s.tiles);
-    for (int i = 0; i < M::kStages; ++i) feed.fill(prm, s);
+    Walk w = start_walk(s.tiles, a.H, run, runs, kLeast);
+    Feed<M, kCap> feed;
+    feed.begin(a, s.tiles, w);
+    for (int i = 0; i < M::kStages; ++i) feed.fill(prm, s.tiles, s.ring[warp], s.full[warp]);
     for (; next_piece(w); advance(s.tiles, w, a.H)) {
         const int b = s.tiles.seq[w.k], t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, b, t0, TT);
         if (w.memories() == 0) {      // nothing to see: the readout is 0
@@ -560,11 +501,7 @@ __global__ void __launch_bounds__(32 * M::kWarps, 1) sma_paged_mma_kernel(const 
             run_piece<T, M, N, TT, 1, PARTS>(prm, s, w, run, t0, rows, feed, taken, wc, ok);
         }
     }
-    // Every copy has been waited for, unless a wait gave up: what is in flight then
-    // is waited for here, before its shared memory goes away.
-    if (!ok && lane == 0)
-        for (int i = max(0, feed.issued - M::kStages); i < feed.issued; ++i)
-            for (int k = 0; k < (1 << 20) && !mbar_try_wait(smem_u32(&s.full[warp][i % M::kStages]), (uint32_t)(i / M::kStages) & 1u); ++k) {}
+    if (!ok) feed.drain(s.full[warp]);      // else every copy has been waited for
 }
 
 template <typename T, typename M, int N, int TT, int PARTS>
