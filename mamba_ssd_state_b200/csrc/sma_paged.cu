@@ -75,7 +75,7 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M, N>& s, cons
             qc[n][kTT + t] = live ? ldf(static_cast<const T*>(a.Cm) + (tok * a.G + grp) * N + n) : 0.f;
         }
     }
-    const int bad = first_bad_memory(a.cache.table + (size_t)s.tiles.seq[w.k] * a.cache.width, a.cache, w.memories());
+    const int bad = readable_memories(a.cache.table + (size_t)s.tiles.seq[w.k] * a.cache.width, a.cache, w.first_memory(), w.last_memory());
     __syncwarp();
     float m[NT], l[NT];
     float2 o[NT];
@@ -227,7 +227,9 @@ __global__ void __launch_bounds__(ROWS * P / 4) sma_paged_combine_kernel(SmaPage
     __shared__ float4 so[SUB][COLS];
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool left = false;                        // a row that is not to be computed, as some piece says
     auto add = [&](float m2, float l2, const float4& o2) {
+        left |= l2 < 0.f;
         if (l2 == 0.f) return;                // saw nothing
         const float mn = fmaxf(m, m2);
         const float f = l == 0.f ? 0.f : exp2f(m - mn), k = exp2f(m2 - mn);
@@ -236,16 +238,14 @@ __global__ void __launch_bounds__(ROWS * P / 4) sma_paged_combine_kernel(SmaPage
                      : make_float4(o.x * f + o2.x * k, o.y * f + o2.y * k, o.z * f + o2.z * k, o.w * f + o2.w * k);
         m = mn;
     };
-    bool left = false;
     const size_t at = ((size_t)(hd.t0 + r0 + t) * a.H + hd.h) * P + p;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
     if (t < rows) {
         const size_t off = (size_t)(r0 + t) * (P + 4);
         const float* own = piece_rows<TT, P>(a.part, blockIdx.x, 1) + off;
         if (grp == 0 && a.y_ssd) y = *reinterpret_cast<const float4*>(a.y_ssd + at);
-        left = own[P + 1] < 0.f;              // a row that is not to be computed
-        if (grp == 0 && !left) add(own[P], own[P + 1], *reinterpret_cast<const float4*>(own + p));
-        for (int j = blockIdx.x + 1 + grp; j <= end && j < runs && !left; j += AHEAD * groups) {
+        if (grp == 0) add(own[P], own[P + 1], *reinterpret_cast<const float4*>(own + p));
+        for (int j = blockIdx.x + 1 + grp; j <= end && j < runs; j += AHEAD * groups) {
             float m2[AHEAD], l2[AHEAD];
             float4 o2[AHEAD];
 #pragma unroll
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(ROWS * P / 4) sma_paged_combine_kernel(SmaPage
         }
     }
     if (groups > 1) {
-        if (p == 0) { sm[sub] = m; sl[sub] = l; }
+        if (p == 0) { sm[sub] = m; sl[sub] = left ? -1.f : l; }
         so[sub][p / 4] = o;
         __syncthreads();
         if (grp == 0)

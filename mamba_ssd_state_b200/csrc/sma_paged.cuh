@@ -230,16 +230,20 @@ __device__ __forceinline__ float* piece_rows(float* part, int run, int which) {
     return part + 2 * kMaxRuns * (sizeof(PieceHeader) / sizeof(float)) + (size_t)(2 * run + which) * TT * (P + 4);
 }
 
-// First memory of sequence row `table` whose page is no page, among the first
-// `count`; `count` if there is none.  All lanes of a warp.
-__device__ __forceinline__ int first_bad_memory(const int* table, const PagedCache& c, int count) {
-    const int lane = threadIdx.x & 31, pages = (int)(((long long)count + c.R - 1) / c.R);
-    for (int k = 0; k < pages; k += 32) {
-        const int page = k + lane < pages ? table[k + lane] : 0;
-        const unsigned m = __ballot_sync(0xffffffffu, page < 0 || page >= c.npages);
-        if (m) return min(count, (k + __ffs(m) - 1) * c.R);
-    }
-    return count;
+// How many of a sequence's memories a row may see as far as the piece with
+// memories [first, last) can tell: up to the first of its pages that is no page,
+// all of the table if there is none.  A row that sees more is not computed; the
+// pieces of an item look at their own pages, the join at what each found.  All
+// lanes of a warp.
+__device__ __forceinline__ int readable_memories(const int* table, const PagedCache& c, int first, int last) {
+    const int lane = threadIdx.x & 31;
+    if (first < last)
+        for (int k = first / c.R, end = (last - 1) / c.R; k <= end; k += 32) {
+            const int page = k + lane <= end ? table[k + lane] : 0;
+            const unsigned m = __ballot_sync(0xffffffffu, page < 0 || page >= c.npages);
+            if (m) return (k + __ffs(m) - 1) * c.R;
+        }
+    return c.width * c.R;
 }
 
 // What a warp that works by itself copies: the memories of its run, piece by
@@ -266,7 +270,6 @@ struct Feed {
         // to the next part of the run that has memories to copy
         while ((more = next_piece(w))) {
             table = a.cache.table + (size_t)L.seq[w.k] * a.cache.width;
-            const int seen = w.memories();
             c = w.first_memory();
             last = w.last_memory();
             piece = 0;
@@ -276,8 +279,8 @@ struct Feed {
                 page = table[idx];
                 look_ahead(a.cache.R);
             }
-            const int bad = first_bad_memory(table, a.cache, seen);
-            if (bad < seen && (threadIdx.x & 31) == 0) flag_status(a.status, kStatusDevice);
+            const int bad = readable_memories(table, a.cache, c, last);
+            if (bad < last && (threadIdx.x & 31) == 0) flag_status(a.status, kStatusDevice);
             last = min(last, bad);
             if (c < last) return;
             advance(L, w, a.H);

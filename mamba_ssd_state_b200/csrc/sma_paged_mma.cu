@@ -341,7 +341,7 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const W
             vs[j] = 1.f / __shfl_sync(0xffffffffu, scale[NT - 1], 4 * ((NT == 2 ? 0 : 4) + tk + j));
         }
     }
-    const int bad = first_bad_memory(a.cache.table + (size_t)s.tiles.seq[w.k] * a.cache.width, a.cache, w.memories());
+    const int bad = readable_memories(a.cache.table + (size_t)s.tiles.seq[w.k] * a.cache.width, a.cache, w.first_memory(), w.last_memory());
     int fewest = INT_MAX; // memories that every row of the tile sees (rows that are not to be computed apart)
 #pragma unroll
     for (int j = 0; j < 2; ++j)

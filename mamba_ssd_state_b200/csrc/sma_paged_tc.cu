@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
                         }
                     }
             }
-            const int bad = first_bad_memory(table, a.cache, w.memories());
-            if (bad < w.memories() && lane == 0) flag_status(a.status, kStatusDevice);
+            const int bad = readable_memories(table, a.cache, w.first_memory(), w.last_memory());
+            if (bad < w.last_memory() && lane == 0) flag_status(a.status, kStatusDevice);
             const int first = w.first_memory(), last = min(w.last_memory(), bad);
             if (first >= last) continue;
             for (int c0 = first; c0 < last; c0 += kCB, ++it) {
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
         uint32_t ph = 0;
         int it = 0;
         for (; ok && next_piece(w); advance(s.tiles, w, a.H)) {
-            const int first = w.first_memory(), last = min(w.last_memory(), first_bad_memory(table_of(), a.cache, w.memories()));
+            const int first = w.first_memory(), last = min(w.last_memory(), readable_memories(table_of(), a.cache, w.first_memory(), w.last_memory()));
             if (first >= last) continue;
             if (!(ok = mbar_wait_warp(bar(Q_FULL), ph, wc, 4))) break;
             for (int c0 = first; c0 < last; c0 += kCB, ++it) {
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
 #pragma unroll
             for (int q = 0; q < kHalfP / 8; ++q)
                 er[q] = live ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.E) + at) + q) : make_uint4(0u, 0u, 0u, 0u);
-            const int bad = first_bad_memory(table_of(), a.cache, w.memories());
+            const int bad = readable_memories(table_of(), a.cache, w.first_memory(), w.last_memory());
             const int first = w.first_memory(), last = min(w.last_memory(), bad);
 #pragma unroll
             for (int q = 0; q < kHalfP / 8; ++q) {

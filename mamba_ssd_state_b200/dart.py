@@ -778,7 +778,7 @@ def dart_sma_paged(Q, E, Cm, cu_tokens, pages, table, mem_count, g: float, y_ssd
         n = workspace.numel() * workspace.element_size()
         wp = _need("workspace", workspace, workspace.shape, workspace.dtype, dev)
     _call(lib.dart_sma_paged, dev, dims, _dtype_code(dtype), Q.data_ptr(), E.data_ptr(), Cm.data_ptr(),
-          _need("cu_tokens", cu_tokens, (B + 1,), i32, dev), cache, _need("mem_count", mem_count, (T,), i32, dev), g, yp, op, wp, n)
+          _need("cu_tokens", cu_tokens, (B + 1,), i32, dev), cache, _need("mem_count", mem_count, (T,), i32, dev), float(g), yp, op, wp, n)
     return out
 
 

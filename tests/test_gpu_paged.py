@@ -464,6 +464,128 @@ def test_long_runs_over_many_memories_are_shared_by_blocks(N, P, dtype, cache, H
     assert rel_err(out, ref.sma(*args64, lens, memories, counts)) <= TOL
 
 
+@pytest.mark.parametrize("N, P, dtype, cache, H, G", SHAPES)
+@pytest.mark.parametrize("lens", [[4], [40], [150]])
+def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(N, P, dtype, cache, H, G, lens):
+    """The last two memories hold NaN (a block of them in 4-bit pages) and, where the format has it, an infinity; rows
+    that do not see them are as if they were not there, rows that do are NaN."""
+    rng = np.random.default_rng(N + lens[0])
+    memories = memories_of(rng, [12], H, N, P, cache, scale=0.5)
+    pool = Pool(memories, H, N, P, 5, cache, rng)
+    page, slot = pool.table_np[0, 10 // 5], 10 % 5
+    nan, inf = (pool.pages[page, :, slot + i] for i in range(2))
+    if cache == "mxfp4":
+        pool.scales[page, :, slot, 7, 1] = 255
+        pool.scales[page, :, slot + 1, 9, 0] = 255
+    else:
+        nan[:, N - 1, P - 1] = float("nan")
+        inf[:, 3, 2] = float("inf")
+    args, args64 = attention_inputs(rng, lens[0], H, G, N, P, dtype)
+    counts = [10 + (i % 4 == 1) + 2 * (i % 4 == 3) for i in range(lens[0])]
+    out = dart.dart_sma_paged(*args, cumulative(lens), pool.pages, pool.table, ints(*counts), 1.0, scales=pool.scales)
+    dart.dart_sync_status()
+    fine = np.array(counts) == 10
+    want = ref.sma(*args64, lens, memories, [10] * lens[0])
+    assert rel_err(out[fine], want[fine]) <= TOL
+    assert torch.isnan(out[~fine]).all()
+
+
+@pytest.mark.parametrize("N, P, dtype, cache, H, G", SHAPES)
+@pytest.mark.parametrize("lens", [[3], [33], [140]])
+def test_a_bad_page_in_a_shared_item(N, P, dtype, cache, H, G, lens):
+    """An item over many blocks whose 15th page of 20 is missing: rows that see it are left, whoever finds it."""
+    rng = np.random.default_rng(H + lens[0])
+    memories = memories_of(rng, [320], H, N, P, cache, scale=0.5)
+    pool = Pool(memories, H, N, P, 16, cache, rng)
+    args, args64 = attention_inputs(rng, lens[0], H, G, N, P, dtype)
+    counts = [(320, 224, 225)[i % 3] for i in range(lens[0])]
+    pool.table[0, 14] = pool.pages.shape[0]
+    out = torch.full((lens[0], H, P), 5.0, device="cuda")
+    dart.dart_sma_paged(*args, cumulative(lens), pool.pages, pool.table, ints(*counts), 1.0, scales=pool.scales, out=out)
+    with pytest.raises(dart.DartError):
+        dart.dart_sync_status()
+    done = np.array(counts) == 224
+    want = ref.sma(*args64, lens, memories, [224] * lens[0])
+    assert rel_err(out[done], want[done]) <= TOL and (out[~done] == 5.0).all()
+
+
+@pytest.mark.parametrize("N, P, dtype, cache, H, G", SHAPES)
+def test_many_sequences(N, P, dtype, cache, H, G):
+    """More sequences than a block has threads, some without tokens, some without memories, most with a few of both."""
+    rng = np.random.default_rng(21)
+    B = 900
+    lens = [int(v) for v in rng.integers(0, 3, B)]
+    mems = [int(v) for v in rng.integers(0, 3, B)]
+    one = memories_of(rng, [4], H, N, P, cache, scale=0.5)[0]
+    pool = Pool([one], H, N, P, 2, cache, rng)
+    pool.table = pool.table.expand(B, 2).contiguous()             # all read the same pages
+    T = sum(lens)
+    args, args64 = attention_inputs(rng, T, H, G, N, P, dtype)
+    counts = [mems[b] for b in range(B) for _ in range(lens[b])]
+    out = dart.dart_sma_paged(*args, cumulative(lens), pool.pages, pool.table, ints(*counts), 1.0, scales=pool.scales)
+    dart.dart_sync_status()
+    assert rel_err(out, ref.sma(*args64, lens, [one] * B, counts)) <= TOL
+
+
+def test_calls_without_tokens():
+    rng = np.random.default_rng(22)
+    H, N, P = 2, 64, 64
+    pool = Pool(memories_of(rng, [2, 1], H, N, P, "bf16"), H, N, P, 2, "bf16", rng)
+    args, _ = extend_inputs(rng, [0, 0], H, 1, N, P, "bf16")
+    s, c, s64, c64 = states(rng, 2, H, N, P)
+    s2, c2 = torch.zeros_like(s), torch.zeros_like(c)
+    got = dart.dart_ssd_extend(*args, ints(0, 0, 0), s, c, pool.pages, pool.table, ints(2, 1), ints(3, 0), 4, state_out=s2, dH_cur_out=c2)
+    att, _ = attention_inputs(rng, 0, H, 1, N, P, "bf16")
+    out = dart.dart_sma_paged(*att, ints(0, 0, 0), pool.pages, pool.table, got["mem_count"], 1.0)
+    dart.dart_sync_status()
+    assert out.shape == (0, H, P) and torch.equal(s2, s) and torch.equal(c2, c)
+    assert got["nchunks"].tolist() == [2, 1] and got["pos"].tolist() == [3, 0]
+
+
+def test_views_and_host_tensors_as_inputs():
+    """Token tensors that are slices of wider ones, or on the host, are taken as what they hold."""
+    rng = np.random.default_rng(23)
+    H, N, P, lens, mems = 2, 128, 64, [3, 20], [4, 9]
+    memories = memories_of(rng, mems, H, N, P, "bf16", scale=0.5)
+    pool = Pool(memories, H, N, P, 4, "bf16", rng)
+    (Q, E, C), args64 = attention_inputs(rng, 23, H, 1, N, P, "bf16")
+    counts = [mems[0]] * 3 + [mems[1]] * 20
+    wide = torch.zeros((23, H, 2 * N), dtype=torch.bfloat16, device="cuda")
+    wide[..., N:] = Q
+    plain = dart.dart_sma_paged(Q, E, C, cumulative(lens), pool.pages, pool.table, ints(*counts), 1.0)
+    view = dart.dart_sma_paged(wide[..., N:], E.transpose(0, 1).contiguous().transpose(0, 1), C[:, 0], cumulative(lens), pool.pages,
+                               pool.table, ints(*counts), 1.0)
+    host = dart.dart_sma_paged(Q.cpu(), E.cpu(), C.cpu(), cumulative(lens), pool.pages, pool.table, ints(*counts), 1.0)
+    dart.dart_sync_status()
+    assert torch.equal(view, plain) and torch.equal(host, plain)
+
+
+def test_two_calls_at_once():
+    """Two streams, each with its own inputs and workspace, many times over: the same bits as one after the other."""
+    rng = np.random.default_rng(24)
+    H, N, P = 4, 128, 64
+    work = []
+    for lens, mems, cache in (([1] * 20, [40] * 20, "bf16"), ([3] * 15, [60] * 15, "mxfp4"), ([100, 60], [30, 50], "bf16")):
+        memories = memories_of(rng, [max(mems)], H, N, P, cache, scale=0.5)
+        pool = Pool(memories, H, N, P, 8, cache, rng)
+        pool.table = pool.table.expand(len(lens), pool.table.shape[1]).contiguous()
+        args, _ = attention_inputs(rng, sum(lens), H, 1, N, P, "bf16")
+        counts = ints(*[m for k, m in zip(lens, mems) for _ in range(k)])
+        cu = cumulative(lens)
+        work.append(lambda a=args, cu=cu, p=pool, c=counts: dart.dart_sma_paged(*a, cu, p.pages, p.table, c, 1.0, scales=p.scales))
+    want = [f() for f in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    for _ in range(20):
+        got = []
+        for f, st in zip(work, streams):
+            with torch.cuda.stream(st):
+                got.append(f())
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+    dart.dart_sync_status()
+
+
 def test_a_shared_page_is_read_by_two_sequences():
     rng = np.random.default_rng(9)
     H, N, P, R = 2, 128, 64, 4
