@@ -470,8 +470,11 @@ cudaError_t run(const SmaPagedArgs& a, cudaStream_t st) {
 }  // namespace
 
 bool sma_paged_tc_applicable(const SmaPagedArgs& a, dart_dtype dt) {
-    // a tile of 128 rows costs about as much as two of 8 rows do on warp-level products
-    return dt == DART_BF16 && !a.cache.mxfp4 && a.P == kP && (a.N == 128 || a.N == 64) && a.T >= 16 * (long long)a.B &&
+    // More than 8 rows a sequence are two tiles of the warp-level kernel, which then streams the memories
+    // twice.  32 sequences over up to 100 memories of 32 heads, warp-level / here: 6 rows on average
+    // 218 / 280 us, 9 rows 341 / 285, 12 rows 399 / 309, 48 rows 1267 / 337; 4 sequences: 42 / 53, 44 / 53,
+    // 50 / 53 and 124 / 57 us.
+    return dt == DART_BF16 && !a.cache.mxfp4 && a.P == kP && (a.N == 128 || a.N == 64) && a.T > 8 * (long long)a.B &&
            a.B + a.T / kRows <= kCap;
 }
 
