@@ -414,7 +414,7 @@ dart_status dart_decode_step_noalloc(const dart_dims* dims, dart_dtype dtype,
  * concern is left as it is and the others are computed.
  *
  * Compiled for (N, P) = (128, 64), (64, 64) and, in DART_CACHE_DTYPE, (16, 16);
- * any chunk S >= 1.  At most 2^18 memories per sequence.
+ * any chunk S >= 1.  At most 2^16 memories per sequence.
  */
 typedef enum { DART_CACHE_DTYPE = 0, DART_CACHE_MXFP4 = 1 } dart_cache_format;
 

@@ -54,8 +54,9 @@ struct SmaPagedArgs {
     int* status;
 };
 
-// Largest number of memories a sequence's table may name: 2^26 tokens of context at S = 256.
-constexpr long long kPagedMaxMemories = 1 << 18;
+// Largest number of memories a sequence's table may name: 2^24 tokens of context at S = 256
+// (and the units of 4096 tiles, at 5 a memory, stay within 31 bits).
+constexpr long long kPagedMaxMemories = 1 << 16;
 
 bool paged_supported(int N, int P, int mxfp4);
 cudaError_t launch_cache_write(const CacheCopyArgs& a, dart_dtype dt, cudaStream_t st);

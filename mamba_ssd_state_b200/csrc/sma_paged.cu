@@ -28,6 +28,7 @@ constexpr int kTT = 8;        // tokens of a tile
 constexpr int kCap = 4096;    // tiles of a call
 constexpr int kLeast = 1;     // units below which a run is not cut
 
+using Tiles = TileList<kCap>;
 struct Params { SmaPagedArgs a; };
 
 template <typename T, int N, int P>
@@ -45,13 +46,13 @@ struct Smem {
     alignas(16) float qc[kWarps][N][2 * kTT];      // Q (times log2(e) / sqrt(N)) and C of a tile's tokens
     uint64_t full[kWarps][M::kStages];
     int abort_flag;
-    TileList<kCap> tiles;
+    Tiles tiles;
 };
 
 // A piece of a run for the first NT tokens of the tile.
 template <typename T, int N, int P, int NT, typename M>
 __device__ __forceinline__ void run_piece(const Params& prm, Smem<M, N>& s, const Walk& w, int run, int t0, int rows,
-                                          Feed<M, kCap>& feed, int& taken, const WaitCtx& wc, bool& ok) {
+                                          Feed<M, Tiles>& feed, int& taken, const WaitCtx& wc, bool& ok) {
     constexpr int LPR = P / 2, RPW = 32 / LPR;      // lanes of a row, rows of the warp at a time
     const SmaPagedArgs& a = prm.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = group_of(w.h, a.H, a.G);
@@ -75,7 +76,7 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M, N>& s, cons
             qc[n][kTT + t] = live ? ldf(static_cast<const T*>(a.Cm) + (tok * a.G + grp) * N + n) : 0.f;
         }
     }
-    const int bad = readable_memories(a.cache.table + (size_t)s.tiles.seq[w.k] * a.cache.width, a.cache, w.first_memory(), w.last_memory());
+    const int bad = readable_memories(a.cache.table + (size_t)s.tiles.seq(w.k) * a.cache.width, a.cache, w.first_memory(), w.last_memory());
     __syncwarp();
     float m[NT], l[NT];
     float2 o[NT];
@@ -184,17 +185,17 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_kernel(const __grid_con
     griddep_wait();
     if (lane < 2) piece_header(a.part, run, lane)->state = 0;
     __syncwarp();
-    build_tiles<kTT, kCap>(a, s.tiles);
+    build_tiles<kTT>(a, s.tiles);
     if (s.tiles.n == 0) return;
     const WaitCtx wc{&s.abort_flag, a.status, 12};
     bool ok = true;
     int taken = 0;
     Walk w = start_walk(s.tiles, a.H, run, runs, kLeast);
-    Feed<M, kCap> feed;
+    Feed<M, Tiles> feed;
     feed.begin(a, s.tiles, w);
     for (int i = 0; i < M::kStages; ++i) feed.fill(prm, s.tiles, s.ring[warp], s.full[warp]);
     for (; next_piece(w); advance(s.tiles, w, a.H)) {
-        const int t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, s.tiles.seq[w.k], t0, kTT);
+        const int t0 = s.tiles.t0[w.k], rows = s.tiles.rows(w.k);
         if (rows == 1) run_piece<T, N, P, 1>(prm, s, w, run, t0, rows, feed, taken, wc, ok);
         else if (rows <= 4) run_piece<T, N, P, 4>(prm, s, w, run, t0, rows, feed, taken, wc, ok);
         else run_piece<T, N, P, 8>(prm, s, w, run, t0, rows, feed, taken, wc, ok);

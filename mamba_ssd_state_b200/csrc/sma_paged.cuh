@@ -46,19 +46,24 @@ cudaError_t launch_sma_paged_tc(const SmaPagedArgs& a, cudaStream_t st);
 
 #ifdef __CUDACC__
 
-// Tiles of the batch in shared memory: tile k covers rows t0[k] .. of sequence
-// seq[k] and has pre[k+1] - pre[k] units a head, kItemUnits + the memories it reads.
-template <int CAP>
+// What a memory costs a worker, in units: the same for all tiles, unless a kernel
+// says otherwise.
+struct EvenCost { static __device__ __forceinline__ int of(int) { return 1; } };
+
+// Tiles of the batch in shared memory: tile k covers rows(k) rows of sequence
+// seq(k) from row t0[k] on and has pre[k+1] - pre[k] units a head, the cost of a
+// memory times (kItemUnits + the memories it reads).
+template <int CAP, typename COST = EvenCost>
 struct TileList {
     int pre[CAP + 1];
-    int seq[CAP];
+    unsigned tile[CAP];      // sequence, and rows << 16
     int t0[CAP];
     int scan[32];
     int n;
+    static_assert(CAP <= 65536, "sequences in 16 bits");
+    __device__ __forceinline__ int seq(int k) const { return (int)(tile[k] & 0xffffu); }
+    __device__ __forceinline__ int rows(int k) const { return (int)(tile[k] >> 16); }
 };
-
-// Rows of tile k.
-__device__ __forceinline__ int tile_rows(const int* cu, int seq, int t0, int TT) { return min(TT, cu[seq + 1] - t0); }
 
 // The count a row may really see: 0 for rows that are not to be computed.
 __device__ __forceinline__ int usable_count(int c, long long limit) { return c < 0 || c > limit ? 0 : c; }
@@ -87,8 +92,8 @@ __device__ __forceinline__ int block_scan(int v, int* scan, int& total) {
 // Builds the list; all threads of the block.  Ranges that are no ranges, counts
 // beyond the table and lists longer than CAP (only overlapping ranges make one)
 // are flagged, and what they name is left out.
-template <int TT, int CAP>
-__device__ __forceinline__ void build_tiles(const SmaPagedArgs& a, TileList<CAP>& L) {
+template <int TT, int CAP, typename COST>
+__device__ __forceinline__ void build_tiles(const SmaPagedArgs& a, TileList<CAP, COST>& L) {
     const int threads = blockDim.x, tid = threadIdx.x;
     const long long limit = (long long)a.cache.width * a.cache.R;
     bool bad = false;
@@ -104,7 +109,7 @@ __device__ __forceinline__ void build_tiles(const SmaPagedArgs& a, TileList<CAP>
         const int at = n + block_scan(tiles, L.scan, total);
         for (int j = 0; j < tiles; ++j) {
             if (at + j >= CAP) { bad = true; break; }
-            L.seq[at + j] = b;
+            L.tile[at + j] = (unsigned)b | (unsigned)min(TT, t1 - t0 - j * TT) << 16;
             L.t0[at + j] = t0 + j * TT;
         }
         n = min(CAP, n + total);
@@ -113,7 +118,7 @@ __device__ __forceinline__ void build_tiles(const SmaPagedArgs& a, TileList<CAP>
     // the units of every tile: a thread reads the counts of a small one, a warp those of a large one
     constexpr int BY = TT < 32 ? 1 : 32;
     for (int k = tid / BY; k < n; k += threads / BY) {
-        const int t0 = L.t0[k], rows = tile_rows(a.cu, L.seq[k], t0, TT);
+        const int t0 = L.t0[k], rows = L.rows(k);
         int most = 0;
 #pragma unroll 8
         for (int r = tid % BY; r < rows; r += BY) {
@@ -122,7 +127,7 @@ __device__ __forceinline__ void build_tiles(const SmaPagedArgs& a, TileList<CAP>
             most = max(most, usable_count(c, limit));
         }
         if (BY == 32) most = __reduce_max_sync(0xffffffffu, most);
-        if (tid % BY == 0) L.pre[k] = most + kItemUnits;
+        if (tid % BY == 0) L.pre[k] = (most + kItemUnits) * COST::of(rows);
     }
     __syncthreads();
     int sum = 0;
@@ -142,17 +147,17 @@ __device__ __forceinline__ void build_tiles(const SmaPagedArgs& a, TileList<CAP>
 struct Walk {
     long long u, end;    // next unit, end of the run
     int k, h, c;         // tile, head, unit of the item at u
-    int units;           // units of the item
-    int last;            // the piece: units [c, last) of the item
-    __device__ __forceinline__ int memories() const { return units - kItemUnits; }   // of the item
-    __device__ __forceinline__ int first_memory() const { return max(c - kItemUnits, 0); }
-    __device__ __forceinline__ int last_memory() const { return last - kItemUnits; }
+    int units, cost;     // units of the item, and of a memory
+    int last;            // the piece: units [c, last) of the item, and the memories that begin there
+    __device__ __forceinline__ int memories() const { return units / cost - kItemUnits; }   // of the item
+    __device__ __forceinline__ int first_memory() const { return max((c + cost - 1) / cost - kItemUnits, 0); }
+    __device__ __forceinline__ int last_memory() const { return (last + cost - 1) / cost - kItemUnits; }
     __device__ __forceinline__ bool whole() const { return last - c == units; }
 };
 
 // The tile of unit u.
-template <int CAP>
-__device__ __forceinline__ int tile_of(const TileList<CAP>& L, int H, long long u) {
+template <typename List>
+__device__ __forceinline__ int tile_of(const List& L, int H, long long u) {
     int lo = 0, hi = L.n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
@@ -170,22 +175,23 @@ __device__ __forceinline__ long long quick_div(long long a, long long b) {
 
 // Run i of `runs`; runs of fewer than `least` units are not cut smaller, and a
 // cut that would leave a run with an item but none of its memories goes before it.
-template <int CAP>
-__device__ __forceinline__ Walk start_walk(const TileList<CAP>& L, int H, int i, int runs, int least) {
+template <int CAP, typename COST>
+__device__ __forceinline__ Walk start_walk(const TileList<CAP, COST>& L, int H, int i, int runs, int least) {
     const long long W = (long long)L.pre[L.n] * H;
     const long long G = W < (long long)runs * least ? quick_div(W + least - 1, least) : runs;
     Walk w;
     auto cut = [&](long long u) {      // leaves w at the cut
         w.u = u;
         w.h = w.c = 0;
-        w.units = 1;
+        w.units = w.cost = 1;
         if (u >= W) return;
         w.k = tile_of(L, H, u);
         w.units = L.pre[w.k + 1] - L.pre[w.k];
+        w.cost = COST::of(L.rows(w.k));
         const long long r = u - (long long)L.pre[w.k] * H;
         w.h = (int)quick_div(r, w.units);
         w.c = (int)(r - (long long)w.h * w.units);
-        if (w.c <= kItemUnits) {           // no memory before the cut
+        if (w.c <= kItemUnits * w.cost) {  // no memory before the cut
             w.u -= w.c;
             w.c = 0;
         }
@@ -208,14 +214,17 @@ __device__ __forceinline__ bool next_piece(Walk& w) {
     w.last = (int)min((long long)w.units, w.c + (w.end - w.u));
     return true;
 }
-template <int CAP>
-__device__ __forceinline__ void advance(const TileList<CAP>& L, Walk& w, int H) {
+template <int CAP, typename COST>
+__device__ __forceinline__ void advance(const TileList<CAP, COST>& L, Walk& w, int H) {
     w.u += w.last - w.c;
     w.c = 0;
     if (++w.h == H) {
         w.h = 0;
         ++w.k;
-        if (w.k < L.n) w.units = L.pre[w.k + 1] - L.pre[w.k];
+        if (w.k < L.n) {
+            w.units = L.pre[w.k + 1] - L.pre[w.k];
+            w.cost = COST::of(L.rows(w.k));
+        }
     }
 }
 
@@ -250,7 +259,7 @@ __device__ __forceinline__ int readable_memories(const int* table, const PagedCa
 // piece, into the stages of its ring, ahead of what it multiplies and over the
 // ends of items.  M says how a memory is kept: kStages, kStageBytes, kPieces
 // pieces of a memory, and copy(params, memory, piece, shared address, barrier).
-template <typename M, int CAP>
+template <typename M, typename List>
 struct Feed {
     Walk w;
     const int* table;        // the sequence's
@@ -260,16 +269,16 @@ struct Feed {
     int issued;              // stages filled
     bool more;
 
-    __device__ __forceinline__ void begin(const SmaPagedArgs& a, const TileList<CAP>& L, const Walk& walk) {
+    __device__ __forceinline__ void begin(const SmaPagedArgs& a, const List& L, const Walk& walk) {
         w = walk;
         issued = 0;
         start(a, L);
     }
     __device__ __forceinline__ void look_ahead(int R) { ahead = (idx + 1) * R < last ? table[idx + 1] : 0; }
-    __device__ __forceinline__ void start(const SmaPagedArgs& a, const TileList<CAP>& L) {
+    __device__ __forceinline__ void start(const SmaPagedArgs& a, const List& L) {
         // to the next part of the run that has memories to copy
         while ((more = next_piece(w))) {
-            table = a.cache.table + (size_t)L.seq[w.k] * a.cache.width;
+            table = a.cache.table + (size_t)L.seq(w.k) * a.cache.width;
             c = w.first_memory();
             last = w.last_memory();
             piece = 0;
@@ -287,7 +296,7 @@ struct Feed {
         }
     }
     template <typename Params, typename Stage>
-    __device__ __forceinline__ void fill(const Params& prm, const TileList<CAP>& L, Stage* ring, uint64_t* full) {
+    __device__ __forceinline__ void fill(const Params& prm, const List& L, Stage* ring, uint64_t* full) {
         if (!more) return;
         const SmaPagedArgs& a = prm.a;
         const int st = issued % M::kStages;

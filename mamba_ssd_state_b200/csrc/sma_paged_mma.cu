@@ -43,7 +43,12 @@ using namespace sm100;
 
 constexpr int kP = 64;
 constexpr int kCap = 4096;                      // tiles of a call
-constexpr int kLeast = 1;                       // units below which a run is not cut
+constexpr int kLeast = 4;                       // units below which a run is not cut
+
+// A memory takes 2.1 us of a warp with two tiles of columns and 1.65 with one
+// (4-bit; counted the same, the runs with more rows ended a fifth later).
+struct RowCost { static __device__ __forceinline__ int of(int rows) { return rows > 4 ? 5 : 4; } };
+using Tiles = TileList<kCap, RowCost>;
 
 struct Params {
     CUtensorMap map;      // bfloat16 memories: (P, rows of N), boxes of one memory
@@ -76,7 +81,7 @@ struct Smem {
     uint8_t ring[M::kWarps][M::kStages][M::kStageBytes];    // first: tiles are 1024-byte aligned
     uint64_t full[M::kWarps][M::kStages];
     int abort_flag;
-    TileList<kCap> tiles;
+    Tiles tiles;
 };
 
 template <int I> struct Piece { static constexpr int value = I; };
@@ -301,7 +306,7 @@ __device__ __forceinline__ bool multiply(const uint8_t* stage, const Column<M, N
 // 4 tokens; NT = 2: a tile each of up to 8.
 template <typename T, typename M, int N, int TT, int NT, int PARTS>
 __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const Walk& w, int run, int t0, int rows,
-                                          Feed<M, kCap>& feed, int& taken, const WaitCtx& wc, bool& ok) {
+                                          Feed<M, Tiles>& feed, int& taken, const WaitCtx& wc, bool& ok) {
     const SmaPagedArgs& a = prm.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
     const int grp = group_of(w.h, a.H, a.G);
@@ -341,7 +346,7 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const W
             vs[j] = 1.f / __shfl_sync(0xffffffffu, scale[NT - 1], 4 * ((NT == 2 ? 0 : 4) + tk + j));
         }
     }
-    const int bad = readable_memories(a.cache.table + (size_t)s.tiles.seq[w.k] * a.cache.width, a.cache, w.first_memory(), w.last_memory());
+    const int bad = readable_memories(a.cache.table + (size_t)s.tiles.seq(w.k) * a.cache.width, a.cache, w.first_memory(), w.last_memory());
     int fewest = INT_MAX; // memories that every row of the tile sees (rows that are not to be computed apart)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -476,17 +481,17 @@ __global__ void __launch_bounds__(32 * M::kWarps, 1) sma_paged_mma_kernel(const 
     griddep_wait();
     if (lane < 2) piece_header(a.part, run, lane)->state = 0;
     __syncwarp();
-    build_tiles<TT, kCap>(a, s.tiles);
+    build_tiles<TT>(a, s.tiles);
     if (s.tiles.n == 0) return;
     const WaitCtx wc{&s.abort_flag, a.status, 10};
     bool ok = true;
     int taken = 0;
     Walk w = start_walk(s.tiles, a.H, run, runs, kLeast);
-    Feed<M, kCap> feed;
+    Feed<M, Tiles> feed;
     feed.begin(a, s.tiles, w);
     for (int i = 0; i < M::kStages; ++i) feed.fill(prm, s.tiles, s.ring[warp], s.full[warp]);
     for (; next_piece(w); advance(s.tiles, w, a.H)) {
-        const int b = s.tiles.seq[w.k], t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, b, t0, TT);
+        const int t0 = s.tiles.t0[w.k], rows = s.tiles.rows(w.k);
         if (w.memories() == 0) {      // nothing to see: the readout is 0
             for (int i = lane; i < rows * kP; i += 32) {
                 const int c = a.mem_count[t0 + i / kP];

@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
     }
     griddep_wait();
     if (tid < 2 && rank == 0) piece_header(a.part, run, tid)->state = 0;
-    build_tiles<TT, kCap>(a, s.tiles);
+    build_tiles<TT>(a, s.tiles);
     tc_fence_before();
     if (kPair) cluster_sync();                   // both CTAs' barriers exist before any remote arrive or copy
     else __syncthreads();
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
     Walk w;
     w.u = w.end = 0;
     if (s.tiles.n > 0) w = start_walk(s.tiles, a.H, run, runs, kLeast);
-    auto table_of = [&]() { return a.cache.table + (size_t)s.tiles.seq[w.k] * a.cache.width; };
+    auto table_of = [&]() { return a.cache.table + (size_t)s.tiles.seq(w.k) * a.cache.width; };
     if (warp == 0) {
         // ------------------------------------------------------------ TMA
         uint32_t ph = 0;          // of Q_FREE and C_FREE
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
         for (; ok && next_piece(w); advance(s.tiles, w, a.H)) {
             const int* table = table_of();
             {   // the rows that the epilogue starts and ends with, while it is still at the last piece
-                const int t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, s.tiles.seq[w.k], t0, TT);
+                const int t0 = s.tiles.t0[w.k], rows = s.tiles.rows(w.k);
 #pragma unroll
                 for (int r = rank * kRows + lane; r < (rank + 1) * kRows; r += 32)
                     if (r < rows) {
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
         const float sscale = kLog2e * rsqrtf((float)N);
         int it = 0;
         for (; next_piece(w); advance(s.tiles, w, a.H)) {
-            const int t0 = s.tiles.t0[w.k], rows = tile_rows(a.cu, s.tiles.seq[w.k], t0, TT);
+            const int t0 = s.tiles.t0[w.k], rows = s.tiles.rows(w.k);
             const int tr = rank * kRows + row;         // row of the tile
             const bool live = tr < rows;
             const int count = live ? a.mem_count[t0 + tr] : -1;
