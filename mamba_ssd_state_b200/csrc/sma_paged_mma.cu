@@ -15,7 +15,7 @@
 // as it has read it, running ahead of itself over the ends of items, and never
 // waits for another warp.  (With one copying warp and eight that shared the
 // pieces of a block, the joins and loads at the ends of items were what bound
-// short ones: 616 us where this takes 495 for 64 sequences of one token and 128 memories.)
+// short ones: 616 us where this takes 465 for 64 sequences of one token and 128 memories.)
 //
 // M^T is the A operand: bfloat16 through ldmatrix.trans; codes become float16
 // in registers (E2M1 values are exact there), laid out in memory so that a lane

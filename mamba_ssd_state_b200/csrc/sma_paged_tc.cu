@@ -7,7 +7,7 @@
 // with the accumulators in TMEM (U in columns 0..255, V in 256..511).  Reading a
 // memory once for 128 tokens instead of 8 makes the run compute-bound:
 // 4 x 256 tokens over 100 memories took 470 us on warp-level products, where
-// every 8 tokens stream all memories through the SM again, and take 92 here.
+// every 8 tokens stream all memories through the SM again, and take about 100 here.
 //
 // What differs from prefill: memories come from pages, a tile ends with its
 // sequence (rows behind it belong to others and are not written), every row has
@@ -131,23 +131,24 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
     auto table_of = [&]() { return a.cache.table + (size_t)s.tiles.seq(w.k) * a.cache.width; };
     if (warp == 0) {
         // ------------------------------------------------------------ TMA
+        // the rows that the epilogue starts and ends with, while it is still at the last piece
+        auto prefetch_rows = [&]() {
+            const int t0 = s.tiles.t0[w.k], rows = s.tiles.rows(w.k);
+#pragma unroll
+            for (int r = rank * kRows + lane; r < (rank + 1) * kRows; r += 32)
+                if (r < rows) {
+                    const size_t at = ((size_t)(t0 + r) * a.H + w.h) * kP;
+                    prefetch_l2(static_cast<const __nv_bfloat16*>(a.E) + at);
+                    if (a.y_ssd && w.whole()) {
+                        prefetch_l2(a.y_ssd + at);
+                        prefetch_l2(a.y_ssd + at + kP / 2);
+                    }
+                }
+        };
         uint32_t ph = 0;          // of Q_FREE and C_FREE
         int it = 0, q_filled = 0;
         for (; ok && next_piece(w); advance(s.tiles, w, a.H)) {
             const int* table = table_of();
-            {   // the rows that the epilogue starts and ends with, while it is still at the last piece
-                const int t0 = s.tiles.t0[w.k], rows = s.tiles.rows(w.k);
-#pragma unroll
-                for (int r = rank * kRows + lane; r < (rank + 1) * kRows; r += 32)
-                    if (r < rows) {
-                        const size_t at = ((size_t)(t0 + r) * a.H + w.h) * kP;
-                        prefetch_l2(static_cast<const __nv_bfloat16*>(a.E) + at);
-                        if (a.y_ssd && w.whole()) {
-                            prefetch_l2(a.y_ssd + at);
-                            prefetch_l2(a.y_ssd + at + kP / 2);
-                        }
-                    }
-            }
             const int bad = readable_memories(table, a.cache, w.first_memory(), w.last_memory());
             if (bad < w.last_memory() && lane == 0) flag_status(a.status, kStatusDevice);
             const int first = w.first_memory(), last = min(w.last_memory(), bad);
@@ -183,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
                     if (!(ok = mbar_wait_warp(bar(C_FREE), ph ^ 1u, wc, 2))) break;
                     if (lane == 0) rows(s.c, &prm.map_c, C_FULL, grp);
                     ph ^= 1u;
+                    prefetch_rows();
                 }
             }
         }
