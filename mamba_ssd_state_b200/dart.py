@@ -615,7 +615,7 @@ def _input(t, dtype, index):
 
 def _call(fn, index, *args):
     """fn on CUDA device `index` and its current stream (the last argument)."""
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
