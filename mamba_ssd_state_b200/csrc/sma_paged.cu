@@ -208,9 +208,12 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_kernel(const __grid_con
 // and where there are fewer rows than threads for them, every n-th of the item's
 // pieces: an item of one row may be spread over all runs, and many read it then.
 template <int TT, int P, int ROWS>
-__global__ void __launch_bounds__(ROWS * P / 4) sma_paged_combine_kernel(SmaPagedArgs a, int runs) {
+__global__ void __launch_bounds__(ROWS * P / 4, TT >= 128 ? 4 : 1) sma_paged_combine_kernel(SmaPagedArgs a, int runs) {
     constexpr int COLS = P / 4, SUB = ROWS;                  // threads of a row, of a column
-    constexpr int AHEAD = 8;                                 // pieces read at a time
+    // Pieces read at a time (8 where an item may have dozens: 29 us for the float32 case, 32 with 4).  An item of a
+    // large tile has few, and all blocks of its rows fit the machine at once with 32
+    // registers a thread (one block an SM and four rounds of them took 12 us behind the prompt pieces)
+    constexpr int AHEAD = TT >= 128 ? 1 : 8;
     sm100::griddep_wait();
     const PieceHeader hd = *piece_header(a.part, blockIdx.x, 1);
     const int r0 = ROWS * blockIdx.y, rows = min(ROWS, hd.rows - r0);
