@@ -9,14 +9,15 @@
 // Both matrices are N x P and their columns are independent, so a block owns a
 // slice of the columns of one (sequence, head) and keeps them in registers from
 // the first token to the last: one read and one write of H and D, the floor of
-// short runs (64 sequences of one token, 32 heads: 269 MB in 47 us, 88% of measured
-// HBM with four blocks of 256 threads an SM and streaming accesses; 53 with
-// three, 50 without the hints).  The loads
-// of the state go out before the run is looked at.  A thread owns four columns
-// and RPT rows; partial sums of y meet over a warp's rows by shuffles and over
-// the warps in shared memory, once for every kTile tokens.  Long runs of
-// bfloat16 tokens are bound by the 4 N P operations a token instead and go to
-// ssd_extend_mma.cu.
+// short runs (64 sequences of one token, 32 heads: 269 MB in 44 us, 93% of measured
+// HBM).  The loads of the state go out before the run is looked at, with
+// streaming hints (3 us less).  A thread owns four columns and RPT rows: 8 rows
+// give it sixteen wide loads in flight, and 128 registers for them (512 threads
+// an SM) measured 44 us where 4 rows of twice the threads took 47, five blocks an
+// SM 46 and six 52, and slices of 16 columns 50.  Partial sums of y meet over a
+// warp's rows by shuffles and over the warps in shared memory, once for every
+// kTile tokens.  Long runs of bfloat16 tokens are bound by the 4 N P operations a
+// token instead and go to ssd_extend_mma.cu.
 #include "dart_paged.cuh"
 #include "sm100.cuh"
 
@@ -26,7 +27,7 @@ namespace {
 constexpr int kTile = 8;   // tokens staged in shared memory at a time
 
 template <typename T, int N, int P, int PS, int RPT>
-__global__ void __launch_bounds__(PS / 4 * N / RPT, 4 * 256 / (PS / 4 * N / RPT)) ssd_extend_kernel(ExtendArgs a) {
+__global__ void __launch_bounds__(PS / 4 * N / RPT, 512 / (PS / 4 * N / RPT)) ssd_extend_kernel(ExtendArgs a) {
     constexpr int CT = PS / 4, kThreads = CT * (N / RPT);   // threads across the columns, of the block
     constexpr int WARPS = kThreads / 32;
     static_assert(kThreads % 32 == 0 && 32 % CT == 0, "whole warps of whole rows");
@@ -127,8 +128,8 @@ cudaError_t run(const ExtendArgs& a, dart_dtype dt, cudaStream_t st) {
 
 cudaError_t launch_ssd_extend(const ExtendArgs& a, dart_dtype dt, cudaStream_t st) {
     if (ssd_extend_mma_applicable(a, dt)) return launch_ssd_extend_mma(a, st);
-    if (a.N == 128 && a.P == 64) return run<128, 64, 32, 4>(a, dt, st);
-    if (a.N == 64 && a.P == 64) return run<64, 64, 32, 4>(a, dt, st);
+    if (a.N == 128 && a.P == 64) return run<128, 64, 32, 8>(a, dt, st);
+    if (a.N == 64 && a.P == 64) return run<64, 64, 32, 8>(a, dt, st);
     if (a.N == 16 && a.P == 16) return run<16, 16, 16, 2>(a, dt, st);
     return cudaErrorInvalidValue;
 }

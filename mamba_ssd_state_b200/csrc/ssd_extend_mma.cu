@@ -357,10 +357,11 @@ cudaError_t run(const ExtendArgs& a, cudaStream_t st) {
 }  // namespace
 
 bool ssd_extend_mma_applicable(const ExtendArgs& a, dart_dtype dt) {
-    // A block costs the same with few tokens as with 64, and ends with its chunk.  32 sequences of 32 heads,
-    // token by token / here: 18 tokens on average 68 / 81 us, 24 tokens 84 / 88, 48 tokens 151 / 107; 4
-    // sequences: 15 / 15, 19 / 16 and 33 / 17 us.  Four pieces of up to 256 tokens: 151 / 187 us with chunks
-    // of 8, 138 / 103 of 16, 117 / 39 of 64.
+    // A block costs the same with few tokens as with 64, and ends with its chunk.  64 sequences of 32 heads,
+    // token by token / here: 12 tokens on average 90 / 136 us, 24 tokens 145 / 156, 35 tokens 198 / 178, 48
+    // tokens 258 / 190; 4 sequences: 14 tokens 11 / 15 us, 27 tokens 18 / 16, 58 tokens 32 / 17.  Four pieces
+    // of up to 256 tokens, token by token / here, before the former's last step (3% of it): 151 / 187 us with
+    // chunks of 8, 138 / 103 of 16, 117 / 39 of 64.
     return dt == DART_BF16 && a.P == kP && (a.N == 128 || a.N == 64) && a.S >= 16 && a.T >= 24 * (long long)a.B;
 }
 
