@@ -6,12 +6,17 @@
 //   o = sum_c softmax_c(s) v_c,  out = y_ssd + g o        (o = 0 with none visible).
 //
 // Every warp is a worker of its own, with its run of units and its ring of stages
-// (16 rows of a memory each, copied ahead over the ends of items): a lane has two
-// columns of a row, and a value is used for U and V of up to 8 tokens, whose Q
-// and C stand in the warp's own shared memory.  Scores are summed over the warp,
+// (16 rows of a memory each, copied ahead over the ends of items): a lane has four
+// columns of every second row, and a value is used for U and V of up to 8 tokens,
+// whose Q and C stand in the warp's own shared memory.  What bounds runs of
+// several tokens is the issue of multiply-adds and of the shared loads that feed
+// them; two tokens of a column share one paired multiply-add, and four columns a lane
+// halve the loads of Q and C (32 runs of up to 6 tokens over 131 memories, 32
+// heads: 888 us with two columns and single multiply-adds, 664 so, 485 at HBM's
+// rate; 64 single tokens 909 and 888 us, HBM).  Scores are summed over the warp,
 // the softmax runs online in base 2, and v is folded into the lane's columns.
 // (With eight warps to a piece and loads straight from global memory, 7 runs of
-// 5 float32 tokens over 45 memories of 8 heads took 32 us; this takes 30.)
+// 5 float32 tokens over 45 memories of 8 heads took 32 us; this takes 26.)
 #include "sm100.cuh"
 #include "sma_paged.cuh"
 
@@ -49,27 +54,93 @@ struct Smem {
     Tiles tiles;
 };
 
+// Two float32 values side by side, multiplied and added by one instruction.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float x, float y) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
+}
+__device__ __forceinline__ void fma2(Pair& d, Pair a, Pair b) { asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b)); }
+__device__ __forceinline__ float half_of(Pair p, int i) {
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+    return i ? hi : lo;
+}
+
+// U and V of a lane's four columns for NT tokens: a pair is two tokens of a
+// column (their Q and C stand side by side), or two columns of a single token.
+template <int NT>
+struct Sums {
+    static constexpr int kPairs = NT == 1 ? 2 : 2 * NT;
+    Pair u[kPairs], v[kPairs];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) u[i] = v[i] = 0;
+    }
+    // adds x (four columns of one row) times that row's Q and C of the tokens at f
+    __device__ __forceinline__ void add(const float4& x, const float* f) {
+        if constexpr (NT == 1) {
+            const Pair q = pair(f[0], f[0]), c = pair(f[kTT], f[kTT]), x01 = pair(x.x, x.y), x23 = pair(x.z, x.w);
+            fma2(u[0], q, x01); fma2(u[1], q, x23);
+            fma2(v[0], c, x01); fma2(v[1], c, x23);
+        } else {
+            const Pair xx[4] = {pair(x.x, x.x), pair(x.y, x.y), pair(x.z, x.z), pair(x.w, x.w)};
+#pragma unroll
+            for (int t = 0; t < NT; t += 4) {
+                ulonglong2 q, c;
+                if (t + 4 <= NT) {
+                    q = *reinterpret_cast<const ulonglong2*>(f + t);
+                    c = *reinterpret_cast<const ulonglong2*>(f + kTT + t);
+                } else {
+                    q.x = *reinterpret_cast<const Pair*>(f + t);
+                    c.x = *reinterpret_cast<const Pair*>(f + kTT + t);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    fma2(u[2 * t + i], q.x, xx[i]);
+                    fma2(v[2 * t + i], c.x, xx[i]);
+                    if (t + 4 <= NT) {
+                        fma2(u[2 * t + 4 + i], q.y, xx[i]);
+                        fma2(v[2 * t + 4 + i], c.y, xx[i]);
+                    }
+                }
+            }
+        }
+    }
+    static __device__ __forceinline__ float at(const Pair* p, int t, int i) {
+        return NT == 1 ? half_of(p[i / 2], i & 1) : half_of(p[t / 2 * 4 + i], t & 1);
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ float4 four_of(const T* p) {
+    if constexpr (sizeof(T) == 4) {
+        return *reinterpret_cast<const float4*>(p);
+    } else {
+        const uint2 b = *reinterpret_cast<const uint2*>(p);
+        return make_float4(__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u), __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u));
+    }
+}
+
 // A piece of a run for the first NT tokens of the tile.
 template <typename T, int N, int P, int NT, typename M>
 __device__ __forceinline__ void run_piece(const Params& prm, Smem<M, N>& s, const Walk& w, int run, int t0, int rows,
                                           Feed<M, Tiles>& feed, int& taken, const WaitCtx& wc, bool& ok) {
-    constexpr int LPR = P / 2, RPW = 32 / LPR;      // lanes of a row, rows of the warp at a time
+    constexpr int LPR = P / 4, RPW = 32 / LPR;      // lanes of a row, rows of the warp at a time
     const SmaPagedArgs& a = prm.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = group_of(w.h, a.H, a.G);
     const float qscale = kLog2e * rsqrtf((float)N);
     float(*qc)[2 * kTT] = s.qc[warp];
     int count[NT];
-    float2 e[NT];
+    float4 e[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const bool live = t < rows;
         const size_t tok = (size_t)(t0 + t);
         count[t] = live ? a.mem_count[t0 + t] : -1;
-        e[t] = make_float2(0.f, 0.f);
-        if (live) {
-            const T* src = static_cast<const T*>(a.E) + (tok * a.H + w.h) * P + 2 * (lane % LPR);
-            e[t] = make_float2(ldf(src), ldf(src + 1));
-        }
+        e[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live) e[t] = four_of(static_cast<const T*>(a.E) + (tok * a.H + w.h) * P + 4 * (lane % LPR));
 #pragma unroll
         for (int n = lane; n < N; n += 32) {
             qc[n][t] = live ? qscale * ldf(static_cast<const T*>(a.Q) + (tok * a.H + w.h) * N + n) : 0.f;
@@ -79,63 +150,36 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M, N>& s, cons
     const int bad = readable_memories(a.cache.table + (size_t)s.tiles.seq(w.k) * a.cache.width, a.cache, w.first_memory(), w.last_memory());
     __syncwarp();
     float m[NT], l[NT];
-    float2 o[NT];
+    float o[NT][4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) { m[t] = -FLT_MAX; l[t] = 0.f; o[t] = make_float2(0.f, 0.f); }
+    for (int t = 0; t < NT; ++t) { m[t] = -FLT_MAX; l[t] = 0.f; o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f; }
     const int last = min(w.last_memory(), bad);
     for (int c = w.first_memory(); c < last; ++c) {
-        float2 u[NT], v[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) u[t] = v[t] = make_float2(0.f, 0.f);
+        Sums<NT> sums;
+        sums.clear();
 #pragma unroll 1
         for (int k = 0; k < M::kPieces; ++k) {
             const int st = taken % M::kStages;
             if (ok) ok = mbar_wait_warp(smem_u32(&s.full[warp][st]), (uint32_t)(taken / M::kStages) & 1u, wc, 1);
             ++taken;
             if (!ok) continue;
-            const T* rows_s = reinterpret_cast<const T*>(s.ring[warp][st]) + (lane / LPR) * P + 2 * (lane % LPR);
+            const T* rows_s = reinterpret_cast<const T*>(s.ring[warp][st]) + (lane / LPR) * P + 4 * (lane % LPR);
 #pragma unroll
-            for (int r = 0; r < M::kRows / RPW; ++r) {
-                float2 x;
-                if constexpr (sizeof(T) == 4) {
-                    x = *reinterpret_cast<const float2*>(rows_s + r * RPW * P);
-                } else {
-                    const unsigned b = *reinterpret_cast<const unsigned*>(rows_s + r * RPW * P);
-                    x = make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
-                }
-                const float* f = qc[k * M::kRows + r * RPW + lane / LPR];
-                alignas(16) float fq[(NT + 3) / 4 * 4], fc[(NT + 3) / 4 * 4];
-#pragma unroll
-                for (int t = 0; t < NT; t += 4) {
-                    if constexpr (NT == 1) {
-                        fq[0] = f[0];
-                        fc[0] = f[kTT];
-                    } else {
-                        *reinterpret_cast<float4*>(fq + t) = *reinterpret_cast<const float4*>(f + t);
-                        *reinterpret_cast<float4*>(fc + t) = *reinterpret_cast<const float4*>(f + kTT + t);
-                    }
-                }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    u[t].x = fmaf(fq[t], x.x, u[t].x);
-                    u[t].y = fmaf(fq[t], x.y, u[t].y);
-                    v[t].x = fmaf(fc[t], x.x, v[t].x);
-                    v[t].y = fmaf(fc[t], x.y, v[t].y);
-                }
-            }
+            for (int r = 0; r < M::kRows / RPW; ++r) sums.add(four_of(rows_s + r * RPW * P), qc[k * M::kRows + r * RPW + lane / LPR]);
             __syncwarp();        // every lane has read the stage
             feed.fill(prm, s.tiles, s.ring[warp], s.full[warp]);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const float sc = warp_sum(fmaf(u[t].x, e[t].x, u[t].y * e[t].y));
+            const float u0 = sums.at(sums.u, t, 0), u1 = sums.at(sums.u, t, 1), u2 = sums.at(sums.u, t, 2), u3 = sums.at(sums.u, t, 3);
+            const float sc = warp_sum(fmaf(u0, e[t].x, u1 * e[t].y) + fmaf(u2, e[t].z, u3 * e[t].w));
             if (c < count[t]) {                       // the row sees this memory (same for the whole warp)
                 const float mn = fmaxf(m[t], sc), al = exp2f(m[t] - mn), wt = exp2f(sc - mn);
                 l[t] = fmaf(l[t], al, wt);
                 m[t] = mn;
                 if (wt != 0.f) {                      // 0 weight reads nothing, whatever the value is
-                    o[t].x = fmaf(o[t].x, al, wt * v[t].x);
-                    o[t].y = fmaf(o[t].y, al, wt * v[t].y);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[t][i] = fmaf(o[t][i], al, wt * sums.at(sums.v, t, i));
                 }
             }
         }
@@ -147,21 +191,20 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M, N>& s, cons
     for (int t = 0; t < NT; ++t) {
         // a lane's o holds the rows it read: sum over the lanes of the same columns
 #pragma unroll
-        for (int off = LPR; off < 32; off <<= 1) {
-            o[t].x += __shfl_xor_sync(0xffffffffu, o[t].x, off);
-            o[t].y += __shfl_xor_sync(0xffffffffu, o[t].y, off);
-        }
+        for (int off = LPR; off < 32; off <<= 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[t][i] += __shfl_xor_sync(0xffffffffu, o[t][i], off);
         if (t >= rows || lane >= LPR) continue;
         const bool left = count[t] < 0 || count[t] > bad;      // a row that is not to be computed
         if (w.whole()) {
             if (left) continue;
-            const size_t at = ((size_t)(t0 + t) * a.H + w.h) * P + 2 * lane;
+            const size_t at = ((size_t)(t0 + t) * a.H + w.h) * P + 4 * lane;
             const float f = l[t] == 0.f ? 0.f : (a.y_ssd ? a.g : 1.f) / l[t];
-            const float2 y = a.y_ssd ? *reinterpret_cast<const float2*>(a.y_ssd + at) : make_float2(0.f, 0.f);
-            *reinterpret_cast<float2*>(a.out + at) = make_float2(fmaf(f, o[t].x, y.x), fmaf(f, o[t].y, y.y));
+            const float4 y = a.y_ssd ? *reinterpret_cast<const float4*>(a.y_ssd + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<float4*>(a.out + at) = make_float4(fmaf(f, o[t][0], y.x), fmaf(f, o[t][1], y.y), fmaf(f, o[t][2], y.z), fmaf(f, o[t][3], y.w));
         } else {
             float* row = piece_rows<kTT, P>(a.part, run, which) + t * (P + 4);
-            *reinterpret_cast<float2*>(row + 2 * lane) = o[t];
+            *reinterpret_cast<float4*>(row + 4 * lane) = make_float4(o[t][0], o[t][1], o[t][2], o[t][3]);
             if (lane == 0) { row[P] = m[t]; row[P + 1] = left ? -1.f : l[t]; }
         }
     }
@@ -197,7 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_kernel(const __grid_con
     for (; next_piece(w); advance(s.tiles, w, a.H)) {
         const int t0 = s.tiles.t0[w.k], rows = s.tiles.rows(w.k);
         if (rows == 1) run_piece<T, N, P, 1>(prm, s, w, run, t0, rows, feed, taken, wc, ok);
+        else if (rows == 2) run_piece<T, N, P, 2>(prm, s, w, run, t0, rows, feed, taken, wc, ok);
         else if (rows <= 4) run_piece<T, N, P, 4>(prm, s, w, run, t0, rows, feed, taken, wc, ok);
+        else if (rows <= 6) run_piece<T, N, P, 6>(prm, s, w, run, t0, rows, feed, taken, wc, ok);
         else run_piece<T, N, P, 8>(prm, s, w, run, t0, rows, feed, taken, wc, ok);
     }
     if (!ok) feed.drain(s.full[warp]);      // else every copy has been waited for
