@@ -6,17 +6,19 @@
 //   o = sum_c softmax_c(s) v_c,  out = y_ssd + g o        (o = 0 with none visible).
 //
 // Every warp is a worker of its own, with its run of units and its ring of stages
-// (16 rows of a memory each, copied ahead over the ends of items): a lane has four
-// columns of every second row, and a value is used for U and V of up to 8 tokens,
-// whose Q and C stand in the warp's own shared memory.  What bounds runs of
-// several tokens is the issue of multiply-adds and of the shared loads that feed
-// them; two tokens of a column share one paired multiply-add, and four columns a lane
-// halve the loads of Q and C (32 runs of up to 6 tokens over 131 memories, 32
-// heads: 888 us with two columns and single multiply-adds, 664 so, 485 at HBM's
-// rate; 64 single tokens 909 and 888 us, HBM).  Scores are summed over the warp,
-// the softmax runs online in base 2, and v is folded into the lane's columns.
-// (With eight warps to a piece and loads straight from global memory, 7 runs of
-// 5 float32 tokens over 45 memories of 8 heads took 32 us; this takes 26.)
+// copied ahead over the ends of items (16 rows of a memory each, 32 where two fit:
+// up to 400 memories in the case below took 90 us with 8 rows, 72 with 16, 62 with
+// 32).  A lane has four columns of every second row, and a value is used for U and
+// V of up to 8 tokens, whose Q and C stand in the warp's own shared memory.  What
+// bounds runs of several tokens is the issue of multiply-adds and of the shared
+// loads that feed them: two tokens of a column share one paired multiply-add, and
+// four columns a lane halve the loads of Q and C (32 runs of up to 6 tokens over
+// 131 memories, 32 heads: 888 us with two columns and single multiply-adds, 664 so,
+// 600-625 with the cheaper wait of sma_paged.cuh, 485 at HBM's rate; 64 single
+// tokens 905 us, HBM).  Scores are summed over the warp, the softmax runs online in
+// base 2, and v is folded into the lane's columns.  (With eight warps to a piece
+// and loads straight from global memory, 7 runs of 5 float32 tokens over 45
+// memories of 8 heads took 32 us; this takes 25.)
 #include "sm100.cuh"
 #include "sma_paged.cuh"
 
@@ -38,7 +40,7 @@ struct Params { SmaPagedArgs a; };
 
 template <typename T, int N, int P>
 struct Dense {
-    static constexpr int kRows = 16, kStages = N == 128 ? 3 : 4, kPieces = N / kRows;      // rows of a stage
+    static constexpr int kRows = N == 64 ? 32 : 16, kStages = N == 64 ? 2 : N == 128 ? 3 : 4, kPieces = N / kRows;
     static constexpr uint32_t kStageBytes = kRows * P * sizeof(T);
     static __device__ __forceinline__ void copy(const Params& prm, size_t mem, int piece, uint32_t dst, uint32_t full) {
         bulk_load(dst, static_cast<const T*>(prm.a.cache.pages) + (mem * N + piece * kRows) * P, kStageBytes, full);
@@ -160,7 +162,7 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M, N>& s, cons
 #pragma unroll 1
         for (int k = 0; k < M::kPieces; ++k) {
             const int st = taken % M::kStages;
-            if (ok) ok = mbar_wait_warp(smem_u32(&s.full[warp][st]), (uint32_t)(taken / M::kStages) & 1u, wc, 1);
+            if (ok) ok = wait_warp(smem_u32(&s.full[warp][st]), (uint32_t)(taken / M::kStages) & 1u, wc, 1);
             ++taken;
             if (!ok) continue;
             const T* rows_s = reinterpret_cast<const T*>(s.ring[warp][st]) + (lane / LPR) * P + 4 * (lane % LPR);

@@ -376,7 +376,9 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const W
         bool clean = true;
         auto take = [&](auto piece) {
             const int st = taken % M::kStages;
-            if (ok) ok = mbar_wait_warp(smem_u32(&s.full[warp][st]), (uint32_t)(taken / M::kStages) & 1u, wc, 1);
+            const uint32_t bar = smem_u32(&s.full[warp][st]), phase = (uint32_t)(taken / M::kStages) & 1u;
+            // bfloat16 memories are waited for longer than a look takes (64 single tokens 462 us, 465 with it)
+            if (ok) ok = M::kFp4 ? wait_warp(bar, phase, wc, 1) : mbar_wait_warp(bar, phase, wc, 1);
             ++taken;
             if (!ok) return;
             clean &= multiply<M, N, NT, PARTS, decltype(piece)::value>(s.ring[warp][st], col, acc);

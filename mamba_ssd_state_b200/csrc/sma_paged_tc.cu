@@ -7,7 +7,7 @@
 // with the accumulators in TMEM (U in columns 0..255, V in 256..511).  Reading a
 // memory once for 128 tokens instead of 8 makes the run compute-bound:
 // 4 x 256 tokens over 100 memories took 470 us on warp-level products, where
-// every 8 tokens stream all memories through the SM again, and take 89 here.
+// every 8 tokens stream all memories through the SM again, and take 79 here.
 //
 // What differs from prefill: memories come from pages, a tile ends with its
 // sequence (rows behind it belong to others and are not written), every row has
@@ -15,7 +15,7 @@
 // that a few long sequences fill the machine; an item that falls into several
 // runs is joined by the combine kernel.
 //
-// CTA pairs (runs of more than 128 tokens on average): two CTAs of a cluster run
+// CTA pairs (runs of more than 160 tokens on average): two CTAs of a cluster run
 // the two halves of a 256-row tile as M = 256 MMAs (cta_group::2).  Each loads
 // its own rows of Q and C and two memories of a batch, so an SM takes in half
 // the bytes for each product and its ring holds twice the batches: with single
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
                 const int q0 = S::kMem * rank, mine = max(0, min(S::kMem, nv - q0));
                 const int c = c0 + (lane < mine ? q0 + lane : 0);
                 const size_t mem = memory_index(a.cache, a.H, table[c / a.cache.R], w.h, c % a.cache.R);
-                if (!(ok = mbar_wait_warp(empty(st), ((uint32_t)(it / S::kStages) & 1u) ^ 1u, wc, 3))) break;
+                if (!(ok = wait_warp(empty(st), ((uint32_t)(it / S::kStages) & 1u) ^ 1u, wc, 3))) break;
                 if (lane == 0 && rank == 0) mbar_expect_tx(full(st), (uint32_t)nv * S::kMemBytes);
                 __syncwarp();
                 if (lane < mine) {
@@ -178,10 +178,10 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
                             else tma_load_3d(smem_u32(to + k * kPanel), map, bar(b), 64 * k, head, t0);
                         }
                     };
-                    if (!(ok = mbar_wait_warp(bar(Q_FREE), ph ^ 1u, wc, 1))) break;
+                    if (!(ok = wait_warp(bar(Q_FREE), ph ^ 1u, wc, 1))) break;
                     if (lane == 0) rows(s.q, &prm.map_q, Q_FULL, w.h);
                     ++q_filled;
-                    if (!(ok = mbar_wait_warp(bar(C_FREE), ph ^ 1u, wc, 2))) break;
+                    if (!(ok = wait_warp(bar(C_FREE), ph ^ 1u, wc, 2))) break;
                     if (lane == 0) rows(s.c, &prm.map_c, C_FULL, grp);
                     ph ^= 1u;
                     prefetch_rows();
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
         for (; ok && next_piece(w); advance(s.tiles, w, a.H)) {
             const int first = w.first_memory(), last = min(w.last_memory(), readable_memories(table_of(), a.cache, w.first_memory(), w.last_memory()));
             if (first >= last) continue;
-            if (!(ok = mbar_wait_warp(bar(Q_FULL), ph, wc, 4))) break;
+            if (!(ok = wait_warp(bar(Q_FULL), ph, wc, 4))) break;
             for (int c0 = first; c0 < last; c0 += kCB, ++it) {
                 const int nv = min(kCB, last - c0), st = it % S::kStages;
                 const bool end = c0 + kCB >= last;
@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
                         else mma_f16_ss(d, ad, bd, idesc, kk > 0 ? 1u : 0u);
                     }
                 };
-                if (!(ok = mbar_wait_warp(full(st), (uint32_t)(it / S::kStages) & 1u, wc, 5))) break;
-                if (!(ok = mbar_wait_warp(bar(U_EMPTY), ((uint32_t)it & 1u) ^ 1u, wc, 6))) break;
+                if (!(ok = wait_warp(full(st), (uint32_t)(it / S::kStages) & 1u, wc, 5))) break;
+                if (!(ok = wait_warp(bar(U_EMPTY), ((uint32_t)it & 1u) ^ 1u, wc, 6))) break;
                 tc_fence_after();
                 if (lane == 0) {
                     product(tmem, s.q);
@@ -235,8 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
                     if (end) commit(bar(Q_FREE));
                 }
                 __syncwarp();
-                if (c0 == first && !(ok = mbar_wait_warp(bar(C_FULL), ph, wc, 7))) break;
-                if (!(ok = mbar_wait_warp(bar(V_EMPTY), ((uint32_t)it & 1u) ^ 1u, wc, 8))) break;
+                if (c0 == first && !(ok = wait_warp(bar(C_FULL), ph, wc, 7))) break;
+                if (!(ok = wait_warp(bar(V_EMPTY), ((uint32_t)it & 1u) ^ 1u, wc, 8))) break;
                 tc_fence_after();
                 if (lane == 0) {
                     product(tmem + kColV, s.c);
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
                 const int nv = min(kCB, last - c0);
                 const uint32_t ph = (uint32_t)it & 1u;
                 float part[kCB] = {0.f, 0.f, 0.f, 0.f};
-                if (ok) ok = mbar_wait_warp(bar(U_FULL), ph, wc, 9);
+                if (ok) ok = wait_warp(bar(U_FULL), ph, wc, 9);
                 if (ok) {
                     tc_fence_after();
 #pragma unroll
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) sma_paged_tc_kernel(const __grid_
                 const float2 alpha2 = make_float2(alpha, alpha);
 #pragma unroll
                 for (int q = 0; q < kHalfP / 2; ++q) o2[q] = __fmul2_rn(o2[q], alpha2);
-                if (ok) ok = mbar_wait_warp(bar(V_FULL), ph, wc, 10);
+                if (ok) ok = wait_warp(bar(V_FULL), ph, wc, 10);
                 if (ok) {
                     tc_fence_after();
 #pragma unroll
@@ -473,15 +473,18 @@ cudaError_t run(const SmaPagedArgs& a, cudaStream_t st) {
 
 bool sma_paged_tc_applicable(const SmaPagedArgs& a, dart_dtype dt) {
     // More than 8 rows a sequence are two tiles of the warp-level kernel, which then streams the memories
-    // twice.  32 sequences over up to 100 memories of 32 heads, warp-level / here: 6 rows on average
-    // 218 / 280 us, 9 rows 341 / 285, 12 rows 399 / 309, 48 rows 1267 / 337; 4 sequences: 42 / 53, 44 / 53,
-    // 50 / 53 and 124 / 57 us.
+    // twice.  32 sequences over up to 100 memories of 32 heads, warp-level / here: 4 rows on average
+    // 188 / 263 us, 6 rows 210 / 289, 9 rows 314 / 316, 12 rows 378 / 282; 4 sequences: 4 rows 41 / 44 us,
+    // 6 rows 43 / 43, 9 rows 48 / 44, 15 rows 51 / 44.
     return dt == DART_BF16 && !a.cache.mxfp4 && a.P == kP && (a.N == 128 || a.N == 64) && a.T > 8 * (long long)a.B &&
            a.B + a.T / kRows <= kCap;
 }
 
 cudaError_t launch_sma_paged_tc(const SmaPagedArgs& a, cudaStream_t st) {
-    if (a.T > 128 * (long long)a.B) return a.N == 128 ? run<128, true>(a, st) : run<64, true>(a, st);
+    // A pair's tile is 256 rows, full or not.  16 sequences, single blocks / pairs: 89 rows on average
+    // 189 / 291 us, 112 rows 195 / 283, 134 rows 274 / 293, 195 rows 370 / 302; 4 sequences: 105 rows 50 / 76 us,
+    // 161 rows 77 / 79, 201 rows 85 / 79.
+    if (a.T > 160 * (long long)a.B) return a.N == 128 ? run<128, true>(a, st) : run<64, true>(a, st);
     return a.N == 128 ? run<128, false>(a, st) : run<64, false>(a, st);
 }
 
