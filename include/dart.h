@@ -461,7 +461,7 @@ dart_status dart_cache_read_paged(const dart_dims* dims, dart_dtype dtype, const
  *   some of the tokens (drafts) turn out not to be wanted.
  *   n_chunks, pos: int32 [B], memories finished and tokens into the chunk, before
  *   the run; n_chunks_out, pos_out: after it, in memory of their own.
- *   y: float [T,H,P].  mem_count: int32 [T], the number of memories each token may
+ *   y: float [T,H,P], apart from the inputs.  mem_count: int32 [T], the number of memories each token may
  *   attend to (those finished before it), -1 for the tokens of a sequence that
  *   was left as it is; dart_sma_paged's argument of that name.
  * A token sees a finished chunk only through its memory, so the pages must have
@@ -483,7 +483,7 @@ size_t dart_sma_paged_workspace_bytes(const dart_dims* dims);
  * sequence's first mem_count[t] memories,
  *   out = y_ssd + g * o  (y_ssd != NULL), else out = o;  o = 0 with none to see.
  *   Q[T,H,N], E[T,H,P], Cm[T,G,N]: dtype; y_ssd: nullable float [T,H,P]; out:
- *   float [T,H,P], y_ssd itself or not overlapping it.
+ *   float [T,H,P], y_ssd itself or not overlapping it, and apart from Q, E and Cm.
  *   mem_count: int32 [T]; -1 marks a row that is left as it is.
  *   workspace: dart_sma_paged_workspace_bytes(), 16-byte aligned, contents on
  *   entry do not matter; calls that may overlap on the GPU need one each.

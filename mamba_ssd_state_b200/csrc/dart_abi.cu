@@ -94,6 +94,11 @@ dart_status check_common(const dart_dims* d, dart_dtype dt, bool need_seqlen) {
     return DART_OK;
 }
 
+bool overlap(const void* p, size_t pbytes, const void* q, size_t qbytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + qbytes && b < a + pbytes;
+}
+
 // The paged cache's own fields, and the memory shape it is asked to hold.
 dart_status check_paged(const char* call, const dart_dims* d, const dart_paged_cache* c, dart::PagedCache* out) {
     if (!c) return fail(DART_ERR_INVALID_ARG, "%s: cache: null pointer", call);
@@ -537,6 +542,11 @@ dart_status dart_ssd_extend(const dart_dims* d, dart_dtype dtype, const void* x,
             if ((i != j || from[i] != to[j]) && from[i] < to[j] + floats && to[j] < from[i] + floats)
                 return fail(DART_ERR_INVALID_ARG,
                             "dart_ssd_extend: state_out and dH_cur_out are their inputs or apart from both");
+    // Blocks read the tokens at their own time, while others write y.
+    const size_t T = d->seqlen, item = dtype == DART_F32 ? 4 : 2, yb = T * d->nheads * d->headdim * 4;
+    const size_t xb = T * d->nheads * d->headdim * item, bc = T * d->ngroups * d->dstate * item;
+    if (T > 0 && (overlap(y, yb, x, xb) || overlap(y, yb, Bm, bc) || overlap(y, yb, Cm, bc) || overlap(y, yb, dt, T * d->nheads * 4)))
+        return fail(DART_ERR_INVALID_ARG, "dart_ssd_extend: y overlaps x, dt, Bm or Cm");
     a.B = d->batch; a.T = d->seqlen; a.H = d->nheads; a.P = d->headdim; a.N = d->dstate; a.S = d->chunk; a.G = d->ngroups;
     a.x = x; a.dt = dt; a.A = A; a.Bm = Bm; a.Cm = Cm; a.cu = cu_tokens;
     a.state = state; a.state_out = state_out; a.cur = dH_cur; a.cur_out = dH_cur_out;
@@ -575,6 +585,11 @@ dart_status dart_sma_paged(const dart_dims* d, dart_dtype dtype, const void* Q, 
     const size_t need = dart_sma_paged_workspace_bytes(d);
     if (workspace_bytes < need)
         return fail(DART_ERR_INVALID_ARG, "workspace: %zu bytes, need %zu", workspace_bytes, need);
+    // Workers read the tokens at their own time, while others write out.
+    const size_t T = d->seqlen, item = dtype == DART_F32 ? 4 : 2, ob = T * d->nheads * d->headdim * 4;
+    if (overlap(out, ob, Q, T * d->nheads * d->dstate * item) || overlap(out, ob, E, T * d->nheads * d->headdim * item) ||
+        overlap(out, ob, Cm, T * d->ngroups * d->dstate * item))
+        return fail(DART_ERR_INVALID_ARG, "dart_sma_paged: out overlaps Q, E or Cm");
     a.B = d->batch; a.T = d->seqlen; a.H = d->nheads; a.P = d->headdim; a.N = d->dstate; a.G = d->ngroups;
     a.Q = Q; a.E = E; a.Cm = Cm; a.cu = cu_tokens; a.mem_count = mem_count; a.g = g; a.y_ssd = y_ssd; a.out = out;
     a.part = static_cast<float*>(workspace); a.status = status_word();

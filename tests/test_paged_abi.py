@@ -114,6 +114,24 @@ def test_extend_arguments(lib):
         assert extend(lib, **kw) == dart.DART_ERR_INVALID_ARG
 
 
+def test_results_do_not_go_onto_the_tokens(lib):
+    d, c = dims(), cache()
+    size = 6 * 4 * 64 * 4
+    for k in range(3):                                      # out begins in, and ends in, each of Q, E and Cm
+        for off in (64, 16 - size):
+            tokens = [FAR[0], FAR[1], FAR[2]]
+            out = ctypes.c_void_p(tokens[k].value + off)
+            assert lib.dart_sma_paged(ctypes.byref(d), 1, *tokens, FAKE, ctypes.byref(c), FAKE, 0.5, None, out, FAKE, 1 << 30, None) == dart.DART_ERR_INVALID_ARG
+            assert b"out overlaps" in lib.dart_last_error()
+    for k in (0, 1, 3, 4):                                  # y on x, dt, Bm and Cm
+        tokens = [FAR[8], FAR[9], FAR[10], FAR[11], FAR[12]]
+        for off in (16, 16 - size):
+            y = ctypes.c_void_p(tokens[k].value + off)
+            assert lib.dart_ssd_extend(ctypes.byref(d), 1, *tokens, FAKE, FAR[0], FAR[0], FAR[1], FAR[1], ctypes.byref(c), FAR[2], FAR[3],
+                                       FAR[4], FAR[5], y, FAKE, None) == dart.DART_ERR_INVALID_ARG
+            assert b"y overlaps" in lib.dart_last_error()
+
+
 def test_binding_refuses_what_does_not_fit():
     """Checks that need no GPU: they come before the first CUDA call."""
     z = torch.zeros
