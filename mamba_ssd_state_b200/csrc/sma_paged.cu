@@ -14,11 +14,14 @@
 // loads that feed them: two tokens of a column share one paired multiply-add, and
 // four columns a lane halve the loads of Q and C (32 runs of up to 6 tokens over
 // 131 memories, 32 heads: 888 us with two columns and single multiply-adds, 664 so,
-// 600-625 with the cheaper wait of sma_paged.cuh, 485 at HBM's rate; 64 single
-// tokens 905 us, HBM).  Scores are summed over the warp, the softmax runs online in
-// base 2, and v is folded into the lane's columns.  (With eight warps to a piece
-// and loads straight from global memory, 7 runs of 5 float32 tokens over 45
-// memories of 8 heads took 32 us; this takes 25.)
+// 590 with the cheaper wait of sma_paged.cuh, 540 with the softmax as below, 485 at
+// HBM's rate; 64 single tokens 892 us, HBM).  A token's scores are summed into the
+// lanes that own it, which alone run its softmax (online, base 2) and pass its two
+// weights on (against a warp sum and a softmax in every lane for each token, 19 runs
+// of up to 137 tokens over 48 memories of 16 x 16: 60 -> 42 us); v is folded into
+// the lane's columns.  (With eight warps to a piece and loads straight from global
+// memory, 7 runs of 5 float32 tokens over 45 memories of 8 heads took 32 us; this
+// takes 24.)
 #include "sm100.cuh"
 #include "sma_paged.cuh"
 
@@ -125,6 +128,25 @@ __device__ __forceinline__ float4 four_of(const T* p) {
     }
 }
 
+// Sums of W values over the warp, the sum of p[lane >> (5 - log2 W)] to each lane:
+// a lane keeps half of its values and passes the other half on while it has
+// several, so 8 sums take 9 shuffles and not 40.
+template <int W>
+__device__ __forceinline__ float sum_to_owner(float (&p)[W], int lane) {
+    int off = 16;
+#pragma unroll
+    for (int half = W / 2; half >= 1; half /= 2, off /= 2)
+#pragma unroll
+        for (int j = 0; j < half; ++j) {
+            const bool up = lane & off;
+            const float got = __shfl_xor_sync(0xffffffffu, up ? p[j] : p[j + half], off);
+            p[j] = (up ? p[j + half] : p[j]) + got;
+        }
+#pragma unroll
+    for (; off >= 1; off /= 2) p[0] += __shfl_xor_sync(0xffffffffu, p[0], off);
+    return p[0];
+}
+
 // A piece of a run for the first NT tokens of the tile.
 template <typename T, int N, int P, int NT, typename M>
 __device__ __forceinline__ void run_piece(const Params& prm, Smem<M, N>& s, const Walk& w, int run, int t0, int rows,
@@ -134,13 +156,14 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M, N>& s, cons
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = group_of(w.h, a.H, a.G);
     const float qscale = kLog2e * rsqrtf((float)N);
     float(*qc)[2 * kTT] = s.qc[warp];
-    int count[NT];
+    // the softmax of a token belongs to the lanes that its sums end in: lane >> kShift is their token
+    constexpr int W = NT == 6 ? 8 : NT, kShift = W == 1 ? 5 : W == 2 ? 4 : W == 4 ? 3 : 2;
+    const int mine = lane >> kShift, count = mine < rows ? a.mem_count[t0 + mine] : -1;
     float4 e[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const bool live = t < rows;
         const size_t tok = (size_t)(t0 + t);
-        count[t] = live ? a.mem_count[t0 + t] : -1;
         e[t] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (live) e[t] = four_of(static_cast<const T*>(a.E) + (tok * a.H + w.h) * P + 4 * (lane % LPR));
 #pragma unroll
@@ -151,10 +174,9 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M, N>& s, cons
     }
     const int bad = readable_memories(a.cache.table + (size_t)s.tiles.seq(w.k) * a.cache.width, a.cache, w.first_memory(), w.last_memory());
     __syncwarp();
-    float m[NT], l[NT];
-    float o[NT][4];
+    float m = -FLT_MAX, l = 0.f, o[NT][4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) { m[t] = -FLT_MAX; l[t] = 0.f; o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f; }
+    for (int t = 0; t < NT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
     const int last = min(w.last_memory(), bad);
     for (int c = w.first_memory(); c < last; ++c) {
         Sums<NT> sums;
@@ -171,18 +193,31 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M, N>& s, cons
             __syncwarp();        // every lane has read the stage
             feed.fill(prm, s.tiles, s.ring[warp], s.full[warp]);
         }
+        float p[W];
+#pragma unroll
+        for (int t = 0; t < W; ++t) {
+            if (t < NT) {
+                const float u0 = sums.at(sums.u, t, 0), u1 = sums.at(sums.u, t, 1), u2 = sums.at(sums.u, t, 2), u3 = sums.at(sums.u, t, 3);
+                p[t] = fmaf(u0, e[t].x, u1 * e[t].y) + fmaf(u2, e[t].z, u3 * e[t].w);
+            } else {
+                p[t] = 0.f;
+            }
+        }
+        const float sc = sum_to_owner<W>(p, lane);
+        float al = 1.f, wt = 0.f;
+        if (c < count) {                              // the row sees this memory
+            const float mn = fmaxf(m, sc);
+            al = exp2f(m - mn);
+            wt = exp2f(sc - mn);
+            l = fmaf(l, al, wt);
+            m = mn;
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const float u0 = sums.at(sums.u, t, 0), u1 = sums.at(sums.u, t, 1), u2 = sums.at(sums.u, t, 2), u3 = sums.at(sums.u, t, 3);
-            const float sc = warp_sum(fmaf(u0, e[t].x, u1 * e[t].y) + fmaf(u2, e[t].z, u3 * e[t].w));
-            if (c < count[t]) {                       // the row sees this memory (same for the whole warp)
-                const float mn = fmaxf(m[t], sc), al = exp2f(m[t] - mn), wt = exp2f(sc - mn);
-                l[t] = fmaf(l[t], al, wt);
-                m[t] = mn;
-                if (wt != 0.f) {                      // 0 weight reads nothing, whatever the value is
+            const float at = __shfl_sync(0xffffffffu, al, t << kShift), wtt = __shfl_sync(0xffffffffu, wt, t << kShift);
+            if (wtt != 0.f) {                         // 0 weight reads nothing, whatever the value is
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[t][i] = fmaf(o[t][i], al, wt * sums.at(sums.v, t, i));
-                }
+                for (int i = 0; i < 4; ++i) o[t][i] = fmaf(o[t][i], at, wtt * sums.at(sums.v, t, i));
             }
         }
     }
@@ -196,18 +231,20 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M, N>& s, cons
         for (int off = LPR; off < 32; off <<= 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[t][i] += __shfl_xor_sync(0xffffffffu, o[t][i], off);
+        const float lt = __shfl_sync(0xffffffffu, l, t << kShift), mt = __shfl_sync(0xffffffffu, m, t << kShift);
+        const int ct = __shfl_sync(0xffffffffu, count, t << kShift);
         if (t >= rows || lane >= LPR) continue;
-        const bool left = count[t] < 0 || count[t] > bad;      // a row that is not to be computed
+        const bool left = ct < 0 || ct > bad;      // a row that is not to be computed
         if (w.whole()) {
             if (left) continue;
             const size_t at = ((size_t)(t0 + t) * a.H + w.h) * P + 4 * lane;
-            const float f = l[t] == 0.f ? 0.f : (a.y_ssd ? a.g : 1.f) / l[t];
+            const float f = lt == 0.f ? 0.f : (a.y_ssd ? a.g : 1.f) / lt;
             const float4 y = a.y_ssd ? *reinterpret_cast<const float4*>(a.y_ssd + at) : make_float4(0.f, 0.f, 0.f, 0.f);
             *reinterpret_cast<float4*>(a.out + at) = make_float4(fmaf(f, o[t][0], y.x), fmaf(f, o[t][1], y.y), fmaf(f, o[t][2], y.z), fmaf(f, o[t][3], y.w));
         } else {
             float* row = piece_rows<kTT, P>(a.part, run, which) + t * (P + 4);
             *reinterpret_cast<float4*>(row + 4 * lane) = make_float4(o[t][0], o[t][1], o[t][2], o[t][3]);
-            if (lane == 0) { row[P] = m[t]; row[P + 1] = left ? -1.f : l[t]; }
+            if (lane == 0) { row[P] = mt; row[P + 1] = left ? -1.f : lt; }
         }
     }
     __syncwarp();        // qc is read no more

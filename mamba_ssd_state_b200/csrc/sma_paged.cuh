@@ -258,8 +258,8 @@ __device__ __forceinline__ int readable_memories(const int* table, const PagedCa
 // A warp's wait that costs little when the phase is over already, as it mostly is
 // in these rings: every lane looks for itself and the warp votes; else the
 // bounded wait.  With that wait alone, in which lane 0 polls and tells the
-// others, float32 runs of drafts took 663 us instead of 600-625, 4-bit ones 134
-// instead of 130 and prompt pieces 90 instead of 80.
+// others, float32 runs of drafts took 663 us instead of 590, 4-bit ones 134
+// instead of 131 and prompt pieces 90 instead of 80.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const sm100::WaitCtx& wc, int site) {
     return __all_sync(0xffffffffu, sm100::mbar_try_wait(bar, parity)) || sm100::mbar_wait_warp(bar, parity, wc, site);
 }
