@@ -393,9 +393,9 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const W
             v[j] = 0.f;
 #pragma unroll
             for (int m = 0; m < 4; ++m) v[j] = fmaf(acc[0][m][j], e[m][j], fmaf(acc[0][m][2 + j], e[m][2 + j], v[j]));
+            if (!clean) v[j] = __int_as_float(0x7fffffff);      // for both tokens: the lanes part them next
         }
         float sc = (mine ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, mine ? v[0] : v[1], 4);
-        if (!clean) sc = __int_as_float(0x7fffffff);
         sc += __shfl_xor_sync(0xffffffffu, sc, 8);
         sc += __shfl_xor_sync(0xffffffffu, sc, 16);
         sc *= qm;
