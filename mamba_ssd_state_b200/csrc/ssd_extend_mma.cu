@@ -17,7 +17,7 @@
 // Gram matrix and the weighted x are float32 and go in as three bfloat16 parts
 // (24 bits), so every product is exact and every sum is in float32.  Decays are
 // exponentials of differences of prefix sums that are kept as two floats (their
-// difference is good to 2^-24 of itself however far the prefix has come).
+// difference is good to 2^-24 as long as the block's |dt A| sum to less than 2^29).
 //
 // A block of 256 threads owns PS columns of one (sequence, head): warp w holds 16
 // of them and N PS / 128 rows of H^T and D^T.  The partial sums of y meet in
@@ -135,17 +135,19 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_extend_mma_kernel(ExtendArgs 
     // Decays of the block in a buffer, by one warp: sums of dt A log2(e) in float64, two tokens a lane.
     auto decays = [&](int k) {
         const double la = (double)Ah * 1.4426950408889634;
-        const double u = la * s.dt[k][2 * lane], v = la * s.dt[k][2 * lane + 1];
-        double c = u + v;
+        const double u = la * s.dt[k][2 * lane];
+        double c = u + la * s.dt[k][2 * lane + 1];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const double before = __shfl_up_sync(0xffffffffu, c, o);
             if (lane >= o) c += before;
         }
         const double end = __shfl_sync(0xffffffffu, c, 31);   // tokens past the block's add nothing
+        double first = __shfl_up_sync(0xffffffffu, c, 1);      // up to the lane's first token: nothing of its second one
+        first = lane > 0 ? first + u : u;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const double cum = i ? c : c - v;
+            const double cum = i ? c : first;
             const int t = 2 * lane + i;
             s.hi[k][t] = (float)cum;
             s.lo[k][t] = (float)(cum - (double)(float)cum);

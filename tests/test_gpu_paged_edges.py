@@ -7,7 +7,7 @@ import torch
 from mamba_ssd_state_b200 import dart
 from tests import paged_reference as ref
 from tests.parity import rel_err
-from tests.test_gpu_paged import SHAPES, TOL, Pool, attention_inputs, cumulative, ints, memories_of
+from tests.test_gpu_paged import SHAPES, TOL, Pool, attention_inputs, cumulative, extend_inputs, ints, memories_of, states
 
 pytestmark = pytest.mark.gpu
 FOUR_BIT = [v for v in SHAPES if v[3] == "mxfp4"]
@@ -35,3 +35,64 @@ def test_a_scale_of_255_is_nan_for_every_token_that_sees_it(N, P, dtype, cache, 
         want = ref.sma(*args64, lens, memories, [3] * T)
         assert torch.isnan(out[torch.from_numpy(see).cuda()]).all()
         assert rel_err(out[torch.from_numpy(~see).cuda()], want[~see]) <= TOL if (~see).any() else True
+
+
+# ------------------------------------------------- tokens that are no numbers
+@pytest.mark.parametrize("N, P, dtype", [(128, 64, "bf16"), (64, 64, "bf16"), (128, 64, "f32"), (64, 64, "f32"), (16, 16, "bf16")])
+@pytest.mark.parametrize("lens, S", [([70], 64), ([70], 256), ([30, 45], 32), ([12, 40, 12], 48), ([9, 14], 256)])
+@pytest.mark.parametrize("what", ["dt", "B", "C"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_a_token_that_is_not_finite_leaves_earlier_ones_alone(N, P, dtype, lens, S, what, value):
+    """The recurrence is causal for every value, in runs of any length: what a token holds reaches its own output and
+    later ones, no earlier one and no other head."""
+    rng = np.random.default_rng(sum(lens) + N)
+    H, B = 3, len(lens)
+    pool = Pool([[]] * B, H, N, P, 2, "bf16" if dtype == "bf16" else "f32", rng, room=1 + max(lens) // S)
+    args, args64 = extend_inputs(rng, lens, H, 1, N, P, dtype)
+    s, c, s64, c64 = states(rng, B, H, N, P)
+    n, pos = [0] * B, [S // 2] * B
+    yr, sr, cr, *_ = ref.extend(*args64, lens, s64, c64, n, pos, S)
+    x, dt, A, Bm, Cm = args
+    b, h = B - 1, 1
+    at = lens[b] // 2 | 1          # odd: the second of two tokens that share a lane
+    t = sum(lens[:b]) + at
+    end = sum(lens)
+    touched = np.zeros((end, H, P), bool)
+    if what == "dt":
+        dt[t, h] = value
+        touched[t:, h] = True
+    elif what == "B":
+        Bm[t, 0, N // 2] = value
+        touched[t:] = True
+    else:
+        Cm[t, 0, N // 2] = value
+        touched[t] = True
+    got = dart.dart_ssd_extend(x, dt, A, Bm, Cm, cumulative(lens), s, c, pool.pages, pool.table, ints(*n), ints(*pos), S)
+    dart.dart_sync_status()
+    y = got["y"].cpu().double().numpy()
+    assert rel_err(np.where(touched, 0.0, y), np.where(touched, 0.0, yr)) <= TOL
+    assert not np.isfinite(y[touched]).any()
+    for key, want in (("state", sr), ("dH_cur", cr)):
+        v = got[key].cpu().double().numpy()
+        kept = np.ones_like(v, bool)
+        if what == "dt":
+            kept[b, h] = False
+        elif what == "B":
+            kept[b, :, N // 2] = False
+        assert rel_err(np.where(kept, v, 0.0), np.where(kept, want, 0.0)) <= TOL
+
+
+@pytest.mark.parametrize("N, P, dtype", [(128, 64, "bf16"), (64, 64, "bf16"), (128, 64, "f32"), (16, 16, "bf16")])
+@pytest.mark.parametrize("lens", [[70], [9]])
+def test_a_token_that_forgets_everything_leaves_earlier_ones_alone(N, P, dtype, lens):
+    """dt A of -1e30: what comes before it keeps its decays."""
+    rng = np.random.default_rng(3)
+    H, S, at = 2, 256, lens[0] // 2 | 1
+    pool = Pool([[]], H, N, P, 2, "bf16" if dtype == "bf16" else "f32", rng, room=1)
+    (x, dt, A, Bm, Cm), args64 = extend_inputs(rng, lens, H, 1, N, P, dtype)
+    s, c, s64, c64 = states(rng, 1, H, N, P)
+    yr = ref.extend(*args64, lens, s64, c64, [0], [0], S)[0]
+    dt[at] = 1e30
+    got = dart.dart_ssd_extend(x, dt, A, Bm, Cm, cumulative(lens), s, c, pool.pages, pool.table, ints(0), ints(0), S)
+    dart.dart_sync_status()
+    assert rel_err(got["y"][:at], yr[:at]) <= TOL
