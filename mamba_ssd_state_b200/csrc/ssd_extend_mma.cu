@@ -19,6 +19,12 @@
 // exponentials of differences of prefix sums that are kept as two floats (their
 // difference is good to 2^-24 as long as the block's |dt A| sum to less than 2^29).
 //
+// No token's value reaches an earlier token, whatever it is: a column of the Gram
+// matrix that a row does not see is 0 by selection, and where an x of the block is
+// not finite (0 times it is NaN) the rows are summed over what they see by CUDA
+// cores.  A state that is not finite gives y that are not finite, NaN where the
+// token-by-token kernel may have an infinity.
+//
 // A block of 256 threads owns PS columns of one (sequence, head): warp w holds 16
 // of them and N PS / 128 rows of H^T and D^T.  The partial sums of y meet in
 // shared memory, in a fixed order.  The next tokens' B, C and x are on their way
@@ -197,15 +203,17 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_extend_mma_kernel(ExtendArgs 
         __syncthreads();
         if (done > 0) finish(base - done, done, closed);
         // ---- the weighted x in three parts
+        bool odd = false;                                     // a value of it is not finite
         for (int i = tid; i < kTB * (PS / 2); i += kThreads) {
             const int r = i / (PS / 2), c = 2 * (i % (PS / 2));
             const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&s.x[buf][r][c]);
+            odd |= !(fabsf(__low2float(v)) < INFINITY && fabsf(__high2float(v)) < INFINITY);
             uint32_t part[3];
             split3(s.w[buf][r] * __low2float(v), s.w[buf][r] * __high2float(v), part);
 #pragma unroll
             for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t*>(&s.wx[k][r][c]) = part[k];
         }
-        __syncthreads();
+        odd = __syncthreads_or(odd);
         if (m2 > 0) fetch(next, m2, buf ^ 1);
         const int li = lane & 7, lm = lane >> 3;              // row and matrix of a ldmatrix address
         // ---- inside the block: 16 rows t by 32 columns s of the decayed Gram matrix, times x
@@ -226,41 +234,63 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_extend_mma_kernel(ExtendArgs 
                         mma(G[j + 1], ca, bb[2], bb[3]);
                     }
                 }
-                // decay; G[j][r] is row tt + g + 8 (r / 2), column ss + 8 j + 2 q + r % 2
-                uint32_t A3[3][2][4];
+                // the decayed G[j][r] of row tt + g + 8 (r / 2), column ss + 8 j + 2 q + r % 2; 0 where the row does not see it
+                auto decayed = [&](int j, int r) {
+                    const int t = tt + g + 8 * (r >> 1), c = ss + 8 * j + 2 * q + (r & 1);
+                    return c <= t && c < m ? exp2f((s.hi[buf][t] - s.hi[buf][c]) + (s.lo[buf][t] - s.lo[buf][c])) * s.dt[buf][c] * G[j][r] : 0.f;
+                };
+                float(*y)[PS + 4] = s.y[warp >> 2];
+                if (odd) {
+                    // 0 times a later token's infinity or NaN would reach earlier ones: only what a row sees is multiplied
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int r = 0; r < 4; r += 2) {
-                        float v[2];
-                        const int t = tt + g + 4 * r;
+                        for (int r = 0; r < 4; ++r) G[j][r] = decayed(j, r);
+#pragma unroll 1
+                    for (int p = 0; p < PS; ++p) {
+                        float u[2] = {0.f, 0.f};              // rows tt + g and tt + g + 8
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const int t = tt + g + 8 * (r >> 1), c = ss + 8 * j + 2 * q + (r & 1);
+                                if (c <= t) u[r >> 1] = fmaf(G[j][r], __bfloat162float(s.x[buf][c][p]), u[r >> 1]);
+                            }
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const int c = ss + 8 * j + 2 * q + i;
-                            v[i] = c <= t && c < m ? exp2f((s.hi[buf][t] - s.hi[buf][c]) + (s.lo[buf][t] - s.lo[buf][c])) * s.dt[buf][c] * G[j][r + i] : 0.f;
+                            u[i] += __shfl_xor_sync(0xffffffffu, u[i], 1);
+                            u[i] += __shfl_xor_sync(0xffffffffu, u[i], 2);
+                            if (q == 0) y[tt + g + 8 * i][p] = u[i];
                         }
-                        uint32_t part[3];
-                        split3(v[0], v[1], part);
-#pragma unroll
-                        for (int k = 0; k < 3; ++k) A3[k][j >> 1][(j & 1) * 2 + (r >> 1)] = part[k];
                     }
-                float Y[PS / 8][4] = {};
+                } else {
+                    uint32_t A3[3][2][4];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if (ss + 16 * k > tt + 15) continue;
-                    uint32_t xb[PS / 16][4];
+                    for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int j = 0; j < PS / 16; ++j) ldsm_t(smem_addr(&s.x[buf][ss + 16 * k + (lm & 1) * 8 + li][16 * j + (lm >> 1) * 8]), xb[j]);
+                        for (int r = 0; r < 4; r += 2) {
+                            uint32_t part[3];
+                            split3(decayed(j, r), decayed(j, r + 1), part);
 #pragma unroll
-                    for (int i = 0; i < 3; ++i)      // products of one part after the other: neighbours do not wait for each other
+                            for (int k = 0; k < 3; ++k) A3[k][j >> 1][(j & 1) * 2 + (r >> 1)] = part[k];
+                        }
+                    float Y[PS / 8][4] = {};
 #pragma unroll
-                        for (int j = 0; j < PS / 8; ++j) mma(Y[j], A3[i][k], xb[j >> 1][2 * (j & 1)], xb[j >> 1][2 * (j & 1) + 1]);
-                }
-                float(*y)[PS + 4] = s.y[warp >> 2];
+                    for (int k = 0; k < 2; ++k) {
+                        if (ss + 16 * k > tt + 15) continue;
+                        uint32_t xb[PS / 16][4];
 #pragma unroll
-                for (int j = 0; j < PS / 8; ++j) {
-                    *reinterpret_cast<float2*>(&y[tt + g][8 * j + 2 * q]) = make_float2(Y[j][0], Y[j][1]);
-                    *reinterpret_cast<float2*>(&y[tt + g + 8][8 * j + 2 * q]) = make_float2(Y[j][2], Y[j][3]);
+                        for (int j = 0; j < PS / 16; ++j) ldsm_t(smem_addr(&s.x[buf][ss + 16 * k + (lm & 1) * 8 + li][16 * j + (lm >> 1) * 8]), xb[j]);
+#pragma unroll
+                        for (int i = 0; i < 3; ++i)      // products of one part after the other: neighbours do not wait for each other
+#pragma unroll
+                            for (int j = 0; j < PS / 8; ++j) mma(Y[j], A3[i][k], xb[j >> 1][2 * (j & 1)], xb[j >> 1][2 * (j & 1) + 1]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < PS / 8; ++j) {
+                        *reinterpret_cast<float2*>(&y[tt + g][8 * j + 2 * q]) = make_float2(Y[j][0], Y[j][1]);
+                        *reinterpret_cast<float2*>(&y[tt + g + 8][8 * j + 2 * q]) = make_float2(Y[j][2], Y[j][3]);
+                    }
                 }
             }
         }

@@ -40,11 +40,11 @@ def test_a_scale_of_255_is_nan_for_every_token_that_sees_it(N, P, dtype, cache, 
 # ------------------------------------------------- tokens that are no numbers
 @pytest.mark.parametrize("N, P, dtype", [(128, 64, "bf16"), (64, 64, "bf16"), (128, 64, "f32"), (64, 64, "f32"), (16, 16, "bf16")])
 @pytest.mark.parametrize("lens, S", [([70], 64), ([70], 256), ([30, 45], 32), ([12, 40, 12], 48), ([9, 14], 256)])
-@pytest.mark.parametrize("what", ["dt", "B", "C"])
+@pytest.mark.parametrize("what", ["x", "dt", "B", "C", "x last"])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
 def test_a_token_that_is_not_finite_leaves_earlier_ones_alone(N, P, dtype, lens, S, what, value):
     """The recurrence is causal for every value, in runs of any length: what a token holds reaches its own output and
-    later ones, no earlier one and no other head."""
+    later ones, no earlier one, no other head and, of x, no other column."""
     rng = np.random.default_rng(sum(lens) + N)
     H, B = 3, len(lens)
     pool = Pool([[]] * B, H, N, P, 2, "bf16" if dtype == "bf16" else "f32", rng, room=1 + max(lens) // S)
@@ -53,12 +53,15 @@ def test_a_token_that_is_not_finite_leaves_earlier_ones_alone(N, P, dtype, lens,
     n, pos = [0] * B, [S // 2] * B
     yr, sr, cr, *_ = ref.extend(*args64, lens, s64, c64, n, pos, S)
     x, dt, A, Bm, Cm = args
-    b, h = B - 1, 1
-    at = lens[b] // 2 | 1          # odd: the second of two tokens that share a lane
+    b, h, p = B - 1, 1, P - 3
+    at = lens[b] - 1 if what == "x last" else lens[b] // 2 | 1          # odd: the second of two tokens that share a lane
     t = sum(lens[:b]) + at
     end = sum(lens)
     touched = np.zeros((end, H, P), bool)
-    if what == "dt":
+    if what in ("x", "x last"):
+        x[t, h, p] = value
+        touched[t:, h, p] = True
+    elif what == "dt":
         dt[t, h] = value
         touched[t:, h] = True
     elif what == "B":
@@ -75,7 +78,9 @@ def test_a_token_that_is_not_finite_leaves_earlier_ones_alone(N, P, dtype, lens,
     for key, want in (("state", sr), ("dH_cur", cr)):
         v = got[key].cpu().double().numpy()
         kept = np.ones_like(v, bool)
-        if what == "dt":
+        if what in ("x", "x last"):
+            kept[b, h, :, p] = False
+        elif what == "dt":
             kept[b, h] = False
         elif what == "B":
             kept[b, :, N // 2] = False
