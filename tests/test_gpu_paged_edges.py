@@ -101,3 +101,33 @@ def test_a_token_that_forgets_everything_leaves_earlier_ones_alone(N, P, dtype, 
     got = dart.dart_ssd_extend(x, dt, A, Bm, Cm, cumulative(lens), s, c, pool.pages, pool.table, ints(0), ints(0), S)
     dart.dart_sync_status()
     assert rel_err(got["y"][:at], yr[:at]) <= TOL
+
+
+# ------------------------------------------------- calls that are refused
+def test_a_layer_call_that_is_refused_changes_nothing():
+    """layer_extend is two operators; whatever the second one refuses is refused before the first one runs."""
+    rng = np.random.default_rng(5)
+    H, N, P, S, lens = 2, 64, 64, 4, [3, 2]
+    pool = Pool([[], []], H, N, P, 2, "bf16", rng, room=2)
+    (x, dt, A, Bm, Cm), _ = extend_inputs(rng, lens, H, 1, N, P, "bf16")
+    (Q, E, _), _ = attention_inputs(rng, 5, H, 1, N, P, "bf16")
+    s, c, _, _ = states(rng, 2, H, N, P)
+    n, pos = ints(0, 1), ints(2, 3)
+    before = [v.clone() for v in (s, c, pool.pages.view(torch.int16), n, pos)]
+    odd = lambda v: torch.cat((v.new_zeros(1), v.flatten()))[1:].reshape(v.shape)      # contiguous, at an address of its own
+    ok = dict(x=x, dt=dt, A=A, Bm=Bm, Cm=Cm, Q=Q, E=E, g=0.5, cu_tokens=cumulative(lens), state=s, dH_cur=c, pages=pool.pages,
+              table=pool.table, nchunks=n, pos=pos, chunk=S)
+    T = 16400                                          # more than an attention call takes
+    (x2, dt2, _, B2, C2), _ = extend_inputs(rng, [T], H, 1, N, P, "bf16")
+    many = dict(x=x2, dt=dt2, Bm=B2, Cm=C2, Q=torch.zeros((T, H, N), dtype=torch.bfloat16, device="cuda"),
+                E=torch.zeros((T, H, P), dtype=torch.bfloat16, device="cuda"))
+    for kw in (dict(Q=Q.float()), dict(E=E.float()), dict(Q=Q[:4]), dict(E=E[:4]), dict(Q=Q[..., :32].contiguous()), dict(E=E[:, :1]),
+               dict(E=E[..., :32]), dict(Q=odd(Q)), dict(E=odd(E)), dict(g="half"), dict(Q=Q[:, :1]), dict(Q=Q[0]), dict(E=E[0, 0]), many):
+        with pytest.raises((TypeError, ValueError, dart.DartError)):
+            dart.layer_extend(**{**ok, **kw})
+        dart.dart_sync_status()
+        for was, v in zip(before, (s, c, pool.pages.view(torch.int16), n, pos)):
+            assert torch.equal(was, v)
+    dart.layer_extend(**ok)
+    dart.dart_sync_status()
+    assert not torch.equal(before[0], s)
