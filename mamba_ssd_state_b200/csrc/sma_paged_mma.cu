@@ -26,7 +26,9 @@
 // float32 inputs are split into a high and a low float16 half (22 bits).
 // A block of 32 codes is two k steps: their product is multiplied by the block's
 // scale in float32 before it is added, so a scale costs 4 multiply-adds for
-// every 2 products and no bit.
+// every 2 products and no bit.  That holds for scale bytes 1 .. 192 (values of up
+// to 2^67); a piece that meets another one is done again on CUDA cores, about 10
+// (one token) to 35 times (six) as slow, for the whole range of the format.
 #include <cuda_fp16.h>
 #include <float.h>
 #include <limits.h>
@@ -124,6 +126,13 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// The power of two that a column of float16 operands is multiplied by: its largest
+// value goes to [2^14, 2^15); one that is not finite stays as it is.
+__device__ __forceinline__ int column_exponent(float amax) {
+    const int e = (int)(__float_as_uint(amax) >> 23);      // biased exponent, 0 for 0 and subnormals
+    return amax > 0.f && e < 255 ? min(max(14 - (e - 127), -126), 126) : 0;
+}
+
 // A lane's columns of B: PARTS float16 halves (or bfloat16 as it is) of N / 16
 // k steps.  Slots 2q, 2q+1, 2q+8, 2q+9 of k step i stand for rows
 // 16i + 4q + {0,1,2,3} with codes, and for 16i + {2q, 2q+1, 2q+8, 2q+9} else
@@ -181,9 +190,7 @@ struct Column {
         if constexpr (M::kFp4) {
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // largest value to [2^14, 2^15); a row that is not finite stays as it is
-            const int e = (int)(__float_as_uint(amax) >> 23);      // biased exponent, 0 for 0 and subnormals
-            if (amax > 0.f && e < 255) scale = mxfp4_pow2(min(max(14 - (e - 127), -126), 126));
+            scale = mxfp4_pow2(column_exponent(amax));
         }
 #pragma unroll
         for (int i = 0; i < N / 16; ++i) {
@@ -209,10 +216,10 @@ struct Column {
     }
 };
 
-// acc[t][m] += (piece of a memory in `stage`)^T times the columns.  Returns
-// whether this lane's rows of it are free of NaN blocks (bfloat16 carries its own).
+// acc[t][m] += (piece of a memory in `stage`)^T times the columns; scale bytes are
+// ordinary ones (or what comes out is not used).
 template <typename M, int N, int NT, int PARTS, int PIECE>
-__device__ __forceinline__ bool multiply(const uint8_t* stage, const Column<M, N, PARTS> (&col)[NT], float (&acc)[NT][4][4]) {
+__device__ __forceinline__ void multiply(const uint8_t* stage, const Column<M, N, PARTS> (&col)[NT], float (&acc)[NT][4][4]) {
     const int lane = threadIdx.x & 31;
     if constexpr (!M::kFp4) {
         const int mi = lane >> 3, r = lane & 7;
@@ -227,14 +234,12 @@ __device__ __forceinline__ bool multiply(const uint8_t* stage, const Column<M, N
                 for (int t = 0; t < NT; ++t) mma_bf16(acc[t][m], a, col[t].b[0][PIECE * (M::kRows / 16) + i]);
             }
         }
-        return true;
     } else {
         // Products that do not wait for each other stand together: MG groups of 16
         // columns of the memory, as many as the registers take.
         constexpr int K = N / 32, MG = NT == 1 ? 4 : 2;
         const int g = lane >> 2, q = lane & 3;
         const uint8_t* scales = stage + M::kCodeBytes;
-        uint32_t nan = 0;
 #pragma unroll
         for (int m0 = 0; m0 < 4; m0 += MG) {
             uint32_t w[MG][2][K], sc[MG][2];       // code words and scale bytes of two rows of a group
@@ -252,7 +257,6 @@ __device__ __forceinline__ bool multiply(const uint8_t* stage, const Column<M, N
                         w[m][r][0] = u.x; w[m][r][1] = u.y;
                         sc[m][r] = *reinterpret_cast<const uint16_t*>(scales + p * 2);
                     }
-                    nan |= __vcmpeq4(sc[m][r], 0xffffffffu);
                 }
 #pragma unroll
             for (int k = 0; k < K; ++k) {
@@ -285,7 +289,7 @@ __device__ __forceinline__ bool multiply(const uint8_t* stage, const Column<M, N
                 }
 #pragma unroll
                 for (int m = 0; m < MG; ++m) {
-                    // 2^(s - 127) of the two rows (2^-127 counts as 0)
+                    // 2^(s - 127) of the two rows
                     const float s0 = __uint_as_float((k < 3 ? sc[m][0] << (23 - 8 * k) : sc[m][0] >> 1) & 0x7f800000u);
                     const float s1 = __uint_as_float((k < 3 ? sc[m][1] << (23 - 8 * k) : sc[m][1] >> 1) & 0x7f800000u);
 #pragma unroll
@@ -298,7 +302,98 @@ __device__ __forceinline__ bool multiply(const uint8_t* stage, const Column<M, N
                 }
             }
         }
-        return nan == 0;
+    }
+}
+
+// Not 0 where one of the scale bytes that this lane looks at is no ordinary one, 1 .. 192:
+// scaled columns times larger ones may overflow where the true sums do not, and 0 and 255
+// do not stand for the exponents that multiply() takes them for.  (A look at every word
+// where it is multiplied by, and the products anew on the spot, cost up to 4%; this costs
+// less than the look for 255 alone did: drafts 131 -> 125 us.)
+template <typename M>
+__device__ __forceinline__ uint32_t odd_scales(const uint8_t* stage) {
+    constexpr int kWords = M::kScaleBytes / 128;             // of a lane
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(stage + M::kCodeBytes) + (threadIdx.x & 31) * kWords;
+    uint32_t odd = 0;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+        const uint32_t less = words[i] - 0x01010101u;        // its bytes' upper two bits are set from 193 on, and where 0 borrows
+        odd |= less & less << 1;
+    }
+    return odd & 0x80808080u;
+}
+
+// A piece whose memories hold scale bytes that are not ordinary, anew: token by token on
+// CUDA cores, from the pages, a lane with the columns `lane` and `lane + 32`.  A block's
+// product meets the powers of two of its scale and of its row of Q or C in one step, so
+// that nothing overflows or vanishes on the way that does not in the sum.  Not inlined: its
+// registers would be the products'.
+template <typename T, typename M, int N, int TT>
+__device__ __noinline__ void run_piece_any_scale(const SmaPagedArgs& a, const int* table, int t0, int rows, int h, int first, int last,
+                                                 int bad, bool whole, int run, int which) {
+    constexpr int K = N / 32;
+    const int lane = threadIdx.x & 31, grp = group_of(h, a.H, a.G);
+    for (int t = 0; t < rows; ++t) {
+        const size_t tok = (size_t)(t0 + t);
+        const T* src[2] = {static_cast<const T*>(a.Q) + (tok * a.H + h) * N, static_cast<const T*>(a.Cm) + (tok * a.G + grp) * N};
+        float pre[2], e[2];
+        int exponent[2];
+        for (int i = 0; i < 2; ++i) {
+            float amax = 0.f;
+            for (int n = 0; n < N; ++n) amax = fmaxf(amax, fabsf(ldf(src[i] + n)));
+            exponent[i] = column_exponent(amax);
+            pre[i] = mxfp4_pow2(exponent[i]);
+            e[i] = ldf(static_cast<const T*>(a.E) + (tok * a.H + h) * kP + lane + 32 * i);
+        }
+        const int count = a.mem_count[tok];
+        float m = -FLT_MAX, l = 0.f, o[2] = {0.f, 0.f};
+        for (int c = first; c < min(last, count); ++c) {
+            const size_t mem = memory_index(a.cache, a.H, table[c / a.cache.R], h, c % a.cache.R);
+            const uint32_t* codes = static_cast<const uint32_t*>(a.cache.pages) + mem * (M::kCodeBytes / 4);
+            const uint8_t* scales = a.cache.scales + mem * M::kScaleBytes;
+            float uv[2][2] = {};                              // of Q and C, of the two columns
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int p = lane + 32 * j;
+#pragma unroll 1
+                for (int k = 0; k < K; ++k) {
+                    float d[2] = {0.f, 0.f};
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t w[4];
+                        widen_codes(codes[p * (N / 8) + q * K + k], w);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&w[i / 2]));
+                            const int n = 32 * k + 16 * (i / 4) + 4 * q + i % 4;
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) d[r] = fmaf(i & 1 ? two.y : two.x, ldf(src[r] + n) * pre[r], d[r]);
+                        }
+                    }
+                    const int s = scales[p * K + k];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) uv[r][j] += s == 255 ? __int_as_float(0x7fffffff) : ldexpf(d[r], s - 127 - exponent[r]);
+                }
+            }
+            const float sc = warp_sum(fmaf(uv[0][0], e[0], uv[0][1] * e[1])) * (kLog2e * rsqrtf((float)N));
+            const float mn = fmaxf(m, sc), f = exp2f(m - mn), wt = exp2f(sc - mn);
+            l = fmaf(l, f, wt);
+            m = mn;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) o[j] = wt != 0.f ? fmaf(o[j], f, wt * uv[1][j]) : o[j];
+        }
+        const bool left = count < 0 || count > bad;           // a row that is not to be computed
+        if (!whole) {
+            float* row = piece_rows<TT, kP>(a.part, run, which) + t * (kP + 4);
+            if (lane == 0) { row[kP] = m; row[kP + 1] = left ? -1.f : l; }
+            row[lane] = o[0];
+            row[lane + 32] = o[1];
+        } else if (!left) {
+            const size_t at = (tok * a.H + h) * kP + lane;
+            const float f = l == 0.f ? 0.f : (a.y_ssd ? a.g : 1.f) / l;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) a.out[at + 32 * j] = fmaf(f, o[j], a.y_ssd ? a.y_ssd[at + 32 * j] : 0.f);
+        }
     }
 }
 
@@ -346,7 +441,8 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const W
             vs[j] = 1.f / __shfl_sync(0xffffffffu, scale[NT - 1], 4 * ((NT == 2 ? 0 : 4) + tk + j));
         }
     }
-    const int bad = readable_memories(a.cache.table + (size_t)s.tiles.seq(w.k) * a.cache.width, a.cache, w.first_memory(), w.last_memory());
+    const int* table = a.cache.table + (size_t)s.tiles.seq(w.k) * a.cache.width;
+    const int bad = readable_memories(table, a.cache, w.first_memory(), w.last_memory());
     int fewest = INT_MAX; // memories that every row of the tile sees (rows that are not to be computed apart)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -364,6 +460,7 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const W
 #pragma unroll
         for (int r = 0; r < 4; ++r) o[m][r] = 0.f;
 
+    uint32_t odd = 0;     // 4-bit: scale bytes that the products below are not made for
     const int last = min(w.last_memory(), bad);
     for (int c = w.first_memory(); c < last; ++c) {
         float acc[NT][4][4];
@@ -373,7 +470,6 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const W
             for (int m = 0; m < 4; ++m)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[t][m][r] = 0.f;
-        bool clean = true;
         auto take = [&](auto piece) {
             const int st = taken % M::kStages;
             const uint32_t bar = smem_u32(&s.full[warp][st]), phase = (uint32_t)(taken / M::kStages) & 1u;
@@ -381,7 +477,8 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const W
             if (ok) ok = M::kFp4 ? wait_warp(bar, phase, wc, 1) : mbar_wait_warp(bar, phase, wc, 1);
             ++taken;
             if (!ok) return;
-            clean &= multiply<M, N, NT, PARTS, decltype(piece)::value>(s.ring[warp][st], col, acc);
+            if constexpr (M::kFp4) odd |= odd_scales<M>(s.ring[warp][st]);
+            multiply<M, N, NT, PARTS, decltype(piece)::value>(s.ring[warp][st], col, acc);
             __syncwarp();        // every lane has read the stage
             feed.fill(prm, s.tiles, s.ring[warp], s.full[warp]);
         };
@@ -393,7 +490,6 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const W
             v[j] = 0.f;
 #pragma unroll
             for (int m = 0; m < 4; ++m) v[j] = fmaf(acc[0][m][j], e[m][j], fmaf(acc[0][m][2 + j], e[m][2 + j], v[j]));
-            if (!clean) v[j] = __int_as_float(0x7fffffff);      // for both tokens: the lanes part them next
         }
         float sc = (mine ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, mine ? v[0] : v[1], 4);
         sc += __shfl_xor_sync(0xffffffffu, sc, 8);
@@ -437,6 +533,12 @@ __device__ __forceinline__ void run_piece(const Params& prm, Smem<M>& s, const W
     const bool whole = w.whole();
     const int which = w.c > 0 ? 0 : 1;
     if (!whole && lane == 0) *piece_header(a.part, run, which) = PieceHeader{w.last == w.units ? 2 : 1, t0, rows, w.h};
+    if constexpr (M::kFp4) {
+        if (__any_sync(0xffffffffu, odd != 0)) {
+            run_piece_any_scale<T, M, N, TT>(a, table, t0, rows, w.h, w.first_memory(), last, bad, whole, run, which);
+            return;
+        }
+    }
     if (NT == 1 && q < 2) return;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {

@@ -7,7 +7,7 @@ import torch
 from mamba_ssd_state_b200 import dart
 from tests import paged_reference as ref
 from tests.parity import rel_err
-from tests.test_gpu_paged import SHAPES, TOL, Pool, attention_inputs, cumulative, extend_inputs, ints, memories_of, states
+from tests.test_gpu_paged import SHAPES, TOL, Pool, attention_inputs, cast, cumulative, extend_inputs, ints, memories_of, states
 
 pytestmark = pytest.mark.gpu
 FOUR_BIT = [v for v in SHAPES if v[3] == "mxfp4"]
@@ -35,6 +35,64 @@ def test_a_scale_of_255_is_nan_for_every_token_that_sees_it(N, P, dtype, cache, 
         want = ref.sma(*args64, lens, memories, [3] * T)
         assert torch.isnan(out[torch.from_numpy(see).cuda()]).all()
         assert rel_err(out[torch.from_numpy(~see).cuda()], want[~see]) <= TOL if (~see).any() else True
+
+
+# --------------------------------------------------- the range of the scales
+@pytest.mark.parametrize("N, P, dtype, cache, H, G", FOUR_BIT)
+@pytest.mark.parametrize("lens", [[1], [3], [8], [2, 6]])
+@pytest.mark.parametrize("low, high, q, c", [(0, 0, 125, 90), (0, 3, 124, 100), (222, 228, -101, -80), (240, 250, -122, -112),
+                                             (250, 252, -124, -115)])
+def test_attention_over_the_whole_range_of_scale_bytes(N, P, dtype, cache, H, G, lens, low, high, q, c):
+    """Scale bytes at both ends of what float32 holds, and tokens that bring scores and values back to ordinary size."""
+    rng = np.random.default_rng(low + sum(lens))
+    pool = Pool(memories_of(rng, [7] * len(lens), H, N, P, cache, scale=0.5), H, N, P, 3, cache, rng)
+    held = []
+    for b in range(len(lens)):
+        for m in range(7):
+            scales = rng.integers(low, high + 1, (H, P, N // 32)).astype(np.uint8)
+            pool.scales[pool.table_np[b, m // 3], :, m % 3] = torch.from_numpy(scales).cuda()
+        held.append(np.stack([pool.memory(b, m) for m in range(7)]))
+    T = sum(lens)
+    Q, Q64 = cast(rng.standard_normal((T, H, N)) * 2.0 ** q, dtype)
+    E, E64 = cast(rng.standard_normal((T, H, P)) / np.sqrt(P), dtype)
+    C, C64 = cast(rng.standard_normal((T, G, N)) * 2.0 ** c, dtype)
+    counts = [7 - (t % 3) for t in range(T)]
+    want = ref.sma(Q64, E64, C64, lens, held, counts)
+    out = dart.dart_sma_paged(Q, E, C, cumulative(lens), pool.pages, pool.table, ints(*counts), 1.0, scales=pool.scales)
+    dart.dart_sync_status()
+    # TOL counts for scores of up to 12, whose error goes with their size
+    ends = np.cumsum([0] + lens)
+    size = max(np.abs(np.einsum("thn,mhnp,thp->thm", Q64[a:e], m, E64[a:e])).max() / np.sqrt(N)
+               for m, a, e in zip(held, ends[:-1], ends[1:]))
+    assert rel_err(out, want) <= TOL * max(1.0, size / 12)
+
+
+@pytest.mark.parametrize("N, P, dtype, cache, H, G", FOUR_BIT)
+def test_many_sequences_over_scales_of_all_kinds(N, P, dtype, cache, H, G):
+    """Items that one worker does whole, with and without y_ssd; the last memory's blocks are NaN."""
+    rng = np.random.default_rng(31)
+    B = 1200
+    lens = [int(v) for v in rng.integers(0, 4, B)]
+    T = sum(lens)
+    pool = Pool(memories_of(rng, [4], H, N, P, cache, scale=0.5), H, N, P, 2, cache, rng)
+    for m in range(3):
+        scales = rng.integers(220, 228, (H, P, N // 32)).astype(np.uint8)
+        pool.scales[pool.table_np[0, m // 2], :, m % 2] = torch.from_numpy(scales).cuda()
+    pool.scales[pool.table_np[0, 1], :, 1, ::2] = 255
+    held = np.stack([pool.memory(0, m) for m in range(3)])
+    pool.table = pool.table.expand(B, 2).contiguous()             # all read the same pages
+    Q, Q64 = cast(rng.standard_normal((T, H, N)) * 2.0 ** -100, dtype)
+    E, E64 = cast(rng.standard_normal((T, H, P)) / np.sqrt(P), dtype)
+    C, C64 = cast(rng.standard_normal((T, G, N)) * 2.0 ** -104, dtype)
+    y, y64 = cast(rng.standard_normal((T, H, P)), "f32")
+    counts = rng.integers(0, 5, T)
+    o = ref.sma(Q64, E64, C64, lens, [held] * B, np.minimum(counts, 3).tolist())
+    out = dart.dart_sma_paged(Q, E, C, cumulative(lens), pool.pages, pool.table, ints(*counts.tolist()), 0.5, y, scales=pool.scales)
+    bare = dart.dart_sma_paged(Q, E, C, cumulative(lens), pool.pages, pool.table, ints(*counts.tolist()), 0.5, scales=pool.scales)
+    dart.dart_sync_status()
+    fine = torch.from_numpy(counts < 4).cuda()
+    assert torch.isnan(out[~fine]).all() and torch.isnan(bare[~fine]).all()
+    assert rel_err(out[fine], (y64 + 0.5 * o)[counts < 4]) <= TOL and rel_err(bare[fine], o[counts < 4]) <= TOL
 
 
 # ------------------------------------------------- tokens that are no numbers
