@@ -409,6 +409,11 @@ dart_status dart_decode_step_noalloc(const dart_dims* dims, dart_dtype dtype,
  * pos) need 4-byte alignment only, so that a sequence's row of a table can be
  * passed by itself; all other tensors 16 bytes, as everywhere.
  *
+ * Results have memory of their own: a call whose result overlaps one of its
+ * inputs, another result or its workspace is refused, but for an update in
+ * place that the call allows.  (dart_cache_write_paged and dart_cache_read_paged
+ * may have dH in the pool itself, apart from the memories that are written.)
+ *
  * Errors the device finds (a range, counter, count or page that is out of
  * bounds) are latched as DART_ERR_DEVICE; the sequence, or the row, that they
  * concern is left as it is and the others are computed.
@@ -456,14 +461,14 @@ dart_status dart_cache_read_paged(const dart_dims* dims, dart_dtype dtype, const
  * cache's format) and restarts at 0.
  *   x[T,H,P], Bm[T,G,N], Cm[T,G,N]: dtype; dt[T,H], A[H]: float.
  *   state, dH_cur: float [B,H,N,P], H and D before the run; state_out,
- *   dH_cur_out: after it.  The same pointers update in place; others must not
- *   overlap the inputs, which then keep the state a caller can go back to when
- *   some of the tokens (drafts) turn out not to be wanted.
+ *   dH_cur_out: after it.  The same pointers update in place; with others the
+ *   inputs keep the state a caller can go back to when some of the tokens
+ *   (drafts) turn out not to be wanted.
  *   n_chunks, pos: int32 [B], memories finished and tokens into the chunk, before
- *   the run; n_chunks_out, pos_out: after it, in memory of their own.
- *   y: float [T,H,P], apart from the inputs.  mem_count: int32 [T], the number of memories each token may
- *   attend to (those finished before it), -1 for the tokens of a sequence that
- *   was left as it is; dart_sma_paged's argument of that name.
+ *   the run; n_chunks_out, pos_out: after it.
+ *   y: float [T,H,P].  mem_count: int32 [T], the number of memories each token
+ *   may attend to (those finished before it), -1 for the tokens of a sequence
+ *   that was left as it is; dart_sma_paged's argument of that name.
  * A token sees a finished chunk only through its memory, so the pages must have
  * room for n_chunks + (pos + tokens) / S memories.  One kernel.
  */
@@ -483,7 +488,7 @@ size_t dart_sma_paged_workspace_bytes(const dart_dims* dims);
  * sequence's first mem_count[t] memories,
  *   out = y_ssd + g * o  (y_ssd != NULL), else out = o;  o = 0 with none to see.
  *   Q[T,H,N], E[T,H,P], Cm[T,G,N]: dtype; y_ssd: nullable float [T,H,P]; out:
- *   float [T,H,P], y_ssd itself or not overlapping it, and apart from Q, E and Cm.
+ *   float [T,H,P], y_ssd itself or apart from it.
  *   mem_count: int32 [T]; -1 marks a row that is left as it is.
  *   workspace: dart_sma_paged_workspace_bytes(), 16-byte aligned, contents on
  *   entry do not matter; calls that may overlap on the GPU need one each.

@@ -94,9 +94,32 @@ dart_status check_common(const dart_dims* d, dart_dtype dt, bool need_seqlen) {
     return DART_OK;
 }
 
-bool overlap(const void* p, size_t pbytes, const void* q, size_t qbytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return a < b + qbytes && b < a + pbytes;
+// A tensor of a call, for the check that results have memory of their own: blocks read
+// their inputs at their own time, while others write.
+struct Span {
+    const char* name;
+    const void* p;
+    size_t bytes;
+    int onto = -1;     // of a result: the input that it may also lie right on
+};
+
+bool overlap(const Span& a, const Span& b) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
+    return a.bytes && b.bytes && p < q + b.bytes && q < p + a.bytes;
+}
+
+// No result on an input or on another result.
+template <int R, int I>
+dart_status check_apart(const char* call, const Span (&results)[R], const Span (&inputs)[I]) {
+    for (int i = 0; i < R; ++i) {
+        for (int j = 0; j < I; ++j)
+            if (overlap(results[i], inputs[j]) && !(j == results[i].onto && inputs[j].p == results[i].p))
+                return fail(DART_ERR_INVALID_ARG, "%s: %s overlaps %s", call, results[i].name, inputs[j].name);
+        for (int j = i + 1; j < R; ++j)
+            if (overlap(results[i], results[j]))
+                return fail(DART_ERR_INVALID_ARG, "%s: %s overlaps %s", call, results[i].name, results[j].name);
+    }
+    return DART_OK;
 }
 
 // The paged cache's own fields, and the memory shape it is asked to hold.
@@ -119,6 +142,17 @@ dart_status check_paged(const char* call, const dart_dims* d, const dart_paged_c
     if (mxfp4) DART_REQUIRE_PTR(scales);
     *out = dart::PagedCache{mxfp4, c->npages, c->page_size, c->table_width, c->pages, c->scales, c->table};
     return DART_OK;
+}
+
+Span pages_span(const dart_dims* d, dart_dtype dtype, const dart::PagedCache& c) {
+    const size_t values = (size_t)c.npages * c.R * d->nheads * d->dstate * d->headdim;
+    return {"pages", c.pages, c.mxfp4 ? values / 2 : values * (dtype == DART_F32 ? 4 : 2)};
+}
+Span scales_span(const dart_dims* d, const dart::PagedCache& c) {
+    return {"scales", c.scales, c.mxfp4 ? (size_t)c.npages * c.R * d->nheads * d->dstate * d->headdim / 32 : 0};
+}
+Span table_span(const dart_dims* d, const dart::PagedCache& c) {
+    return {"table", c.table, (size_t)d->batch * c.width * sizeof(int)};
 }
 
 }  // namespace
@@ -493,6 +527,11 @@ static dart_status cache_copy(const char* call, bool write, const dart_dims* d, 
     DART_REQUIRE_PTR(dH); DART_REQUIRE_INTS(first); DART_REQUIRE_INTS(count);
     a.B = d->batch; a.C = nmem; a.H = d->nheads; a.P = d->headdim; a.N = d->dstate;
     a.dH = dH; a.first = first; a.count = count; a.status = status_word();
+    const size_t ints = (size_t)d->batch * sizeof(int);
+    const Span in[3] = {{"first", first, ints}, {"count", count, ints}, table_span(d, a.cache)};
+    const Span dense = {"dH", dH, (size_t)d->batch * d->nheads * nmem * d->dstate * d->headdim * (dtype == DART_F32 ? 4 : 2)};
+    const Span to_pages[2] = {pages_span(d, dtype, a.cache), scales_span(d, a.cache)}, to_dense[1] = {dense};
+    if ((st = write ? check_apart(call, to_pages, in) : check_apart(call, to_dense, in)) != DART_OK) return st;
     if (!a.status) return fail(DART_ERR_CUDA, "%s: no device status word", call);
     cudaError_t e = write ? dart::launch_cache_write(a, dtype, static_cast<cudaStream_t>(stream))
                           : dart::launch_cache_read(a, dtype, static_cast<cudaStream_t>(stream));
@@ -527,26 +566,15 @@ dart_status dart_ssd_extend(const dart_dims* d, dart_dtype dtype, const void* x,
     DART_REQUIRE_PTR(A); DART_REQUIRE_INTS(cu_tokens); DART_REQUIRE_PTR(state); DART_REQUIRE_PTR(state_out);
     DART_REQUIRE_PTR(dH_cur); DART_REQUIRE_PTR(dH_cur_out); DART_REQUIRE_INTS(n_chunks); DART_REQUIRE_INTS(pos);
     DART_REQUIRE_INTS(n_chunks_out); DART_REQUIRE_INTS(pos_out);
-    // The blocks of a sequence read its counters at their own time: the new ones go elsewhere.
-    const int* in[2] = {n_chunks, pos};
-    const int* out[2] = {n_chunks_out, pos_out};
-    for (const int* i : in)
-        for (const int* o : out)
-            if (i < o + d->batch && o < i + d->batch)
-                return fail(DART_ERR_INVALID_ARG, "dart_ssd_extend: n_chunks_out and pos_out overlap n_chunks or pos");
-    const size_t floats = (size_t)d->batch * d->nheads * d->dstate * d->headdim;
-    const float* from[2] = {state, dH_cur};
-    const float* to[2] = {state_out, dH_cur_out};
-    for (int i = 0; i < 2; ++i)
-        for (int j = 0; j < 2; ++j)
-            if ((i != j || from[i] != to[j]) && from[i] < to[j] + floats && to[j] < from[i] + floats)
-                return fail(DART_ERR_INVALID_ARG,
-                            "dart_ssd_extend: state_out and dH_cur_out are their inputs or apart from both");
-    // Blocks read the tokens at their own time, while others write y.
-    const size_t T = d->seqlen, item = dtype == DART_F32 ? 4 : 2, yb = T * d->nheads * d->headdim * 4;
-    const size_t xb = T * d->nheads * d->headdim * item, bc = T * d->ngroups * d->dstate * item;
-    if (T > 0 && (overlap(y, yb, x, xb) || overlap(y, yb, Bm, bc) || overlap(y, yb, Cm, bc) || overlap(y, yb, dt, T * d->nheads * 4)))
-        return fail(DART_ERR_INVALID_ARG, "dart_ssd_extend: y overlaps x, dt, Bm or Cm");
+    const size_t T = d->seqlen, H = d->nheads, item = dtype == DART_F32 ? 4 : 2, ints = (size_t)d->batch * sizeof(int);
+    const size_t tokens = T * H * d->headdim, bc = T * d->ngroups * d->dstate * item, matrices = d->batch * H * d->dstate * d->headdim * 4;
+    const Span in[11] = {{"x", x, tokens * item}, {"dt", dt, T * H * 4}, {"A", A, H * 4}, {"Bm", Bm, bc}, {"Cm", Cm, bc},
+                         {"cu_tokens", cu_tokens, ints + sizeof(int)}, {"state", state, matrices}, {"dH_cur", dH_cur, matrices},
+                         {"n_chunks", n_chunks, ints}, {"pos", pos, ints}, table_span(d, a.cache)};
+    const Span out[8] = {{"y", y, tokens * 4}, {"mem_count", mem_count, T * sizeof(int)}, {"n_chunks_out", n_chunks_out, ints},
+                         {"pos_out", pos_out, ints}, {"state_out", state_out, matrices, 6}, {"dH_cur_out", dH_cur_out, matrices, 7},
+                         pages_span(d, dtype, a.cache), scales_span(d, a.cache)};
+    if ((st = check_apart("dart_ssd_extend", out, in)) != DART_OK) return st;
     a.B = d->batch; a.T = d->seqlen; a.H = d->nheads; a.P = d->headdim; a.N = d->dstate; a.S = d->chunk; a.G = d->ngroups;
     a.x = x; a.dt = dt; a.A = A; a.Bm = Bm; a.Cm = Cm; a.cu = cu_tokens;
     a.state = state; a.state_out = state_out; a.cur = dH_cur; a.cur_out = dH_cur_out;
@@ -574,22 +602,18 @@ dart_status dart_sma_paged(const dart_dims* d, dart_dtype dtype, const void* Q, 
     if (d->seqlen == 0) return DART_OK;
     DART_REQUIRE_PTR(Q); DART_REQUIRE_PTR(E); DART_REQUIRE_PTR(Cm); DART_REQUIRE_INTS(cu_tokens);
     DART_REQUIRE_INTS(mem_count); DART_OPTIONAL_PTR(y_ssd); DART_REQUIRE_PTR(out); DART_REQUIRE_PTR(workspace);
-    if (y_ssd && y_ssd != out) {
-        const size_t floats = (size_t)d->seqlen * d->nheads * d->headdim;
-        if (y_ssd < out + floats && out < y_ssd + floats)
-            return fail(DART_ERR_INVALID_ARG, "dart_sma_paged: out overlaps y_ssd without being the same pointer");
-    }
     if (dart::sma_paged_tiles(d->batch, d->seqlen) > dart::sma_paged_max_tiles())
         return fail(DART_ERR_UNSUPPORTED, "dart_sma_paged: %d sequences and %d tokens are too many for one call "
                     "(batch + seqlen / 4 must be <= %lld)", d->batch, d->seqlen, dart::sma_paged_max_tiles());
     const size_t need = dart_sma_paged_workspace_bytes(d);
     if (workspace_bytes < need)
         return fail(DART_ERR_INVALID_ARG, "workspace: %zu bytes, need %zu", workspace_bytes, need);
-    // Workers read the tokens at their own time, while others write out.
-    const size_t T = d->seqlen, item = dtype == DART_F32 ? 4 : 2, ob = T * d->nheads * d->headdim * 4;
-    if (overlap(out, ob, Q, T * d->nheads * d->dstate * item) || overlap(out, ob, E, T * d->nheads * d->headdim * item) ||
-        overlap(out, ob, Cm, T * d->ngroups * d->dstate * item))
-        return fail(DART_ERR_INVALID_ARG, "dart_sma_paged: out overlaps Q, E or Cm");
+    const size_t T = d->seqlen, item = dtype == DART_F32 ? 4 : 2, tokens = T * d->nheads * d->headdim;
+    const Span in[9] = {{"Q", Q, T * d->nheads * d->dstate * item}, {"E", E, tokens * item}, {"Cm", Cm, T * d->ngroups * d->dstate * item},
+                        {"y_ssd", y_ssd, y_ssd ? tokens * 4 : 0}, {"cu_tokens", cu_tokens, (d->batch + (size_t)1) * sizeof(int)},
+                        {"mem_count", mem_count, T * sizeof(int)}, table_span(d, a.cache), pages_span(d, dtype, a.cache), scales_span(d, a.cache)};
+    const Span results[2] = {{"out", out, tokens * 4, 3}, {"workspace", workspace, need}};
+    if ((st = check_apart("dart_sma_paged", results, in)) != DART_OK) return st;
     a.B = d->batch; a.T = d->seqlen; a.H = d->nheads; a.P = d->headdim; a.N = d->dstate; a.G = d->ngroups;
     a.Q = Q; a.E = E; a.Cm = Cm; a.cu = cu_tokens; a.mem_count = mem_count; a.g = g; a.y_ssd = y_ssd; a.out = out;
     a.part = static_cast<float*>(workspace); a.status = status_word();

@@ -189,3 +189,45 @@ def test_a_layer_call_that_is_refused_changes_nothing():
     dart.layer_extend(**ok)
     dart.dart_sync_status()
     assert not torch.equal(before[0], s)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "mxfp4"])
+def test_neighbours_in_one_buffer_are_apart(cache):
+    """Every tensor of both calls is a slice of one buffer, one right behind the other."""
+    rng = np.random.default_rng(6)
+    H, N, P, S, R, lens, mems = 2, 128, 64, 4, 2, [3, 2], [1, 2]
+    memories = memories_of(rng, mems, H, N, P, cache, scale=0.5)
+    pool = Pool(memories, H, N, P, R, cache, rng, room=2)
+    (x, dt, A, Bm, Cm), args64 = extend_inputs(rng, lens, H, 1, N, P, "bf16")
+    (Q, E, _), (Q64, E64, _) = attention_inputs(rng, 5, H, 1, N, P, "bf16")
+    s, c, s64, c64 = states(rng, 2, H, N, P)
+    empty = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device="cuda")
+    i32 = torch.int32
+    parts = dict(x=x, y=empty(5, H, P), dt=dt, mem_count=empty(5, dtype=i32), Bm=Bm, nchunks_out=empty(2, dtype=i32), Cm=Cm,
+                 pos_out=empty(2, dtype=i32), cu_tokens=cumulative(lens), state=s, state_out=empty(*s.shape), dH_cur=c,
+                 dH_cur_out=empty(*c.shape), pages=pool.pages, table=pool.table, nchunks=ints(*mems), pos=ints(1, 3), A=A, Q=Q,
+                 out=empty(5, H, P), E=E, workspace=empty(dart.load().dart_sma_paged_workspace_bytes(dart._pack_dims(2, 5, H, P, N, 1, 1)) // 4))
+    if pool.scales is not None:
+        parts["scales"] = pool.scales
+    size = lambda v: -(-v.numel() * v.element_size() // 16) * 16
+    whole = torch.zeros(sum(size(v) for v in parts.values()), dtype=torch.uint8, device="cuda")
+    at = 0
+    for k, v in parts.items():
+        there = whole[at:at + v.numel() * v.element_size()].view(v.dtype).view(v.shape)
+        there.copy_(v)
+        at += size(v)
+        parts[k] = there
+    pool.pages, pool.scales = parts["pages"], parts.get("scales")
+    ext = ("x", "dt", "A", "Bm", "Cm", "cu_tokens", "state", "dH_cur", "pages", "table", "nchunks", "pos")
+    outs = ("state_out", "dH_cur_out", "nchunks_out", "pos_out", "y", "mem_count")
+    got = dart.dart_ssd_extend(*(parts[k] for k in ext), S, scales=pool.scales, **{k: parts[k] for k in outs})
+    dart.dart_sma_paged(parts["Q"], parts["E"], parts["Cm"], parts["cu_tokens"], pool.pages, parts["table"], parts["mem_count"], 0.5,
+                        parts["y"], scales=pool.scales, out=parts["out"], workspace=parts["workspace"])
+    dart.dart_sync_status()
+    yr, sr, cr, nr, pr, counts, _ = ref.extend(*args64, lens, s64, c64, mems, [1, 3], S)
+    held = [np.stack([pool.memory(b, m) for m in range(nr[b])]) for b in range(2)]
+    o = ref.sma(Q64, E64, args64[4], lens, held, counts)
+    assert rel_err(parts["out"], yr + 0.5 * o) <= TOL
+    assert rel_err(parts["state_out"], sr) <= TOL and rel_err(parts["dH_cur_out"], cr) <= TOL
+    assert got["nchunks"].tolist() == nr and got["pos"].tolist() == pr and got["mem_count"].tolist() == counts
+    assert torch.equal(parts["state"], s) and torch.equal(parts["dH_cur"], c) and torch.equal(parts["x"], x)

@@ -132,6 +132,74 @@ def test_results_do_not_go_onto_the_tokens(lib):
             assert b"y overlaps" in lib.dart_last_error()
 
 
+EXTEND = ("x", "dt", "A", "Bm", "Cm", "cu_tokens", "state", "state_out", "dH_cur", "dH_cur_out", "n_chunks", "pos", "n_chunks_out",
+          "pos_out", "y", "mem_count")
+SMA = ("Q", "E", "Cm", "cu_tokens", "mem_count", "y_ssd", "out", "workspace")
+CACHE = ("pages", "scales", "table")
+
+
+def spaced(names):
+    return {k: (i + 1) << 34 for i, k in enumerate(names)}          # apart by more than any of them holds
+
+
+def bytes_of(four_bit):
+    """Of every tensor of the calls below: batch 2, 6 tokens, 4 heads, one group, N = 128, P = 64, bfloat16."""
+    values = 8 * 4 * 4 * 128 * 64
+    ints = dict(cu_tokens=12, n_chunks=8, pos=8, n_chunks_out=8, pos_out=8, mem_count=24, first=8, count=8, table=24)
+    return dict(x=3072, dt=96, A=16, Bm=1536, Cm=1536, y=6144, Q=6144, E=3072, y_ssd=6144, out=6144, dH=2 * 4 * 3 * 128 * 64 * 2,
+                pages=values // 2 if four_bit else 2 * values, scales=values // 32 if four_bit else 0,
+                **dict.fromkeys(("state", "state_out", "dH_cur", "dH_cur_out"), 2 * 4 * 128 * 64 * 4), **ints)
+
+
+def run_at(lib, call, at, four_bit):
+    d = ctypes.byref(dims())
+    c = ctypes.byref(cache(format=int(four_bit), pages=at["pages"], scales=at["scales"] if four_bit else None, table=at["table"]))
+    p = lambda names: [ctypes.c_void_p(at[k]) for k in names]
+    if call == "extend":
+        return lib.dart_ssd_extend(d, 1, *p(EXTEND[:10]), c, *p(EXTEND[10:]), None)
+    if call == "sma":
+        need = lib.dart_sma_paged_workspace_bytes(d)
+        return lib.dart_sma_paged(d, 1, *p(SMA[:4]), c, *p(("mem_count",)), 0.5, *p(SMA[5:]), need, None)
+    if call == "write":
+        return lib.dart_cache_write_paged(d, 1, *p(("dH",)), 3, *p(("first", "count")), c, None)
+    return lib.dart_cache_read_paged(d, 1, c, *p(("first", "count", "dH")), 3, None)
+
+
+RESULTS = {"extend": ("y", "mem_count", "n_chunks_out", "pos_out", "state_out", "dH_cur_out", "pages", "scales"),
+           "sma": ("out", "workspace"), "write": ("pages", "scales"), "read": ("dH",)}
+
+
+@pytest.mark.parametrize("four_bit", [False, True])
+@pytest.mark.parametrize("call", RESULTS)
+def test_results_have_memory_of_their_own(lib, call, four_bit):
+    """Every result against every input and every other result: begun inside it, and ending inside it."""
+    names = {"extend": EXTEND + CACHE, "sma": SMA + CACHE, "write": ("dH", "first", "count") + CACHE,
+             "read": ("dH", "first", "count", "table")}[call]
+    size = dict(bytes_of(four_bit), workspace=lib.dart_sma_paged_workspace_bytes(ctypes.byref(dims())))
+    if not four_bit:
+        names = tuple(k for k in names if k != "scales")
+    for result in RESULTS[call]:
+        for other in names:
+            # the memories that are moved may lie in the pool as well; scales come with 4-bit pages only
+            if result == other or result not in names or (call == "write" and other == "dH"):
+                continue
+            for at in ((size[other] - 1) // 16 * 16, 16 - -(-size[result] // 16) * 16):
+                where = spaced(names + CACHE)
+                where[result] = where[other] + at
+                assert run_at(lib, call, where, four_bit) == dart.DART_ERR_INVALID_ARG, (result, other, at)
+                said = lib.dart_last_error().decode()
+                assert f"{result} overlaps {other}" in said or f"{other} overlaps {result}" in said
+            if (result, other) not in (("state_out", "state"), ("dH_cur_out", "dH_cur"), ("out", "y_ssd")):
+                where = spaced(names + CACHE)
+                where[result] = where[other]
+                assert run_at(lib, call, where, four_bit) == dart.DART_ERR_INVALID_ARG, (result, other)
+    # the one's input in place of the other's is no update in place
+    if call == "extend":
+        where = spaced(names + CACHE)
+        where["state_out"] = where["dH_cur"] = where["state"]
+        assert run_at(lib, call, where, four_bit) == dart.DART_ERR_INVALID_ARG
+
+
 def test_binding_refuses_what_does_not_fit():
     """Checks that need no GPU: they come before the first CUDA call."""
     z = torch.zeros
