@@ -402,8 +402,11 @@ dart_status dart_decode_step_noalloc(const dart_dims* dims, dart_dtype dtype,
  *
  * Tokens.  dims->batch sequences own rows cu_tokens[b] .. cu_tokens[b+1]-1 of
  * the packed token tensors (x[T,H,P] and so on), dims->seqlen = T rows in all;
- * cu_tokens is int32 [batch+1] on the device.  Sequences may own no row, and
- * rows that none owns are left as they are.
+ * cu_tokens is int32 [batch+1] on the device, within 0..T and never falling.
+ * Sequences may own no row, and rows that none owns are left as they are.  A
+ * sequence with an entry out of bounds, with its two entries in the wrong order,
+ * or that begins before an earlier entry (of those in bounds) owns none and is
+ * left, with an error as below.
  *
  * int32 vectors (the table and cu_tokens, first, count, mem_count, n_chunks and
  * pos) need 4-byte alignment only, so that a sequence's row of a table can be
@@ -467,8 +470,8 @@ dart_status dart_cache_read_paged(const dart_dims* dims, dart_dtype dtype, const
  *   n_chunks, pos: int32 [B], memories finished and tokens into the chunk, before
  *   the run; n_chunks_out, pos_out: after it.
  *   y: float [T,H,P].  mem_count: int32 [T], the number of memories each token
- *   may attend to (those finished before it), -1 for the tokens of a sequence
- *   that was left as it is; dart_sma_paged's argument of that name.
+ *   may attend to (those finished before it), -1 for the rows of a sequence that
+ *   was left as it is; dart_sma_paged's argument of that name.
  * A token sees a finished chunk only through its memory, so the pages must have
  * room for n_chunks + (pos + tokens) / S memories.  One kernel.
  */

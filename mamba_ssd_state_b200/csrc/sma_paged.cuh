@@ -68,7 +68,8 @@ struct TileList {
 // The count a row may really see: 0 for rows that are not to be computed.
 __device__ __forceinline__ int usable_count(int c, long long limit) { return c < 0 || c > limit ? 0 : c; }
 
-// Sum over the block of one value per thread, exclusive; total to all.  scan: 32 ints.
+// Sum over the block of one value per thread, exclusive; total to all.  scan: 32 ints
+// that are not read any more; all threads have passed a barrier since.
 __device__ __forceinline__ int block_scan(int v, int* scan, int& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (int)blockDim.x >> 5;
     int s = v;
@@ -77,7 +78,6 @@ __device__ __forceinline__ int block_scan(int v, int* scan, int& total) {
         const int u = __shfl_up_sync(0xffffffffu, s, o);
         if (lane >= o) s += u;
     }
-    __syncthreads();   // scan may still be read from the last call
     if (lane == 31) scan[warp] = s;
     __syncthreads();
     int before = 0;
@@ -89,9 +89,9 @@ __device__ __forceinline__ int block_scan(int v, int* scan, int& total) {
     return before + s - v;
 }
 
-// Builds the list; all threads of the block.  Ranges that are no ranges, counts
-// beyond the table and lists longer than CAP (only overlapping ranges make one)
-// are flagged, and what they name is left out.
+// Builds the list; all threads of the block.  Ranges that are no ranges or that an
+// earlier sequence's may meet and counts beyond the table are flagged, and what they
+// name is left out.  (CAP tiles hold every batch the host lets through.)
 template <int TT, int CAP, typename COST>
 __device__ __forceinline__ void build_tiles(const SmaPagedArgs& a, TileList<CAP, COST>& L) {
     const int threads = blockDim.x, tid = threadIdx.x;
@@ -104,6 +104,11 @@ __device__ __forceinline__ void build_tiles(const SmaPagedArgs& a, TileList<CAP,
         if (b < a.B) {
             if (token_range(a.cu, b, a.T, t0, t1)) tiles = (t1 - t0 + TT - 1) / TT;
             else bad = true;
+        }
+        // ranges can only meet where one before them is out of order
+        if (__syncthreads_or(bad) && tiles > 0 && rows_taken(a.cu, b, a.T, t0, 0, 1)) {
+            bad = true;
+            tiles = 0;
         }
         int total;
         const int at = n + block_scan(tiles, L.scan, total);
@@ -133,6 +138,7 @@ __device__ __forceinline__ void build_tiles(const SmaPagedArgs& a, TileList<CAP,
     int sum = 0;
     for (int k0 = 0; k0 < n; k0 += threads) {
         const int k = k0 + tid;
+        if (k0 > 0) __syncthreads();       // the last scan has been read
         int total;
         const int at = sum + block_scan(k < n ? L.pre[k] : 0, L.scan, total);
         if (k < n) L.pre[k] = at;

@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kTile = 8;   // tokens staged in shared memory at a time
 
-template <typename T, int N, int P, int PS, int RPT>
+template <typename T, int N, int P, int PS, int RPT, bool kMany>
 __global__ void __launch_bounds__(PS / 4 * N / RPT, 512 / (PS / 4 * N / RPT)) ssd_extend_kernel(ExtendArgs a) {
     constexpr int CT = PS / 4, kThreads = CT * (N / RPT);   // threads across the columns, of the block
     constexpr int WARPS = kThreads / 32;
@@ -37,6 +37,7 @@ __global__ void __launch_bounds__(PS / 4 * N / RPT, 512 / (PS / 4 * N / RPT)) ss
     __shared__ float dts[kTile], as[kTile];
     __shared__ __align__(16) float ys[kTile][WARPS][PS], ds[N * PS];
     sm100::griddep_wait();
+    const EarlierEntries<kMany> earlier(a, b);
     const size_t bh = (size_t)b * a.H + h, at = (bh * N + n0) * P + p0 + col;
     float H[RPT][4], D[RPT][4];
 #pragma unroll
@@ -45,7 +46,7 @@ __global__ void __launch_bounds__(PS / 4 * N / RPT, 512 / (PS / 4 * N / RPT)) ss
         H[r][0] = u.x; H[r][1] = u.y; H[r][2] = u.z; H[r][3] = u.w;
         D[r][0] = v.x; D[r][1] = v.y; D[r][2] = v.z; D[r][3] = v.w;
     }
-    const ExtendPlan plan = plan_extend(a, b, p0 == 0 && h == 0);
+    const ExtendPlan plan = plan_extend(a, b, p0 == 0 && h == 0, earlier);
     if (plan.len == 0 && a.state_out == a.state && a.cur_out == a.cur) return;   // the sequence stays as it is
     const float Ah = a.A[h];
     const int grp = group_of(h, a.H, a.G), t1 = plan.t0 + plan.len;
@@ -116,12 +117,18 @@ __global__ void __launch_bounds__(PS / 4 * N / RPT, 512 / (PS / 4 * N / RPT)) ss
     }
 }
 
-template <int N, int P, int PS, int RPT>
-cudaError_t run(const ExtendArgs& a, dart_dtype dt, cudaStream_t st) {
-    auto kern = dt == DART_F32 ? ssd_extend_kernel<float, N, P, PS, RPT> : ssd_extend_kernel<__nv_bfloat16, N, P, PS, RPT>;
-    const cudaError_t e = launch_dependent(kern, dim3(P / PS, a.H, a.B), dim3(PS / 4 * N / RPT), 0, st, 1, a);
+template <typename T, int N, int P, int PS, int RPT>
+cudaError_t run(const ExtendArgs& a, cudaStream_t st) {
+    constexpr int threads = PS / 4 * N / RPT;
+    const bool many = a.B > EarlierEntries<true>::kEach * threads;
+    auto kern = many ? ssd_extend_kernel<T, N, P, PS, RPT, true> : ssd_extend_kernel<T, N, P, PS, RPT, false>;
+    const cudaError_t e = launch_dependent(kern, dim3(P / PS, a.H, a.B), dim3(threads), 0, st, 1, a);
     if (e == cudaSuccess) count_launches(1);
     return e;
+}
+template <int N, int P, int PS, int RPT>
+cudaError_t run(const ExtendArgs& a, dart_dtype dt, cudaStream_t st) {
+    return dt == DART_F32 ? run<float, N, P, PS, RPT>(a, st) : run<__nv_bfloat16, N, P, PS, RPT>(a, st);
 }
 
 }  // namespace

@@ -80,7 +80,7 @@ struct Smem {
     float hi[2][kTB], lo[2][kTB], grow[2][kTB], w[2][kTB], total[2];
 };
 
-template <int N, int PS>
+template <int N, int PS, bool kMany>
 __global__ void __launch_bounds__(kThreads, 1) ssd_extend_mma_kernel(ExtendArgs a) {
     using T = __nv_bfloat16;
     using S = Smem<N, PS>;
@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_extend_mma_kernel(ExtendArgs 
     const int p0 = blockIdx.x * PS, h = blockIdx.y, b = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
     sm100::griddep_wait();
+    const EarlierEntries<kMany> earlier(a, b);
     const int wp = warp % S::kPW, wn = warp / S::kPW;        // this warp's 16 columns and NW rows of the state
     const size_t bh = (size_t)b * a.H + h;
     // element (p, n) of H^T: columns p0 + 16 wp + g (+ 8), rows NW wn + 8 j + 2 q (+ 1)
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_extend_mma_kernel(ExtendArgs 
             H[j][r] = a.state[e];
             D[j][r] = a.cur[e];
         }
-    const ExtendPlan plan = plan_extend(a, b, p0 == 0 && h == 0);
+    const ExtendPlan plan = plan_extend(a, b, p0 == 0 && h == 0, earlier);
     auto store = [&]() {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -374,9 +375,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_extend_mma_kernel(ExtendArgs 
     store();
 }
 
-template <int N, int PS>
+template <int N, int PS, bool kMany>
 cudaError_t run(const ExtendArgs& a, cudaStream_t st) {
-    auto kern = ssd_extend_mma_kernel<N, PS>;
+    auto kern = ssd_extend_mma_kernel<N, PS, kMany>;
     const int smem = (int)sizeof(Smem<N, PS>);
     static_assert(sizeof(Smem<N, PS>) <= 232448, "shared memory");
     static std::atomic<unsigned long long> ready{0};   // devices whose kernel has its shared memory allowed
@@ -400,8 +401,9 @@ bool ssd_extend_mma_applicable(const ExtendArgs& a, dart_dtype dt) {
 cudaError_t launch_ssd_extend_mma(const ExtendArgs& a, cudaStream_t st) {
     // half the columns a block where whole ones would leave half of the machine idle
     const bool half = 2ll * a.B * a.H <= paged_sm_count();
-    if (a.N == 128) return half ? run<128, 32>(a, st) : run<128, 64>(a, st);
-    return half ? run<64, 32>(a, st) : run<64, 64>(a, st);
+    if (a.B > EarlierEntries<true>::kEach * kThreads) return a.N == 128 ? run<128, 64, true>(a, st) : run<64, 64, true>(a, st);
+    if (a.N == 128) return half ? run<128, 32, false>(a, st) : run<128, 64, false>(a, st);
+    return half ? run<64, 32, false>(a, st) : run<64, 64, false>(a, st);
 }
 
 }  // namespace dart

@@ -231,3 +231,75 @@ def test_neighbours_in_one_buffer_are_apart(cache):
     assert rel_err(parts["state_out"], sr) <= TOL and rel_err(parts["dH_cur_out"], cr) <= TOL
     assert got["nchunks"].tolist() == nr and got["pos"].tolist() == pr and got["mem_count"].tolist() == counts
     assert torch.equal(parts["state"], s) and torch.equal(parts["dH_cur"], c) and torch.equal(parts["x"], x)
+
+
+# ------------------------------------------------- token ranges that are none
+def owned(cu, T):
+    """The sequences that own their rows, by the rule of the header."""
+    good = []
+    for b in range(len(cu) - 1):
+        before = [v for v in cu[:b] if 0 <= v <= T]
+        good.append(0 <= cu[b] <= cu[b + 1] <= T and all(v <= cu[b] for v in before))
+    return good
+
+
+FALLING = [n if n != 650 else 600 for n in range(701)]      # sequence 650 would begin among the rows of 600 to 648
+RANGES = [([0, 5, 3, 8], 9), ([-2, 3, 6], 8), ([0, 4, 99], 8), ([0, 99, 3, 8], 9), ([6, 8, 0, 4], 9), ([0, 40, 30, 70, 20, 90], 95),
+          ([0, 300, 200, 500], 520), ([2, 2, 1, 1, 5], 6), (FALLING, 700)]
+
+
+def test_the_ranges_of_these_tests():
+    assert owned([0, 5, 3, 8], 9) == [True, False, False] and owned([0, 99, 3, 8], 9) == [False, False, True]
+    assert owned([-2, 3, 6], 8) == [False, True] and owned([0, 4, 99], 8) == [True, False]
+    assert [b for b, v in enumerate(owned(FALLING, 700)) if not v] == [649, 650]
+
+
+@pytest.mark.parametrize("N, P, dtype, cache, H, G", SHAPES)
+@pytest.mark.parametrize("cu, T", RANGES)
+def test_attention_leaves_sequences_that_own_no_rows(N, P, dtype, cache, H, G, cu, T):
+    rng = np.random.default_rng(T)
+    B, good = len(cu) - 1, owned(cu, T)
+    one = memories_of(rng, [4], H, N, P, cache, scale=0.5)[0]
+    pool = Pool([one], H, N, P, 2, cache, rng)
+    pool.table = pool.table.expand(B, 2).contiguous()
+    args, args64 = attention_inputs(rng, T, H, G, N, P, dtype)
+    counts = rng.integers(0, 5, T)
+    rows = np.concatenate([np.arange(cu[b], cu[b + 1]) for b in range(B) if good[b]] + [np.arange(0)])
+    y, y64 = cast(rng.standard_normal((T, H, P)), "f32")
+    want = np.full((T, H, P), 5.0)
+    want[rows] = y64[rows] + 0.5 * ref.sma(*[v[rows] for v in args64], [1] * len(rows), [one] * len(rows), counts[rows].tolist())
+    out = torch.full_like(y, 5.0)
+    out[rows] = y[rows]                                  # in place over y_ssd: nothing may be added twice
+    dart.dart_sma_paged(*args, ints(*cu), pool.pages, pool.table, ints(*counts.tolist()), 0.5, out, scales=pool.scales, out=out)
+    with pytest.raises(dart.DartError):
+        dart.dart_sync_status()
+    assert rel_err(out, want) <= TOL
+
+
+MANY = [24 * n if n != 1050 else 24 * 1030 for n in range(1101)]
+
+
+@pytest.mark.parametrize("N, P, dtype, H, cu, T", [(N, P, dtype, 2, cu, T) for N, P, dtype in [(128, 64, "bf16"), (64, 64, "f32"), (16, 16, "f32")]
+                                                   for cu, T in RANGES] + [(64, 64, "bf16", 1, MANY, MANY[-1]), (16, 16, "f32", 1, MANY, MANY[-1])])
+def test_recurrence_leaves_sequences_that_own_no_rows(N, P, dtype, H, cu, T):
+    rng = np.random.default_rng(T)
+    S, B, good = 64, len(cu) - 1, owned(cu, T)
+    pool = Pool([[]] * B, H, N, P, 2, dtype, rng, room=5)
+    args, args64 = extend_inputs(rng, [T], H, 1, N, P, dtype)
+    s, c, s64, c64 = states(rng, B, H, N, P)
+    y = torch.full((T, H, P), 9.0, device="cuda")
+    seen = torch.full((T,), 99, dtype=torch.int32, device="cuda")
+    got = dart.dart_ssd_extend(*args, ints(*cu), s.clone(), c.clone(), pool.pages, pool.table, ints(*[0] * B), ints(*[60] * B), S, y=y,
+                               mem_count=seen)
+    with pytest.raises(dart.DartError):
+        dart.dart_sync_status()
+    lens = [cu[b + 1] - cu[b] if good[b] else 0 for b in range(B)]
+    rows = np.concatenate([np.arange(cu[b], cu[b + 1]) for b in range(B) if good[b]] + [np.arange(0)])
+    yr, sr, cr, nr, pr, counts, _ = ref.extend(*[v[rows] if v.ndim > 1 else v for v in args64], lens, s64, c64, [0] * B, [60] * B, S)
+    want, marks = np.full((T, H, P), 9.0), np.full(T, 99)
+    want[rows], marks[rows] = yr, counts
+    assert rel_err(y, want) <= TOL
+    # rows of a sequence that has them in order and to itself, but begins before an earlier entry, stay as they are too
+    assert (seen.cpu().numpy() == marks).all()
+    assert rel_err(got["state"], sr) <= TOL and rel_err(got["dH_cur"], cr) <= TOL
+    assert got["nchunks"].tolist() == nr and got["pos"].tolist() == pr
