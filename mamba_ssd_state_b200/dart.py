@@ -740,8 +740,15 @@ _SMA_PAGED_WORKSPACE = {}   # bytes by headdim
 _SMA_PAGED_TILES = 4096      # the most that batch + T / 4 may be
 
 
-def _sma_paged_args(Q, E, Cm, cu_tokens, pages, table, mem_count, g, y_ssd, scales, out, workspace):
-    """dart_sma_paged's checks: the device, the C call's arguments, out, and what has to live until the call."""
+def dart_sma_paged(Q, E, Cm, cu_tokens, pages, table, mem_count, g: float, y_ssd=None, *, scales=None, out=None,
+                   workspace=None, _first=None):
+    """State-memory attention of packed tokens over paged memories: float32
+    [T,H,P] equal to y_ssd + g*o (or o when y_ssd is None), token t of sequence b
+    seeing the sequence's first mem_count[t] memories (int32 [T], as
+    dart_ssd_extend returns it; -1 leaves the row as it is).  Q[T,H,N], E[T,H,P],
+    Cm[T,N] or [T,G,N] in one dtype.  out may be y_ssd itself.  workspace: a tensor of
+    dart_sma_paged_workspace_bytes bytes; calls that may overlap need one each.  Rows no sequence owns are not written."""
+    lib = load()
     dev = pages.get_device()
     f32, i32, dtype = torch.float32, torch.int32, Q.dtype
     T, H, N = Q.shape
@@ -753,40 +760,38 @@ def _sma_paged_args(Q, E, Cm, cu_tokens, pages, table, mem_count, g, y_ssd, scal
     if Cm.shape[-1] != N:
         raise ValueError(f"Cm: expected {N} columns, got {Cm.shape[-1]}")
     shape = (T, H, P)
-    yp = None if y_ssd is None else _need("y_ssd", y_ssd, shape, f32, dev)
     if E.shape != shape:
         raise ValueError(f"E: expected shape {shape}, got {tuple(E.shape)}")
-    if out is None:
-        out = torch.empty_like(E, dtype=f32)
-        op = out.data_ptr()
-    else:
-        op = _need("out", out, shape, f32, dev)
     dims = _pack_dims(B, T, H, P, N, 1, G)
     if workspace is None:
         n = _SMA_PAGED_WORKSPACE.get(P)
         if n is None:
-            n = _SMA_PAGED_WORKSPACE[P] = load().dart_sma_paged_workspace_bytes(dims)
+            n = _SMA_PAGED_WORKSPACE[P] = lib.dart_sma_paged_workspace_bytes(dims)
         workspace = table.new_empty(n // 4)
         wp = workspace.data_ptr()
     else:
         n = workspace.numel() * workspace.element_size()
         wp = _need("workspace", workspace, workspace.shape, workspace.dtype, dev)
-    args = (dims, _dtype_code(dtype), Q.data_ptr(), E.data_ptr(), Cm.data_ptr(), _need("cu_tokens", cu_tokens, (B + 1,), i32, dev),
-            cache, _need("mem_count", mem_count, (T,), i32, dev), float(g), yp, op, wp, n)
-    return dev, args, out, (Q, E, Cm, workspace)
-
-
-def dart_sma_paged(Q, E, Cm, cu_tokens, pages, table, mem_count, g: float, y_ssd=None, *, scales=None, out=None,
-                   workspace=None):
-    """State-memory attention of packed tokens over paged memories: float32
-    [T,H,P] equal to y_ssd + g*o (or o when y_ssd is None), token t of sequence b
-    seeing the sequence's first mem_count[t] memories (int32 [T], as
-    dart_ssd_extend returns it; -1 leaves the row as it is).  Q[T,H,N], E[T,H,P],
-    Cm[T,N] or [T,G,N] in one dtype.  out may be y_ssd itself.  workspace: a tensor of
-    dart_sma_paged_workspace_bytes bytes; calls that may overlap need one each.  Rows no sequence owns are not written."""
-    dev, args, out, _held = _sma_paged_args(Q, E, Cm, cu_tokens, pages, table, mem_count, g, y_ssd, scales, out, workspace)
-    _call(load().dart_sma_paged, dev, *args)
-    return out
+    qp, ep, cp, cup, g = Q.data_ptr(), E.data_ptr(), Cm.data_ptr(), _need("cu_tokens", cu_tokens, (B + 1,), i32, dev), float(g)
+    first = None
+    if _first is not None:      # layer_extend's other call, which gives y_ssd and mem_count, once nothing else can be refused
+        if T and (qp | ep | cp) & 15:
+            raise DartError(DART_ERR_INVALID_ARG, "Q, E and Cm must be 16-byte aligned")
+        if T and B + T // 4 > _SMA_PAGED_TILES:
+            raise DartError(DART_ERR_UNSUPPORTED, f"{B} sequences and {T} tokens are too many for one call "
+                                                  f"(batch + tokens / 4 must be <= {_SMA_PAGED_TILES})")
+        first = _first(shape)
+        y_ssd = out = first["y"]
+        mem_count = first["mem_count"]
+    yp = None if y_ssd is None else _need("y_ssd", y_ssd, shape, f32, dev)
+    if out is None:
+        out = torch.empty_like(E, dtype=f32)
+        op = out.data_ptr()
+    else:
+        op = _need("out", out, shape, f32, dev)
+    _call(lib.dart_sma_paged, dev, dims, _dtype_code(dtype), qp, ep, cp, cup, cache, _need("mem_count", mem_count, (T,), i32, dev), g,
+          yp, op, wp, n)
+    return out if first is None else first
 
 
 def layer_extend(x, dt, A, Bm, Cm, Q, E, g: float, cu_tokens, state, dH_cur, pages, table, nchunks, pos, chunk: int, *,
@@ -795,19 +800,13 @@ def layer_extend(x, dt, A, Bm, Cm, Q, E, g: float, cu_tokens, state, dH_cur, pag
     dart_sma_paged with the gated residual written in place over y.  Returns
     dart_ssd_extend's dict with y the layer output.  Arguments that either of the
     two refuses are refused before the first one runs."""
-    T, H, P = x.shape
-    y, mem_count = table.new_empty((T, H, P), dtype=torch.float32), table.new_empty(T)
-    dev, args, _, _held = _sma_paged_args(Q, E, Cm, cu_tokens, pages, table, mem_count, g, y, scales, y, None)
-    # what the C call refuses beyond these and beyond what dart_ssd_extend refuses too
-    if T and (args[2] | args[3]) & 15:
-        raise DartError(DART_ERR_INVALID_ARG, "Q and E must be 16-byte aligned")
-    if T and table.shape[0] + T // 4 > _SMA_PAGED_TILES:
-        raise DartError(DART_ERR_UNSUPPORTED, f"{table.shape[0]} sequences and {T} tokens are too many for one call "
-                                              f"(batch + tokens / 4 must be <= {_SMA_PAGED_TILES})")
-    res = dart_ssd_extend(x, dt, A, Bm, Cm, cu_tokens, state, dH_cur, pages, table, nchunks, pos, chunk,
-                          scales=scales, state_out=state_out, dH_cur_out=dH_cur_out, y=y, mem_count=mem_count)
-    _call(load().dart_sma_paged, dev, *args)
-    return res
+    def extend(shape):
+        if x.shape != shape:
+            raise ValueError(f"x: expected shape {shape}, got {tuple(x.shape)}")
+        return dart_ssd_extend(x, dt, A, Bm, Cm, cu_tokens, state, dH_cur, pages, table, nchunks, pos, chunk, scales=scales,
+                               state_out=state_out, dH_cur_out=dH_cur_out)
+
+    return dart_sma_paged(Q, E, Cm, cu_tokens, pages, table, None, g, scales=scales, _first=extend)
 
 
 def dart_decode_step_noalloc(x, dt, A, Bm, Cm, Q, E, g: float, state, dH_cur, cache, nchunks, pos,
