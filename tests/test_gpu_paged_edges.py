@@ -303,3 +303,24 @@ def test_recurrence_leaves_sequences_that_own_no_rows(N, P, dtype, H, cu, T):
     assert (seen.cpu().numpy() == marks).all()
     assert rel_err(got["state"], sr) <= TOL and rel_err(got["dH_cur"], cr) <= TOL
     assert got["nchunks"].tolist() == nr and got["pos"].tolist() == pr
+
+
+@pytest.mark.parametrize("N, P, dtype, cache, H, G", SHAPES)
+@pytest.mark.parametrize("lens", [[1, 1], [4], [8], [3, 40], [200]])
+@pytest.mark.parametrize("what", ["Q", "E", "C"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_a_row_that_is_not_finite_leaves_other_rows_alone(N, P, dtype, cache, H, G, lens, what, value):
+    """One value of one token, in one head of Q or E or in one group of C: every other row of the tile is as it was."""
+    rng = np.random.default_rng(sum(lens) + N)
+    memories = memories_of(rng, [9] * len(lens), H, N, P, cache, scale=0.5)
+    pool = Pool(memories, H, N, P, 4, cache, rng)
+    T = sum(lens)
+    (Q, E, C), args64 = attention_inputs(rng, T, H, G, N, P, dtype)
+    counts = [9 - (t % 3) for t in range(T)]
+    want = ref.sma(*args64, lens, memories, counts)
+    t, touched = T // 2, np.zeros((T, H), bool)
+    {"Q": Q, "E": E, "C": C}[what][t, -1, 5] = value
+    touched[t, H - 1 if what != "C" else slice(H - H // G, H)] = True
+    out = dart.dart_sma_paged(Q, E, C, cumulative(lens), pool.pages, pool.table, ints(*counts), 1.0, scales=pool.scales)
+    dart.dart_sync_status()
+    assert rel_err(out[torch.from_numpy(~touched).cuda()], want[~touched]) <= TOL
