@@ -495,6 +495,9 @@ size_t dart_sma_paged_workspace_bytes(const dart_dims* dims);
  *   mem_count: int32 [T]; -1 marks a row that is left as it is.
  *   workspace: dart_sma_paged_workspace_bytes(), 16-byte aligned, contents on
  *   entry do not matter; calls that may overlap on the GPU need one each.
+ * Over DART_CACHE_MXFP4 pages a row of Q or C is multiplied as float16 (float32:
+ * as two halves) scaled by a power of two, which holds each value to 2^-39 of the
+ * row's largest (float32: or 2^-23 of itself, if that is more).
  * Limits: batch + T / 4 <= 4096.  Deterministic.  Two kernels.
  */
 dart_status dart_sma_paged(const dart_dims* dims, dart_dtype dtype, const void* Q, const void* E,

@@ -15,7 +15,7 @@
 // four columns a lane halve the loads of Q and C (32 runs of up to 6 tokens over
 // 131 memories, 32 heads: 888 us with two columns and single multiply-adds, 664 so,
 // 590 with the cheaper wait of sma_paged.cuh, 540 with the softmax as below, 485 at
-// HBM's rate; 64 single tokens 892 us, HBM).  A token's scores are summed into the
+// a copy's rate; 64 single tokens 892 us, HBM).  A token's scores are summed into the
 // lanes that own it, which alone run its softmax (online, base 2) and pass its two
 // weights on (against a warp sum and a softmax in every lane for each token, 19 runs
 // of up to 137 tokens over 48 memories of 16 x 16: 60 -> 42 us); v is folded into

@@ -22,8 +22,8 @@
 // finds the codes of its fragments in its own 16 bytes of a column.  The columns
 // of B are tokens: with up to 4 tokens one tile of 8 columns holds Q and C, else
 // one tile each.  float16 operands hold Q and C scaled by a power of two per
-// token, so that nothing is lost but what lies 2^-29 below a row's largest value;
-// float32 inputs are split into a high and a low float16 half (22 bits).
+// token, so that a value is off by at most 2^-39 of its row's largest; float32 inputs
+// are split into a high and a low float16 half (2^-23 of the value, or 2^-39 as above).
 // A block of 32 codes is two k steps: their product is multiplied by the block's
 // scale in float32 before it is added, so a scale costs 4 multiply-adds for
 // every 2 products and no bit.  That holds for scale bytes 1 .. 192 (values of up
@@ -47,7 +47,7 @@ constexpr int kP = 64;
 constexpr int kCap = 4096;                      // tiles of a call
 constexpr int kLeast = 4;                       // units below which a run is not cut
 
-// A memory takes 2.1 us of a warp with two tiles of columns and 1.65 with one
+// A memory takes 2.0 us of a warp with two tiles of columns and 1.6 with one
 // (4-bit; counted the same, the runs with more rows ended a fifth later).
 struct RowCost { static __device__ __forceinline__ int of(int rows) { return rows > 4 ? 5 : 4; } };
 using Tiles = TileList<kCap, RowCost>;

@@ -7,7 +7,8 @@
 // with the accumulators in TMEM (U in columns 0..255, V in 256..511).  Reading a
 // memory once for 128 tokens instead of 8 makes the run compute-bound:
 // 4 x 256 tokens over 100 memories took 470 us on warp-level products, where
-// every 8 tokens stream all memories through the SM again, and take 79 here.
+// every 8 tokens stream all memories through the SM again, and take 79 here (93 with
+// nothing in L2).
 //
 // What differs from prefill: memories come from pages, a tile ends with its
 // sequence (rows behind it belong to others and are not written), every row has
